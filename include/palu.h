@@ -61,8 +61,11 @@ enum {
   PALU_DEVERR_LENGTH_MISMATCH = 4u, /* key and value caches differ in length */
   PALU_DEVERR_NOT_CONVERGED = 8u,   /* eigen-solver hit its sweep limit */
   PALU_DEVERR_ROLLBACK = 16u,       /* a per-sequence rollback was refused (that sequence kept its length) */
-  PALU_DEVERR_BOUNDS = 32u          /* bounds-checking build only (PALU_DEBUG_BOUNDS): a kernel found a
+  PALU_DEVERR_BOUNDS = 32u,         /* bounds-checking build only (PALU_DEBUG_BOUNDS): a kernel found a
                                        computed block index out of range and skipped that access */
+  PALU_DEVERR_PAGE = 64u,           /* a page table names a page outside the pool (paged.h) */
+  PALU_DEVERR_SPAN = 128u,          /* a sequence's offsets or its number of new tokens make no sense (paged.h) */
+  PALU_DEVERR_POSITION = 256u       /* a position outside the rotation table (paged.h) */
 };
 
 /* Configuration, mirroring the page's KVCacheConfig fields (section "Usage"):

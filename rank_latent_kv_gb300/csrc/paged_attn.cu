@@ -1,0 +1,610 @@
+// Attention over the paged cache for few rows a KV head (single-token decode,
+// a few drafted tokens), the joining of partial results, and the host side.
+//
+// paged_few_kernel is bound by reading the cache: 512 bytes a token and KV
+// head feed 4 * 128 * rows flops, far below the card's ratio for up to 16
+// rows.  So everything serves the loads: one persistent CTA an SM, a loading
+// warp that keeps three 64 KB tiles (128 keys and values) in flight by TMA,
+// one copy a page and 64-channel panel, and eight warps that take 16 tokens
+// of each tile: scores as K q^T with the tokens as the m side and the rows as
+// the n side of m16n8k16, so no product is spent on padding 3 or 7 rows to
+// 16; a running maximum a warp, merged once a unit.
+#include <math.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "paged_attn.cuh"
+#include "splitk_attend.cuh"
+
+namespace palu {
+
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = 32 * (kFewWarps + 1);
+constexpr int kFewStages = 3;
+constexpr int kMergeStride = kHeadDim + 2;
+
+struct FewSmem {
+  uint64_t full[kFewStages], empty[kFewStages], join;
+  TileMeta meta[kFewStages];
+  PlanScratch plan;
+  int failed;  // a wait ran out: the remaining ones are not begun
+};
+// tiles (1024-byte aligned), the warps' merge area (8 rows at a time), the rest
+constexpr int kFewMergeBytes = kFewWarps * 8 * kMergeStride * 4;
+constexpr int kFewSmemBytes = 1024 + kFewStages * 2 * kTileBytes + kFewMergeBytes + (int)sizeof(FewSmem);
+static_assert(kFewSmemBytes <= 232448, "shared memory of paged_few_kernel");
+
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(0), "r"(head), "r"(page)
+      : "memory");
+}
+
+// Shared-memory address of 16-byte chunk ch (0..15) of a tile's row, in the
+// 128-byte swizzle the copies write.
+__device__ __forceinline__ uint32_t panel_addr(uint32_t tile, int row, int ch) {
+  return tile + (ch >> 3) * kPanelBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma_16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  if (BF16)
+    mma_bf16(d, a0, a1, a2, a3, b0, b1);
+  else
+    mma_f16(d, a0, a1, a2, a3, b0, b1);
+}
+
+// The limit of a row of the unit: how many of the sequence's tokens it sees.
+__device__ __forceinline__ int unit_row_limit(const AttnParams& p, const TileMeta& m, int r) {
+  const int tok = (m.row0 + r) / p.Gq;
+  if (!m.prefix) return m.base + tok + 1;
+  // token numbers of the whole call: the row's sequence
+  int lo = 0, hi = p.c.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.offsets + mid) <= tok)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  unsigned bad = 0;
+  const SeqSpan s = seq_span(p, lo, &bad);
+  const int i = tok - s.tok0;
+  return i >= 0 && i < s.n ? min(row_limit(s, i), p.S0) : 0;
+}
+
+// A wait that gives up sets the error word, and `failed` for the block: every
+// role then runs on to its end without waiting (what it computes is void).
+__device__ __forceinline__ void wait_or_fail(uint64_t* bar, uint32_t parity, int* failed, unsigned* error) {
+  if (*(volatile int*)failed) return;
+  if (!mbar_wait_bounded(bar, parity)) {
+    *(volatile int*)failed = 1;
+    atomicOr(error, PALU_DEVERR_TIMEOUT);
+  }
+}
+
+// NT: n8 tiles of rows (8 or 16 rows a unit).
+template <bool BF16, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    paged_few_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* merge = reinterpret_cast<float*>(smem + kFewStages * 2 * kTileBytes);
+  FewSmem& sh = *reinterpret_cast<FewSmem*>(smem + kFewStages * 2 * kTileBytes + kFewMergeBytes);
+  constexpr int R = 8 * NT;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dep_launch();
+  if (tid == 0) {
+    for (int i = 0; i < kFewStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kFewWarps);
+      sh.meta[i] = TileMeta{};
+    }
+    mbar_init(&sh.join, kFewWarps);
+    sh.failed = 0;
+    fence_mbar_init();
+  }
+  plan_start<R>(p, &sh.plan);
+  const int n_tiles = (int)min(sh.plan.w1 - sh.plan.w0, 0x7fffffffLL);
+  if (n_tiles > 0) {
+    if (warp == kFewWarps) {
+      // ---- the loading warp
+      unsigned bad = 0;
+      int it = 0;
+      plan_walk<R>(p, &sh.plan, [&](const TileMeta& m) -> bool {
+        const int st = it % kFewStages;
+        if (it >= kFewStages) wait_or_fail(&sh.empty[st], ((it / kFewStages) - 1) & 1, &sh.failed, p.c.error);
+        // all lanes stop together
+        if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) return false;
+        ++it;
+        const int pages = (m.valid + p.c.page - 1) >> p.c.page_shift;
+        if (lane == 0) {
+          sh.meta[st] = m;
+          mbar_arrive_expect_tx(&sh.full[st], pages * p.c.page * kHeadDim * 4);
+        }
+        __syncwarp();
+        uint32_t kt = smem_addr(smem + st * 2 * kTileBytes);
+        if (lane < pages) {
+          int page = __ldg(p.c.table + (long long)m.seq * p.c.width + (m.key0 >> p.c.page_shift) + lane);
+          if (page < 0 || page >= p.c.n_pages) {
+            bad |= PALU_DEVERR_PAGE;
+            page = 0;
+          }
+          kt += lane * p.c.page * 128;
+          tma_page(kt, &kmap, &sh.full[st], 0, m.kh, page);
+          tma_page(kt + kPanelBytes, &kmap, &sh.full[st], 64, m.kh, page);
+          tma_page(kt + kTileBytes, &vmap, &sh.full[st], 0, m.kh, page);
+          tma_page(kt + kTileBytes + kPanelBytes, &vmap, &sh.full[st], 64, m.kh, page);
+        }
+        return true;
+      });
+      if (bad) atomicOr(p.c.error, bad);
+      // no copy is in flight when the block ends, also where the others gave up
+      for (int k = max(it - kFewStages, 0); k < it; ++k)
+        if (!mbar_wait_bounded(&sh.full[k % kFewStages], (k / kFewStages) & 1)) break;
+    } else {
+      // ---- 16 tokens of each tile a warp
+      const int g = lane >> 2, c = lane & 3, mat = lane >> 3, rr = lane & 7, r0 = 16 * warp;
+      float m_run[NT][2], l_run[NT][2], acc[NT][8][4];
+      uint32_t qb[NT][8][2];
+      int lim[NT][2];
+      uint32_t joins = 0;
+      // the eight warps meet (bounded, unlike a named barrier)
+      auto join = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.join);
+        wait_or_fail(&sh.join, joins & 1, &sh.failed, p.c.error);
+        ++joins;
+        __syncwarp();
+      };
+      for (int it = 0; it < n_tiles; ++it) {
+        const int st = it % kFewStages;
+        wait_or_fail(&sh.full[st], (it / kFewStages) & 1, &sh.failed, p.c.error);
+        const TileMeta m = sh.meta[st];
+        if (m.first) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int rg = nt * 8 + g;
+            const int row = m.row0 + rg;
+            const uint16_t* qh = p.q + (long long)(m.tok0 + row / p.Gq) * p.qs0 +
+                                 (long long)(m.kh * p.Gq + row % p.Gq) * p.qs1;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              qb[nt][ks][0] = rg < m.rows ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
+              qb[nt][ks][1] = rg < m.rows ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 8 + 2 * c) : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = nt * 8 + 2 * c + e;
+              lim[nt][e] = r < m.rows ? unit_row_limit(p, m, r) : 0;
+              m_run[nt][e] = -INFINITY;
+              l_run[nt][e] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
+          }
+        }
+        const uint32_t kt = smem_addr(smem + st * 2 * kTileBytes), vt = kt + kTileBytes;
+        if (r0 < m.valid) {
+          if (m.valid < r0 + 16) {
+            // whatever lies behind the last key must not reach the products: 0 * NaN is NaN
+            const int z0 = m.valid - r0;
+            for (int i = lane; i < (16 - z0) * 16; i += 32) {
+              const uint32_t a = panel_addr(vt, r0 + z0 + (i >> 4), i & 15);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          float sc[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4(a0, a1, a2, a3, panel_addr(kt, r0 + rr + ((mat & 1) << 3), 2 * ks + (mat >> 1)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16<BF16>(sc[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
+          }
+          const int t = m.key0 + r0 + g;
+          uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float* s = sc[nt];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s[e] = t + 8 * (e >> 1) < lim[nt][e & 1] ? s[e] * p.scale_log2 : -INFINITY;
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float bm = fmaxf(s[e], s[e + 2]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
+              const float mn = fmaxf(m_run[nt][e], bm);
+              const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen so far: every weight is 0
+              const float al = ex2f_(m_run[nt][e] - ref);
+              m_run[nt][e] = mn;
+              pr[e] = ex2f_(s[e] - ref);
+              pr[e + 2] = ex2f_(s[e + 2] - ref);
+              l_run[nt][e] = l_run[nt][e] * al + (pr[e] + pr[e + 2]);
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) {
+                acc[nt][mt][e] *= al;
+                acc[nt][mt][e + 2] *= al;
+              }
+            }
+            // The weights enter as a rounded value and its remainder: two
+            // products instead of one cost nothing here, and the output is
+            // then as exact as its own rounding lets it be.
+            const uint32_t h0 = pack2<BF16>(pr[0], pr[1]), h1 = pack2<BF16>(pr[2], pr[3]);
+            const float2 f0 = unpack2<BF16>(h0), f1 = unpack2<BF16>(h1);
+            ph[nt][0] = movmatrix_t(h0);
+            ph[nt][1] = movmatrix_t(h1);
+            pl[nt][0] = movmatrix_t(pack2<BF16>(pr[0] - f0.x, pr[1] - f0.y));
+            pl[nt][1] = movmatrix_t(pack2<BF16>(pr[2] - f1.x, pr[3] - f1.y));
+          }
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4_t(a0, a1, a2, a3, panel_addr(vt, r0 + rr + ((mat >> 1) << 3), 2 * mt + (mat & 1)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16<BF16>(acc[nt][mt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+              mma_16<BF16>(acc[nt][mt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[st]);
+        if (m.last) {
+          // join the warps' states, 8 rows at a time, and write the unit's result
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            join();
+            float* mw = merge + warp * 8 * kMergeStride;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float l = l_run[nt][e];
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+              if (g == 0) {
+                mw[(2 * c + e) * kMergeStride + kHeadDim] = m_run[nt][e];
+                mw[(2 * c + e) * kMergeStride + kHeadDim + 1] = l;
+              }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                mw[(2 * c + (e & 1)) * kMergeStride + 16 * mt + g + 8 * (e >> 1)] = acc[nt][mt][e];
+            join();
+            // a warp a row, four channels a lane
+            const int r = nt * 8 + warp;
+            if (r < m.rows) {
+              const float* mr = merge + warp * kMergeStride;
+              float M = -INFINITY;
+#pragma unroll
+              for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, mr[w * 8 * kMergeStride + kHeadDim]);
+              const float ref = M == -INFINITY ? 0.f : M;
+              float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int w = 0; w < kFewWarps; ++w) {
+                const float* x = mr + w * 8 * kMergeStride;
+                const float f = ex2f_(x[kHeadDim] - ref);
+                L += x[kHeadDim + 1] * f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] += x[4 * lane + i] * f;
+              }
+              const int row = m.row0 + r;
+              const long long at = (long long)(m.tok0 + row / p.Gq) * p.Hq + m.kh * p.Gq + row % p.Gq;
+              if (m.dest == kToOut) {
+                const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
+                uint2 v = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
+                *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) = v;
+              } else {
+                const long long rec = m.dest == kToRow ? (m.prefix ? 0 : (long long)p.N * p.Hq) + at
+                                                       : (long long)m.dest * p.part.R + r;
+                float2* ml = (m.dest == kToRow ? p.row_ml : p.part.ml) + rec;
+                float* ac = (m.dest == kToRow ? p.row_acc : p.part.acc) + rec * kHeadDim;
+                if (lane == 0) *ml = make_float2(M, L);
+                *reinterpret_cast<float4*>(ac + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  // a launch before this one (the prefix on another kernel) has ended too when this one has
+  grid_dep_wait();
+}
+
+// Joins a row's parts: a warp a row, four channels a lane.  Rows whose unit
+// was complete in one CTA, with no prefix to join, are already in the output.
+struct CombineParams {
+  AttnParams a;
+  PartSet prefix, own;
+};
+constexpr int kCombineWarps = 4;
+
+template <bool BF16>
+__global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const CombineParams p) {
+  const AttnParams& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  if (row >= (long long)a.N * a.Hq) {
+    grid_dep_wait();
+    return;
+  }
+  const int tok = (int)(row / a.Hq), h = (int)(row - (long long)tok * a.Hq), kh = h / a.Gq, gi = h - kh * a.Gq;
+  // the row's place in the plan does not depend on the attention: only its parts do
+  if (tok >= __ldg(a.offsets + a.c.batch)) {
+    grid_dep_wait();
+    return;
+  }
+  const int b = find_sequence(a.offsets, a.c.batch, tok, lane & 15, (lane & 16) ? 0xffff0000u : 0x0000ffffu);
+  unsigned bad = 0;
+  const SeqSpan s = seq_span(a, b, &bad);
+  const int i = tok - s.tok0;
+  uint16_t* out = a.out + row * kHeadDim;
+  grid_dep_wait();
+  if (i < 0 || i >= s.n) {
+    *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0u, 0u);
+    return;
+  }
+  const int lim = row_limit(s, i);
+  // parts of one kind: CTAs first .. last of its launch hold them, or one record a row does
+  struct Parts {
+    int first, n, r;
+    bool whole;
+    long long W, u0;
+  };
+  auto parts_of = [&](const PartSet& ps, long long u0, int tiles, int r) {
+    Parts q;
+    q.W = __ldcg(ps.plan);
+    q.u0 = u0;
+    q.r = r;
+    q.first = (int)(u0 / q.W);
+    q.n = tiles ? (int)((u0 + tiles - 1) / q.W) - q.first + 1 : 0;
+    q.whole = q.n == 1;
+    return q;
+  };
+  Parts own = {}, pre = {};
+  {
+    const int R = p.own.R, lr = i * a.Gq + gi, rt = lr / R;
+    int tiles = 0;
+    long long u0 = __ldcg(p.own.plan + 1 + b);
+    for (int t = 0; t <= rt; ++t) {
+      const int last = min((t + 1) * R, s.n * a.Gq) - 1, keys = row_limit(s, last / a.Gq) - a.S0;
+      tiles = keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 0;
+      u0 += (long long)tiles * (t < rt ? a.c.kv_heads : kh);
+    }
+    own = parts_of(p.own, u0, tiles, lr - rt * R);
+    if (own.whole && a.S0 == 0) return;
+  }
+  if (a.S0 > 0) {
+    const int R = p.prefix.R, lr = tok * a.Gq + gi, rt = lr / R, rts = (a.N * a.Gq + R - 1) / R;
+    const long long t0 = prefix_tiles_of(a.S0);
+    pre = parts_of(p.prefix, ((long long)kh * rts + rt) * t0, (int)t0, lr - rt * R);
+  }
+  const int n = pre.n + own.n;
+  const float2* ml;
+  const float* ac;
+  auto part = [&](int k) {  // where part k lies
+    const bool is_pre = k < pre.n;
+    const PartSet& ps = is_pre ? p.prefix : p.own;
+    const Parts& q = is_pre ? pre : own;
+    const long long c = q.first + (is_pre ? k : k - pre.n);
+    const long long rec = q.whole ? (is_pre ? 0 : (long long)a.N * a.Hq) + row
+                                  : (2 * c + (c * q.W > q.u0 ? 0 : 1)) * ps.R + q.r;
+    ml = (q.whole ? a.row_ml : ps.ml) + rec;
+    ac = (q.whole ? a.row_acc : ps.acc) + rec * kHeadDim;
+  };
+  float M = -INFINITY;
+  if (lim > 0) {
+    for (int k = lane; k < n; k += 32) {
+      part(k);
+      M = fmaxf(M, __ldcg(&ml->x));
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  }
+  float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (lim > 0 && M != -INFINITY) {
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      part(k);
+      const float2 v = __ldcg(ml);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(ac) + lane);
+      const float f = ex2f_(v.x - M);
+      L += v.y * f;
+      o[0] += x.x * f;
+      o[1] += x.y * f;
+      o[2] += x.z * f;
+      o[3] += x.w * f;
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
+  *reinterpret_cast<uint2*>(out + 4 * lane) =
+      make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
+}
+
+// ------------------------------------------------------------------ host
+
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static TensorMapEncode tensor_map_encode() {
+  static TensorMapEncode fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<TensorMapEncode>(f);
+  }();
+  return fn;
+}
+
+// The pool as [page][head][token][channel]; a copy takes one page of one head, 64 channels.
+static palu_status page_map(CUtensorMap* map, const palu_paged_cache* c, const void* base, const int64_t* strides) {
+  TensorMapEncode encode = tensor_map_encode();
+  if (!encode) return fail(PALU_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)c->page_size, (cuuint64_t)c->kv_heads, (cuuint64_t)c->n_pages};
+  const cuuint64_t str[3] = {(cuuint64_t)strides[2] * 2, (cuuint64_t)strides[1] * 2, (cuuint64_t)strides[0] * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)c->page_size, 1, 1}, one[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, c->dtype == PALU_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                            4, const_cast<void*>(base), dims, str, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PALU_ERR_CUDA, "cuTensorMapEncodeTiled refused the pages' strides (" + std::to_string(r) + ")");
+  return PALU_OK;
+}
+
+// Sizes that the host can know: which kernel takes the shared and which the
+// own keys, and the workspace's parts.
+struct AttnLayout {
+  bool shared;       // the prefix is a part of its own
+  int R_prefix, R_own;
+  size_t plan_p, ml_p, acc_p, plan_o, ml_o, acc_o, row_ml, row_acc, total;
+};
+
+static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_t q_heads, int32_t max_new,
+                               int32_t shared_pages, AttnLayout* l) {
+  palu_status st = paged_check(c);
+  if (st != PALU_OK) return st;
+  if (tokens < 1 || q_heads < 1 || max_new < 1) return fail(PALU_ERR_INVALID_ARG, "tokens, q_heads and max_new must be positive");
+  if (q_heads % c->kv_heads) return fail(PALU_ERR_INVALID_ARG, "q_heads must be a multiple of the cache's kv_heads");
+  const int Gq = q_heads / c->kv_heads;
+  if (Gq > kMaxPagedGq) return fail(PALU_ERR_UNSUPPORTED, "at most 64 query heads per KV head");
+  if (tokens > (1LL << 31) / q_heads - 256) return fail(PALU_ERR_UNSUPPORTED, "too many tokens for one call");
+  if (shared_pages < 0 || shared_pages > c->table_width)
+    return fail(PALU_ERR_INVALID_ARG, "shared_pages must be in [0, table_width]");
+  const int64_t own_rows = std::min<int64_t>(max_new, tokens) * Gq, all_rows = tokens * Gq;
+  l->shared = shared_pages > 0 && c->batch > 1;
+  l->R_own = own_rows <= 8 ? 8 : 16;
+  l->R_prefix = all_rows <= 8 ? 8 : 16;
+  const size_t slots = 2 * (size_t)device_sm_count();
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  l->plan_p = take(sizeof(long long) * (1 + (size_t)c->batch));
+  l->ml_p = l->shared ? take(slots * l->R_prefix * sizeof(float2)) : 0;
+  l->acc_p = l->shared ? take(slots * l->R_prefix * kHeadDim * sizeof(float)) : 0;
+  l->plan_o = take(sizeof(long long) * (1 + (size_t)c->batch));
+  l->ml_o = take(slots * l->R_own * sizeof(float2));
+  l->acc_o = take(slots * l->R_own * kHeadDim * sizeof(float));
+  l->row_ml = l->shared ? take(2 * (size_t)tokens * q_heads * sizeof(float2)) : 0;
+  l->row_acc = l->shared ? take(2 * (size_t)tokens * q_heads * kHeadDim * sizeof(float)) : 0;
+  l->total = o;
+  return PALU_OK;
+}
+
+template <class K, class... Args>
+static palu_status launch(K kernel, int grid, int threads, int smem, bool dependent, cudaStream_t stream, const char* what,
+                          Args... args) {
+  int per_sm = 0;
+  palu_status st = kernel_occupancy(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
+  if (st != PALU_OK) return st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), what);
+}
+
+template <bool BF16>
+static palu_status launch_few(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool dependent,
+                              cudaStream_t s) {
+  return p.part.R == 8 ? launch(paged_few_kernel<BF16, 1>, p.part.grid, kFewThreads, kFewSmemBytes, dependent, s,
+                                "paged_few_kernel launch", p, km, vm)
+                       : launch(paged_few_kernel<BF16, 2>, p.part.grid, kFewThreads, kFewSmemBytes, dependent, s,
+                                "paged_few_kernel launch", p, km, vm);
+}
+
+}  // namespace palu
+
+using namespace palu;
+
+extern "C" palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_t tokens, int32_t q_heads,
+                                                      int32_t max_new, int32_t shared_pages, size_t* bytes) {
+  AttnLayout l;
+  palu_status st = attn_layout(cache, tokens, q_heads, max_new, shared_pages, &l);
+  if (st != PALU_OK) return st;
+  if (!bytes) return fail(PALU_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = l.total;
+  return PALU_OK;
+}
+
+extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t tokens, const int32_t* offsets,
+                                       int32_t max_new, int32_t q_heads, const void* q, const int64_t q_strides[2],
+                                       int32_t shared_pages, float softmax_scale, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  AttnLayout l;
+  palu_status st = attn_layout(cache, tokens, q_heads, max_new, shared_pages, &l);
+  if (st != PALU_OK) return st;
+  if (!q || !q_strides || !offsets || !out || !workspace) return fail(PALU_ERR_INVALID_ARG, "NULL pointer");
+  if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15 || (uintptr_t)offsets & 3)
+    return fail(PALU_ERR_INVALID_ARG, "pointers must be 16-byte aligned (offsets 4)");
+  for (int i = 0; i < 2; ++i)
+    if (q_strides[i] < 0 || q_strides[i] % 8)
+      return fail(PALU_ERR_INVALID_ARG, "q's strides must be non-negative multiples of 8 elements");
+  if (!(softmax_scale >= 0.f) || isinf(softmax_scale))
+    return fail(PALU_ERR_INVALID_ARG, "softmax_scale must be finite and not negative");
+  if (workspace_bytes < l.total) return fail(PALU_ERR_INVALID_ARG, "workspace too small");
+  CUtensorMap km, vm;
+  if ((st = page_map(&km, cache, cache->k_pages, cache->k_strides)) != PALU_OK ||
+      (st = page_map(&vm, cache, cache->v_pages, cache->v_strides)) != PALU_OK)
+    return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttnParams p = {};
+  p.c = paged_view(cache);
+  p.q = static_cast<const uint16_t*>(q);
+  p.qs0 = q_strides[0], p.qs1 = q_strides[1];
+  p.offsets = offsets;
+  p.out = static_cast<uint16_t*>(out);
+  p.row_ml = reinterpret_cast<float2*>(ws + l.row_ml);
+  p.row_acc = reinterpret_cast<float*>(ws + l.row_acc);
+  p.N = (int)tokens;
+  p.max_new = max_new;
+  p.Hq = q_heads;
+  p.Gq = q_heads / cache->kv_heads;
+  p.S0 = l.shared ? shared_pages * cache->page_size : 0;
+  p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
+  const int grid = device_sm_count();
+  const PartSet prefix = {reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
+                          reinterpret_cast<long long*>(ws + l.plan_p), grid, l.R_prefix};
+  const PartSet own = {reinterpret_cast<float2*>(ws + l.ml_o), reinterpret_cast<float*>(ws + l.acc_o),
+                       reinterpret_cast<long long*>(ws + l.plan_o), grid, l.R_own};
+  const bool bf16 = cache->dtype == PALU_TYPE_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (l.shared) {
+    p.part = prefix;
+    p.do_prefix = 1;
+    p.do_own = 0;
+    if ((st = bf16 ? launch_few<true>(p, km, vm, false, s) : launch_few<false>(p, km, vm, false, s)) != PALU_OK) return st;
+  }
+  p.part = own;
+  p.do_prefix = 0;
+  p.do_own = 1;
+  if ((st = bf16 ? launch_few<true>(p, km, vm, l.shared, s) : launch_few<false>(p, km, vm, l.shared, s)) != PALU_OK) return st;
+  CombineParams cp = {p, prefix, own};
+  const long long rows = (long long)p.N * p.Hq;
+  const int cgrid = (int)((rows + kCombineWarps - 1) / kCombineWarps);
+  return bf16 ? launch(paged_combine_kernel<true>, cgrid, 32 * kCombineWarps, 0, true, s, "paged_combine_kernel launch", cp)
+              : launch(paged_combine_kernel<false>, cgrid, 32 * kCombineWarps, 0, true, s, "paged_combine_kernel launch", cp);
+}

@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libpalu (include/palu.h, include/kivi.h).
+"""Thin ctypes binding of libpalu (include/*.h).
 
 Argument marshalling only: every step of the fit, append and decode runs in
 the library's CUDA kernels.  PyTorch provides device memory and the current
@@ -27,6 +27,11 @@ PALU_DEVERR_LENGTH_MISMATCH = 4
 PALU_DEVERR_NOT_CONVERGED = 8
 PALU_DEVERR_ROLLBACK = 16
 PALU_DEVERR_BOUNDS = 32
+PALU_DEVERR_PAGE = 64
+PALU_DEVERR_SPAN = 128
+PALU_DEVERR_POSITION = 256
+PALU_TYPE_F16 = 0
+PALU_TYPE_BF16 = 1
 STATUS_NAMES = {0: "PALU_OK", 1: "PALU_ERR_INVALID_ARG", 2: "PALU_ERR_UNSUPPORTED", 3: "PALU_ERR_CAPACITY",
                 4: "PALU_ERR_NOT_INITIALIZED", 5: "PALU_ERR_CUDA", 6: "PALU_ERR_DEVICE"}
 
@@ -62,6 +67,18 @@ class palu_svdq_cache(ctypes.Structure):
     _fields_ = [("magic", c_int32), ("batch", c_int32), ("kv_heads", c_int32), ("r_max", c_int32),
                 ("record_bytes", c_int32), ("pad0", c_int32), ("capacity", c_int64), ("n_blk_cap", c_int64),
                 ("blocks", c_void_p), ("tail", c_void_p), ("state", c_void_p), ("length", c_int64)]
+
+
+class palu_qk_transform(ctypes.Structure):
+    _fields_ = [("q_weight", c_void_p), ("k_weight", c_void_p), ("cos_sin", c_void_p), ("n_positions", c_int64),
+                ("rope_dim", c_int32), ("interleaved", c_int32), ("eps", c_float), ("pad0", c_int32)]
+
+
+class palu_paged_cache(ctypes.Structure):
+    _fields_ = [("magic", c_int32), ("dtype", c_int32), ("kv_heads", c_int32), ("page_size", c_int32),
+                ("batch", c_int32), ("table_width", c_int32), ("n_pages", c_int64), ("k_pages", c_void_p),
+                ("v_pages", c_void_p), ("k_strides", c_int64 * 3), ("v_strides", c_int64 * 3),
+                ("page_table", c_void_p), ("lengths", c_void_p), ("error", c_void_p)]
 
 
 _P = POINTER
@@ -116,6 +133,21 @@ _SIGNATURES = {
     "palu_kivi_decode_workspace_size": (c_int32, [_P(palu_kivi_cache), c_int32, _P(c_size_t)]),
     "palu_kivi_decode_attn": (c_int32, [_P(palu_kivi_cache), c_void_p, c_int32, c_float, c_void_p, c_int32,
                                         c_void_p, c_size_t, c_void_p]),
+    "palu_qk_norm_rope": (c_int32, [_P(palu_qk_transform), c_int32, c_int64, c_int64, c_int32, c_int32, c_void_p,
+                                    _P(c_int64), c_void_p, _P(c_int64), c_void_p, c_void_p, c_void_p, c_void_p,
+                                    c_void_p]),
+    "palu_paged_cache_init": (c_int32, [_P(palu_paged_cache), c_int32, c_int32, c_int32, c_int64, c_void_p, _P(c_int64),
+                                        c_void_p, _P(c_int64), c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
+    "palu_paged_append": (c_int32, [_P(palu_paged_cache), _P(palu_qk_transform), c_int64, c_void_p, c_int32, c_void_p,
+                                    _P(c_int64), c_void_p, _P(c_int64), c_void_p, _P(c_int64), c_void_p, c_void_p,
+                                    c_void_p]),
+    "palu_paged_attn_workspace_size": (c_int32, [_P(palu_paged_cache), c_int64, c_int32, c_int32, c_int32,
+                                                 _P(c_size_t)]),
+    "palu_paged_attn": (c_int32, [_P(palu_paged_cache), c_int64, c_void_p, c_int32, c_int32, c_void_p, _P(c_int64),
+                                  c_int32, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "palu_paged_sync": (c_int32, [_P(palu_paged_cache), _P(c_uint32), c_void_p]),
+    "palu_draft_verify": (c_int32, [c_int64, c_int32, c_int64, c_void_p, _P(c_int64), c_void_p, _P(c_int64), c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
 }
 
 _lib = None
@@ -445,6 +477,254 @@ def palu_kivi_decode_attn(cache: palu_kivi_cache, q, out, workspace, softmax_sca
     _check(lib().palu_kivi_decode_attn(ctypes.byref(cache), _ptr(q), q.shape[1], softmax_scale, _ptr(out),
                                        1 if out.dtype == torch.float32 else 0, _ptr(workspace),
                                        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ the serving step (include/paged.h, include/draft.h)
+
+_TYPES = {torch.float16: PALU_TYPE_F16, torch.bfloat16: PALU_TYPE_BF16}
+
+
+def _need_rows(t, name, shape, dtype, device):
+    """A token-major operand: any strides with contiguous channels and 16-byte aligned rows (entries of `shape` that
+    are None match any extent).  Returns its leading strides, of an extent-1 dimension 0: torch leaves those open."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    got = t.shape
+    if len(got) != len(shape) or any(e is not None and e != s for e, s in zip(shape, got)):
+        raise ValueError(f"{name} has shape {tuple(got)}; expected {tuple('*' if e is None else e for e in shape)}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    lead = [s if n > 1 else 0 for s, n in zip(st[:-1], got)]
+    if t.data_ptr() % 16 or any(s % 8 for s in lead):
+        raise ValueError(f"{name}'s rows must be 16-byte aligned (strides {st})")
+    return (c_int64 * len(lead))(*lead)
+
+
+def _need_on(t, name, shape, dtype, device):
+    """A contiguous operand of one type on one device."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}; expected {dtype} {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _need_device(t, name):
+    """The library launches on the current device: its operands must be there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, which is not the current device")
+    return dev
+
+
+def _transform(dtype, device, cos_sin, q_weight, k_weight, eps, interleaved):
+    t = palu_qk_transform()
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need_on(w, name, (D,), dtype, device)
+            setattr(t, name, w.data_ptr())
+    if cos_sin is not None:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a tensor [positions, rope_dim]")
+        _need_on(cos_sin, "cos_sin", tuple(cos_sin.shape), torch.float32, device)
+        t.cos_sin, (t.n_positions, t.rope_dim) = cos_sin.data_ptr(), cos_sin.shape
+    t.interleaved = 1 if interleaved else 0
+    t.eps = eps
+    return t
+
+
+def qk_norm_rope(q, k, positions, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, error=None, stream=None):
+    """Per-head RMS norm (where a weight is given) and rotation (where a table is given) of q [B, T, Hq, 128] and
+    k [B, T, Hkv, 128] (fp16 or bf16; any strides with contiguous channels, e.g. views of one projection), positions
+    int64 [B, T], cos_sin fp32 [n_positions, rope_dim] (cosines, then sines).  Returns (q_out [B, Hq, T, 128],
+    k_out [B, Hkv, T, 128]), the layout the caches take.  error: int32 [1] on the device, collecting
+    PALU_DEVERR_POSITION; the rows of such a token are NaN."""
+    dev = _need_device(q, "q")
+    if q.dtype not in _TYPES:
+        raise ValueError(f"q has dtype {q.dtype}; expected torch.float16 or torch.bfloat16")
+    dt = q.dtype
+    qs = _need_rows(q, "q", (None, None, None, D), dt, dev)
+    B, T, Hq, _ = q.shape
+    ks = _need_rows(k, "k", (B, T, None, D), dt, dev)
+    Hk = k.shape[2]
+    tr = _transform(dt, dev, cos_sin, q_weight, k_weight, eps, interleaved)
+    if cos_sin is not None:
+        _need_on(positions, "positions", (B, T), torch.int64, dev)
+    if error is not None:
+        _need_on(error, "error", (1,), torch.int32, dev)
+    if q_out is None:
+        q_out = torch.empty((B, Hq, T, D), dtype=dt, device=dev)
+    else:
+        _need_on(q_out, "q_out", (B, Hq, T, D), dt, dev)
+    if k_out is None:
+        k_out = torch.empty((B, Hk, T, D), dtype=dt, device=dev)
+    else:
+        _need_on(k_out, "k_out", (B, Hk, T, D), dt, dev)
+    if B and T:
+        _check(lib().palu_qk_norm_rope(ctypes.byref(tr), _TYPES[dt], B, T, Hq, Hk, q.data_ptr(), qs, k.data_ptr(), ks,
+                                       positions.data_ptr() if cos_sin is not None else None, q_out.data_ptr(),
+                                       k_out.data_ptr(), None if error is None else error.data_ptr(), _stream(stream)))
+    return q_out, k_out
+
+
+class PagedCache:
+    """A paged key/value cache (include/paged.h) on the caller's tensors.
+    k_pages, v_pages: fp16 or bf16 [n_pages, Hkv, page_size, 128], any strides with contiguous channels (a pool kept
+    token-major, or keys and values interleaved, is passed as a view).  page_table int32 [B, width] and lengths int64
+    [B]: the program's own, read by every call; change them in place to hand out pages and to roll tokens back."""
+
+    def __init__(self, k_pages, v_pages, page_table, lengths):
+        dev = _need_device(k_pages, "k_pages")
+        if k_pages.dtype not in _TYPES:
+            raise ValueError(f"k_pages has dtype {k_pages.dtype}; expected torch.float16 or torch.bfloat16")
+        self.dtype, self.device = k_pages.dtype, dev
+        _need_rows(k_pages, "k_pages", (None, None, None, D), self.dtype, dev)
+        _need_rows(v_pages, "v_pages", tuple(k_pages.shape), self.dtype, dev)
+        n_pages, self.kv_heads, self.page_size, _ = k_pages.shape
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be a tensor [batch, width]")
+        self.batch, self.width = page_table.shape
+        _need_on(page_table, "page_table", (self.batch, self.width), torch.int32, dev)
+        _need_on(lengths, "lengths", (self.batch,), torch.int64, dev)
+        self.k_pages, self.v_pages, self.page_table, self.lengths = k_pages, v_pages, page_table, lengths
+        self.error = torch.zeros(1, dtype=torch.int32, device=dev)
+
+        def strides(t):  # of a dimension of one element: anything that is aligned
+            return (c_int64 * 3)(*[s if n > 1 else D for s, n in zip(t.stride()[:3], t.shape)])
+        self.c = palu_paged_cache()
+        _check(lib().palu_paged_cache_init(ctypes.byref(self.c), _TYPES[self.dtype], self.kv_heads, self.page_size, n_pages,
+                                           k_pages.data_ptr(), strides(k_pages), v_pages.data_ptr(), strides(v_pages),
+                                           page_table.data_ptr(), self.batch, self.width, lengths.data_ptr(),
+                                           self.error.data_ptr()))
+
+    def _here(self):
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.device}, which is not the current device")
+
+    def append(self, k, v, offsets, q=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+               positions=None, q_out=None, stream=None):
+        """Append the batch's new tokens: rows offsets[b] .. offsets[b+1]-1 (int32 [B + 1]) of k and v [N, Hkv, 128] are
+        the last tokens of sequence b (lengths[b] counts them already).  Keys, and q [N, Hq, 128] where given, are
+        normalised and rotated as in qk_norm_rope, by default at each token's place.  Returns q_out (None without q);
+        rows behind offsets[B] are left as they were."""
+        self._here()
+        dt, dev = self.dtype, self.device
+        ks = _need_rows(k, "k", (None, self.kv_heads, D), dt, dev)
+        n = k.shape[0]
+        vs = _need_rows(v, "v", (n, self.kv_heads, D), dt, dev)
+        _need_on(offsets, "offsets", (self.batch + 1,), torch.int32, dev)
+        tr = _transform(dt, dev, cos_sin, q_weight, k_weight, eps, interleaved)
+        if positions is not None:
+            _need_on(positions, "positions", (n,), torch.int64, dev)
+        qs, hq = None, 0
+        if q is not None:
+            qs = _need_rows(q, "q", (n, None, D), dt, dev)
+            hq = q.shape[1]
+            if q_out is None:
+                q_out = torch.empty((n, hq, D), dtype=dt, device=dev)
+            else:
+                _need_on(q_out, "q_out", (n, hq, D), dt, dev)
+        elif q_out is not None:
+            raise ValueError("q_out is given without q")
+        if n:
+            _check(lib().palu_paged_append(ctypes.byref(self.c), ctypes.byref(tr), n, offsets.data_ptr(), hq,
+                                           None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                           None if positions is None else positions.data_ptr(),
+                                           None if q is None else q_out.data_ptr(), _stream(stream)))
+        return q_out
+
+    def attend_workspace(self, tokens, q_heads, max_new, shared_pages=0):
+        """A workspace for attend calls of up to these sizes (calls that share one must not overlap on the GPU)."""
+        n = c_size_t()
+        _check(lib().palu_paged_attn_workspace_size(ctypes.byref(self.c), max(tokens, 1), q_heads, max_new, shared_pages,
+                                                    ctypes.byref(n)))
+        return _dev_bytes(n.value, self.device)
+
+    def attend(self, q, offsets, max_new, shared_pages=0, softmax_scale=0.0, workspace=None, out=None, stream=None):
+        """Attention of the new tokens (already appended) over the cache: row r of q [N, Hq, 128], sequence b's token
+        at place t, attends to tokens 0 .. t of its sequence.  max_new: the most rows a sequence has.  shared_pages:
+        leading page-table entries that are the same in every row; they are read once for the batch.  Returns out
+        [N, Hq, 128]; rows behind offsets[B] are left as they were."""
+        self._here()
+        dev = self.device
+        qs = _need_rows(q, "q", (None, None, D), self.dtype, dev)
+        n, hq, _ = q.shape
+        _need_on(offsets, "offsets", (self.batch + 1,), torch.int32, dev)
+        if out is None:
+            out = torch.empty((n, hq, D), dtype=self.dtype, device=dev)
+        else:
+            _need_on(out, "out", (n, hq, D), self.dtype, dev)
+        if n == 0:
+            return out
+        if workspace is None:
+            workspace = self.attend_workspace(n, hq, max_new, shared_pages)
+        else:
+            _need_on(workspace, "workspace", tuple(workspace.shape), torch.uint8, dev)
+        _check(lib().palu_paged_attn(ctypes.byref(self.c), n, offsets.data_ptr(), max_new, hq, q.data_ptr(), qs,
+                                     shared_pages, softmax_scale, out.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel(), _stream(stream)))
+        return out
+
+    def sync(self, stream=None):
+        """Synchronise; raises PaluError if the device error word was set (and clears it)."""
+        e = c_uint32()
+        _check(lib().palu_paged_sync(ctypes.byref(self.c), ctypes.byref(e), _stream(stream)))
+        return e.value
+
+
+def draft_verify(target, draft, drafts, accept_u, sample_u, n_drafts=None, lengths=None, tokens=None, n_kept=None,
+                 new_lengths=None, stream=None):
+    """Verify drafted tokens (include/draft.h): target fp32 [B, k+1, V], draft fp32 [B, k, V] or None, drafts int64
+    [B, k], accept_u fp32 [B, k] and sample_u fp32 [B] in [0, 1), n_drafts int32 [B] (default k each), lengths int64 [B]
+    with all drafts counted.  Returns (tokens int64 [B, k+1]: the kept drafts, one drawn token, -1; n_kept int32 [B];
+    new_lengths int64 [B], or None without lengths)."""
+    dev = _need_device(target, "target")
+    if not isinstance(drafts, torch.Tensor) or drafts.dim() != 2:
+        raise ValueError("drafts must be a tensor [batch, k]")
+    B, k = drafts.shape
+    _need_on(drafts, "drafts", (B, k), torch.int64, dev)
+    if target.dtype != torch.float32 or target.dim() != 3 or tuple(target.shape[:2]) != (B, k + 1) or \
+            (target.shape[2] > 1 and target.stride(2) != 1):
+        raise ValueError(f"target is {target.dtype} {tuple(target.shape)}; expected torch.float32 {(B, k + 1, '*')} with "
+                         "contiguous rows")
+    V = target.shape[2]
+    ds = None
+    if draft is not None:
+        if not isinstance(draft, torch.Tensor) or draft.device != dev or draft.dtype != torch.float32 or \
+                tuple(draft.shape) != (B, k, V) or (V > 1 and draft.stride(2) != 1):
+            raise ValueError(f"draft must be torch.float32 {(B, k, V)} on {dev} with contiguous rows")
+        ds = (c_int64 * 2)(*draft.stride()[:2])
+    _need_on(accept_u, "accept_u", (B, k), torch.float32, dev)
+    _need_on(sample_u, "sample_u", (B,), torch.float32, dev)
+    if n_drafts is not None:
+        _need_on(n_drafts, "n_drafts", (B,), torch.int32, dev)
+    for t, name, shape, dt in ((tokens, "tokens", (B, k + 1), torch.int64), (n_kept, "n_kept", (B,), torch.int32),
+                               (lengths, "lengths", (B,), torch.int64), (new_lengths, "new_lengths", (B,), torch.int64)):
+        if t is not None:
+            _need_on(t, name, shape, dt, dev)
+    if new_lengths is not None and lengths is None:
+        raise ValueError("new_lengths is given without lengths")
+    if tokens is None:
+        tokens = torch.empty((B, k + 1), dtype=torch.int64, device=dev)
+    if n_kept is None:
+        n_kept = torch.empty(B, dtype=torch.int32, device=dev)
+    if lengths is not None and new_lengths is None:
+        new_lengths = torch.empty(B, dtype=torch.int64, device=dev)
+    if B:
+        _check(lib().palu_draft_verify(B, k, V, target.data_ptr(), (c_int64 * 2)(*target.stride()[:2]),
+                                       None if draft is None else draft.data_ptr(), ds, drafts.data_ptr(),
+                                       None if n_drafts is None else n_drafts.data_ptr(), accept_u.data_ptr(),
+                                       sample_u.data_ptr(), None if lengths is None else lengths.data_ptr(),
+                                       tokens.data_ptr(), n_kept.data_ptr(),
+                                       None if lengths is None else new_lengths.data_ptr(), _stream(stream)))
+    return tokens, n_kept, new_lengths
 
 
 # ------------------------------------------------------------------ buffer helpers
