@@ -24,6 +24,13 @@ constexpr int kFewThreads = 32 * (kFewWarps + 1);
 constexpr int kFewStages = 3;
 constexpr int kMergeStride = kHeadDim + 2;
 
+// One tile, as the loading warp hands it to the others.
+struct TileMeta {
+  UnitMeta u;
+  int key0;         // place of the first key
+  int valid;        // keys of the tile that exist (1 .. 128)
+  int first, last;  // of the stretch
+};
 struct FewSmem {
   uint64_t full[kFewStages], empty[kFewStages], join;
   TileMeta meta[kFewStages];
@@ -35,19 +42,6 @@ constexpr int kFewMergeBytes = kFewWarps * 8 * kMergeStride * 4;
 constexpr int kFewSmemBytes = 1024 + kFewStages * 2 * kTileBytes + kFewMergeBytes + (int)sizeof(FewSmem);
 static_assert(kFewSmemBytes <= 232448, "shared memory of paged_few_kernel");
 
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(0), "r"(head), "r"(page)
-      : "memory");
-}
-
-// Shared-memory address of 16-byte chunk ch (0..15) of a tile's row, in the
-// 128-byte swizzle the copies write.
-__device__ __forceinline__ uint32_t panel_addr(uint32_t tile, int row, int ch) {
-  return tile + (ch >> 3) * kPanelBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-}
-
 template <bool BF16>
 __device__ __forceinline__ void mma_16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
@@ -55,35 +49,6 @@ __device__ __forceinline__ void mma_16(float d[4], uint32_t a0, uint32_t a1, uin
     mma_bf16(d, a0, a1, a2, a3, b0, b1);
   else
     mma_f16(d, a0, a1, a2, a3, b0, b1);
-}
-
-// The limit of a row of the unit: how many of the sequence's tokens it sees.
-__device__ __forceinline__ int unit_row_limit(const AttnParams& p, const TileMeta& m, int r) {
-  const int tok = (m.row0 + r) / p.Gq;
-  if (!m.prefix) return m.base + tok + 1;
-  // token numbers of the whole call: the row's sequence
-  int lo = 0, hi = p.c.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.offsets + mid) <= tok)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  unsigned bad = 0;
-  const SeqSpan s = seq_span(p, lo, &bad);
-  const int i = tok - s.tok0;
-  return i >= 0 && i < s.n ? min(row_limit(s, i), p.S0) : 0;
-}
-
-// A wait that gives up sets the error word, and `failed` for the block: every
-// role then runs on to its end without waiting (what it computes is void).
-__device__ __forceinline__ void wait_or_fail(uint64_t* bar, uint32_t parity, int* failed, unsigned* error) {
-  if (*(volatile int*)failed) return;
-  if (!mbar_wait_bounded(bar, parity)) {
-    *(volatile int*)failed = 1;
-    atomicOr(error, PALU_DEVERR_TIMEOUT);
-  }
 }
 
 // NT: n8 tiles of rows (8 or 16 rows a unit).
@@ -114,30 +79,26 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // ---- the loading warp
       unsigned bad = 0;
       int it = 0;
-      plan_walk<R>(p, &sh.plan, [&](const TileMeta& m) -> bool {
-        const int st = it % kFewStages;
-        if (it >= kFewStages) wait_or_fail(&sh.empty[st], ((it / kFewStages) - 1) & 1, &sh.failed, p.c.error);
-        // all lanes stop together
-        if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) return false;
-        ++it;
-        const int pages = (m.valid + p.c.page - 1) >> p.c.page_shift;
-        if (lane == 0) {
-          sh.meta[st] = m;
-          mbar_arrive_expect_tx(&sh.full[st], pages * p.c.page * kHeadDim * 4);
-        }
-        __syncwarp();
-        uint32_t kt = smem_addr(smem + st * 2 * kTileBytes);
-        if (lane < pages) {
-          int page = __ldg(p.c.table + (long long)m.seq * p.c.width + (m.key0 >> p.c.page_shift) + lane);
-          if (page < 0 || page >= p.c.n_pages) {
-            bad |= PALU_DEVERR_PAGE;
-            page = 0;
+      plan_walk<R>(p, &sh.plan, [&](const UnitMeta& u) -> bool {
+        for (int k = 0; k < u.n; ++k, ++it) {
+          const int st = it % kFewStages, key0 = u.key0 + k * kKeyTile, valid = min(kKeyTile, u.key_end - key0);
+          const int pages = (valid + p.c.page - 1) >> p.c.page_shift;
+          const int page = lane < pages ? page_of(p, u.seq, key0 + lane * p.c.page, &bad) : 0;
+          if (it >= kFewStages) wait_or_fail(&sh.empty[st], ((it / kFewStages) - 1) & 1, &sh.failed, p.c.error);
+          // all lanes stop together
+          if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) return false;
+          if (lane == 0) {
+            sh.meta[st] = TileMeta{u, key0, valid, k == 0, k == u.n - 1};
+            mbar_arrive_expect_tx(&sh.full[st], pages * p.c.page * kHeadDim * 4);
           }
-          kt += lane * p.c.page * 128;
-          tma_page(kt, &kmap, &sh.full[st], 0, m.kh, page);
-          tma_page(kt + kPanelBytes, &kmap, &sh.full[st], 64, m.kh, page);
-          tma_page(kt + kTileBytes, &vmap, &sh.full[st], 0, m.kh, page);
-          tma_page(kt + kTileBytes + kPanelBytes, &vmap, &sh.full[st], 64, m.kh, page);
+          __syncwarp();
+          if (lane < pages) {
+            const uint32_t kt = smem_addr(smem + st * 2 * kTileBytes) + lane * p.c.page * 128;
+            tma_page(kt, &kmap, &sh.full[st], 0, u.kh, page);
+            tma_page(kt + kPanelBytes, &kmap, &sh.full[st], 64, u.kh, page);
+            tma_page(kt + kTileBytes, &vmap, &sh.full[st], 0, u.kh, page);
+            tma_page(kt + kTileBytes + kPanelBytes, &vmap, &sh.full[st], 64, u.kh, page);
+          }
         }
         return true;
       });
@@ -151,6 +112,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       float m_run[NT][2], l_run[NT][2], acc[NT][8][4];
       uint32_t qb[NT][8][2];
       int lim[NT][2];
+      UnitMeta m = {};
       uint32_t joins = 0;
       // the eight warps meet (bounded, unlike a named barrier)
       auto join = [&] {
@@ -163,8 +125,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int it = 0; it < n_tiles; ++it) {
         const int st = it % kFewStages;
         wait_or_fail(&sh.full[st], (it / kFewStages) & 1, &sh.failed, p.c.error);
-        const TileMeta m = sh.meta[st];
-        if (m.first) {
+        const TileMeta& tm = sh.meta[st];
+        const int valid = tm.valid, key0 = tm.key0, last = tm.last;
+        if (tm.first) {
+          m = tm.u;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const int rg = nt * 8 + g;
@@ -190,10 +154,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
         }
         const uint32_t kt = smem_addr(smem + st * 2 * kTileBytes), vt = kt + kTileBytes;
-        if (r0 < m.valid) {
-          if (m.valid < r0 + 16) {
+        if (r0 < valid) {
+          if (valid < r0 + 16) {
             // whatever lies behind the last key must not reach the products: 0 * NaN is NaN
-            const int z0 = m.valid - r0;
+            const int z0 = valid - r0;
             for (int i = lane; i < (16 - z0) * 16; i += 32) {
               const uint32_t a = panel_addr(vt, r0 + z0 + (i >> 4), i & 15);
               asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
@@ -211,7 +175,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_16<BF16>(sc[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
           }
-          const int t = m.key0 + r0 + g;
+          const int t = key0 + r0 + g;
           uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -261,7 +225,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[st]);
-        if (m.last) {
+        if (last) {
           // join the warps' states, 8 rows at a time, and write the unit's result
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -470,6 +434,7 @@ static palu_status page_map(CUtensorMap* map, const palu_paged_cache* c, const v
 // own keys, and the workspace's parts.
 struct AttnLayout {
   bool shared;       // the prefix is a part of its own
+  bool one_launch;   // both parts on the kernel for many rows
   int R_prefix, R_own;
   size_t plan_p, ml_p, acc_p, plan_o, ml_o, acc_o, row_ml, row_acc, total;
 };
@@ -487,8 +452,9 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     return fail(PALU_ERR_INVALID_ARG, "shared_pages must be in [0, table_width]");
   const int64_t own_rows = std::min<int64_t>(max_new, tokens) * Gq, all_rows = tokens * Gq;
   l->shared = shared_pages > 0 && c->batch > 1;
-  l->R_own = own_rows <= 8 ? 8 : 16;
-  l->R_prefix = all_rows <= 8 ? 8 : 16;
+  l->R_own = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
+  l->R_prefix = all_rows <= 8 ? 8 : all_rows <= 16 ? 16 : kManyRows;
+  l->one_launch = l->shared && l->R_own == kManyRows;  // then the prefix has many rows, too
   const size_t slots = 2 * (size_t)device_sm_count();
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -496,9 +462,10 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     o = align_up(o + bytes, 256);
     return at;
   };
-  l->plan_p = take(sizeof(long long) * (1 + (size_t)c->batch));
-  l->ml_p = l->shared ? take(slots * l->R_prefix * sizeof(float2)) : 0;
-  l->acc_p = l->shared ? take(slots * l->R_prefix * kHeadDim * sizeof(float)) : 0;
+  const bool two = l->shared && !l->one_launch;
+  l->plan_p = two ? take(sizeof(long long) * (1 + (size_t)c->batch)) : 0;
+  l->ml_p = two ? take(slots * l->R_prefix * sizeof(float2)) : 0;
+  l->acc_p = two ? take(slots * l->R_prefix * kHeadDim * sizeof(float)) : 0;
   l->plan_o = take(sizeof(long long) * (1 + (size_t)c->batch));
   l->ml_o = take(slots * l->R_own * sizeof(float2));
   l->acc_o = take(slots * l->R_own * kHeadDim * sizeof(float));
@@ -508,25 +475,6 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   return PALU_OK;
 }
 
-template <class K, class... Args>
-static palu_status launch(K kernel, int grid, int threads, int smem, bool dependent, cudaStream_t stream, const char* what,
-                          Args... args) {
-  int per_sm = 0;
-  palu_status st = kernel_occupancy(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
-  if (st != PALU_OK) return st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), what);
-}
-
 template <bool BF16>
 static palu_status launch_few(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool dependent,
                               cudaStream_t s) {
@@ -534,6 +482,14 @@ static palu_status launch_few(const AttnParams& p, const CUtensorMap& km, const 
                                 "paged_few_kernel launch", p, km, vm)
                        : launch(paged_few_kernel<BF16, 2>, p.part.grid, kFewThreads, kFewSmemBytes, dependent, s,
                                 "paged_few_kernel launch", p, km, vm);
+}
+
+// The launch of one part, on the kernel for its number of rows.  `dependent`:
+// it may begin while the launch before it (the prefix) still runs.
+static palu_status launch_part(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, bool dependent,
+                               cudaStream_t s) {
+  if (p.part.R == kManyRows) return launch_many(p, km, vm, bf16, s);
+  return bf16 ? launch_few<true>(p, km, vm, dependent, s) : launch_few<false>(p, km, vm, dependent, s);
 }
 
 }  // namespace palu
@@ -586,22 +542,22 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   p.S0 = l.shared ? shared_pages * cache->page_size : 0;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
   const int grid = device_sm_count();
-  const PartSet prefix = {reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
-                          reinterpret_cast<long long*>(ws + l.plan_p), grid, l.R_prefix};
   const PartSet own = {reinterpret_cast<float2*>(ws + l.ml_o), reinterpret_cast<float*>(ws + l.acc_o),
                        reinterpret_cast<long long*>(ws + l.plan_o), grid, l.R_own};
+  const PartSet prefix = l.one_launch ? own
+                                      : PartSet{reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
+                                                reinterpret_cast<long long*>(ws + l.plan_p), grid, l.R_prefix};
   const bool bf16 = cache->dtype == PALU_TYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (l.shared) {
+  if (l.shared && !l.one_launch) {
     p.part = prefix;
     p.do_prefix = 1;
-    p.do_own = 0;
-    if ((st = bf16 ? launch_few<true>(p, km, vm, false, s) : launch_few<false>(p, km, vm, false, s)) != PALU_OK) return st;
+    if ((st = launch_part(p, km, vm, bf16, false, s)) != PALU_OK) return st;
   }
   p.part = own;
-  p.do_prefix = 0;
+  p.do_prefix = l.one_launch;
   p.do_own = 1;
-  if ((st = bf16 ? launch_few<true>(p, km, vm, l.shared, s) : launch_few<false>(p, km, vm, l.shared, s)) != PALU_OK) return st;
+  if ((st = launch_part(p, km, vm, bf16, l.shared && !l.one_launch, s)) != PALU_OK) return st;
   CombineParams cp = {p, prefix, own};
   const long long rows = (long long)p.N * p.Hq;
   const int cgrid = (int)((rows + kCombineWarps - 1) / kCombineWarps);

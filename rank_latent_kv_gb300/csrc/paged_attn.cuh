@@ -94,19 +94,20 @@ __host__ __device__ inline long long prefix_tiles_of(int S0) { return (S0 + kKey
 // Where a finished unit goes.
 enum { kToOut = -1, kToRow = -2 };
 
-// One tile of the line, as the loading warp hands it to the others.
-struct TileMeta {
-  int key0;    // first key's place
-  int valid;   // keys of the tile that exist (1 .. 128)
-  int first, last;  // of the CTA's stretch of the unit
-  int kh;      // KV head
-  int row0;    // first row of the row tile, among the unit set's rows
-  int rows;    // rows in it
-  int tok0;    // token of row 0 of the set
-  int base;    // own units: the place of the set's first new token
-  int seq;     // row of the page table
-  int prefix;  // a prefix unit: each row's own limit is looked up
-  int dest;    // slot, kToOut or kToRow
+// A CTA's stretch of a unit: `n` tiles from key0 on, as the loading warp hands
+// it to the others.
+struct UnitMeta {
+  int key0;     // place of the first key
+  int key_end;  // behind the unit's last key (inside the stretch's last tile, or behind it)
+  int n;        // tiles; 0: the line has ended
+  int kh;       // KV head
+  int row0;     // first row of the row tile, among the unit set's rows
+  int rows;     // rows in it
+  int tok0;     // token of row 0 of the set
+  int base;     // own units: the place of the set's first new token
+  int seq;      // row of the page table
+  int prefix;   // a prefix unit: each row's own limit is looked up
+  int dest;     // slot, kToOut or kToRow
 };
 
 // The CTA's stretch of the line, found by the whole CTA (blockDim.x threads).
@@ -171,10 +172,10 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
   __syncthreads();
 }
 
-// Calls tile(meta) for each tile of the CTA's stretch, in order: run by one
-// warp, all its lanes.
+// Calls unit(meta) for each unit that the CTA's stretch of the line touches, in
+// order, until it returns false: run by one warp, all its lanes.
 template <int R, class F>
-__device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch* sc, F&& tile) {
+__device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch* sc, F&& unit) {
   const int Hkv = p.c.kv_heads;
   const long long w1 = sc->w1;
   long long pos = sc->w0;
@@ -183,21 +184,17 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
   const int rts = (all_rows + R - 1) / R;
   const long long prefix = p.do_prefix ? (long long)Hkv * rts * tiles0 : 0;
   const int cta = blockIdx.x;
-  TileMeta m;
+  UnitMeta m;
   // the unit [u0, u0 + n) and the stretch of it that starts at pos
   auto run_unit = [&](long long u0, int n, int key_base, int key_end) -> bool {
     const int k0 = (int)(pos - u0);
     const int k1 = (int)min((long long)n, k0 + (w1 - pos));
     m.dest = k0 > 0 ? 2 * cta : k1 < n ? 2 * cta + 1 : p.S0 > 0 ? kToRow : kToOut;
-    for (int k = k0; k < k1; ++k) {
-      m.key0 = key_base + k * kKeyTile;
-      m.valid = min(kKeyTile, key_end - m.key0);
-      m.first = k == k0;
-      m.last = k == k1 - 1;
-      if (!tile(m)) return false;
-    }
-    pos += k1 - k0;
-    return true;
+    m.key0 = key_base + k0 * kKeyTile;
+    m.key_end = key_end;
+    m.n = k1 - k0;
+    pos += m.n;
+    return unit(m);
   };
   while (pos < w1 && pos < prefix) {
     const int u = (int)(pos / tiles0);
@@ -235,5 +232,82 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
     }
   }
 }
+
+// The limit of a row of the unit: how many of the sequence's tokens it sees.
+__device__ __forceinline__ int unit_row_limit(const AttnParams& p, const UnitMeta& m, int r) {
+  const int tok = (m.row0 + r) / p.Gq;
+  if (!m.prefix) return m.base + tok + 1;
+  // token numbers of the whole call: the row's sequence
+  int lo = 0, hi = p.c.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.offsets + mid) <= tok)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  unsigned bad = 0;
+  const SeqSpan s = seq_span(p, lo, &bad);
+  const int i = tok - s.tok0;
+  return i >= 0 && i < s.n ? min(row_limit(s, i), p.S0) : 0;
+}
+
+// The page that holds token `place` of table row `seq` (0 and an error bit for
+// an id outside the pool).
+__device__ __forceinline__ int page_of(const AttnParams& p, int seq, int place, unsigned* bad) {
+  const int page = __ldg(p.c.table + (long long)seq * p.c.width + (place >> p.c.page_shift));
+  if (page >= 0 && page < p.c.n_pages) return page;
+  *bad |= PALU_DEVERR_PAGE;
+  return 0;
+}
+
+// One page of one head, 64 channels from x on, into a panel.
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(0), "r"(head), "r"(page)
+      : "memory");
+}
+
+// Shared-memory address of 16-byte chunk ch (0..15) of a tile's row, in the
+// 128-byte swizzle the copies write.
+__device__ __forceinline__ uint32_t panel_addr(uint32_t tile, int row, int ch) {
+  return tile + (ch >> 3) * kPanelBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+}
+
+// A wait that gives up sets the error word, and `failed` for the block: every
+// role then runs on to its end without waiting (what it computes is void).
+__device__ __forceinline__ void wait_or_fail(uint64_t* bar, uint32_t parity, int* failed, unsigned* error) {
+  if (*(volatile int*)failed) return;
+  if (!mbar_wait_bounded(bar, parity)) {
+    *(volatile int*)failed = 1;
+    atomicOr(error, PALU_DEVERR_TIMEOUT);
+  }
+}
+
+// A launch; `dependent`: it may begin while the one before it on the stream still
+// runs, and waits for it inside.
+template <class K, class... Args>
+palu_status launch(K kernel, int grid, int threads, int smem, bool dependent, cudaStream_t stream, const char* what,
+                          Args... args) {
+  int per_sm = 0;
+  palu_status st = kernel_occupancy(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
+  if (st != PALU_OK) return st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), what);
+}
+
+// The kernel for many rows (paged_many.cu).
+constexpr int kManyRows = 256;
+palu_status launch_many(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 
 }  // namespace palu

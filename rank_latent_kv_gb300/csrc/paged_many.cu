@@ -1,0 +1,533 @@
+// Attention over the paged cache for many rows a KV head: a shared prefix
+// that all sequences' queries read, several drafted tokens, prompt chunks.
+//
+// From about 300 rows on, the 4 * 128 flops a (row, key) cost more than
+// reading the key: the tensor cores are the bound, and 128 rows against 128
+// keys (two products of 128^3) take 1024 clocks of them, in which the
+// softmax's 16,384 exponentials have to be done too.  One persistent CTA an
+// SM works on 256 rows at a time, as two row halves of 128 that take turns:
+// while one half's weights are computed by its 128 threads (a row a thread, no
+// shuffles), the tensor cores work for the other.  Both halves use the same
+// keys and values, so a tile is read once for 256 rows.  A unit of at most
+// 128 rows gives its even tiles to one half and its odd tiles to the other, and
+// the two results are joined at the end.
+//
+//   TMEM (512 columns): S0 S1 O0 O1, 128 fp32 columns each; the weights P
+//   overwrite their S as 16-bit pairs and enter the second product from there.
+//   Shared memory: Q0 Q1 (32 KB each), a ring of five 32 KB tiles that holds
+//   K and V of successive key tiles in turn.
+//   Warps 0-3, 4-7: the halves' softmax; warp 8: loads; warp 9: products;
+//   warps 10, 11 fill the third warpgroup and do nothing.
+//
+// The running maximum is raised only when it grows by more than 2^8 (the
+// weights then stay below 2^8, far inside fp16): the accumulator in TMEM is
+// rescaled a few times a unit instead of once a tile.  Weights are rounded
+// once, to the type of the values (the tensor cores take no other); their sum is
+// kept in fp32 before that rounding, so the roundings' errors average out
+// instead of adding up.
+#include "paged_attn.cuh"
+#include "splitk_attend.cuh"
+
+namespace palu {
+
+// Twelve warps launch with 168 registers a thread, 3 * 168 = 504 a lane of the
+// three warpgroups; the softmax warpgroups, which hold a row of 128 scores,
+// then take 208 each and leave 88 to the third (208 + 208 + 88 = 504).
+constexpr int kManyThreads = 384;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kRing = 5;
+constexpr int kHalf = 128;
+
+struct ManySmem {
+  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t meta_full[2], meta_empty[2];
+  uint64_t q_full, s_full[2], p_full[2], unit_done, join, drain;
+  UnitMeta meta[2];
+  float2 ml[kHalf];  // second half's (m, l) when the halves are joined
+  PlanScratch plan;
+  uint32_t tmem;
+  int failed;
+};
+constexpr int kManySmemBytes = 1024 + (2 + kRing) * kTileBytes + (int)sizeof(ManySmem);
+static_assert(kManySmemBytes <= 232448, "shared memory of paged_many_kernel");
+
+// ---------------------------------------------------------------- tcgen05
+__device__ __forceinline__ void tc_alloc(uint32_t* dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(dst)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t t) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// d (+)= a b, both operands in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// d (+)= a b, a in TMEM
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes, a lane a thread
+__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptor, 128-byte swizzle: byte offsets between
+// 8-row groups (stride) and, for an operand whose rows run along N (the
+// values: 64 channels a panel), between panels (lead).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ULL << 46 | 2ULL << 61;
+}
+// Instruction descriptor: fp32 accumulator, 128 x 128, both operands of one 16-bit type.
+template <bool BF16>
+__device__ constexpr uint32_t instr_desc(bool b_n_major) {
+  return 1u << 4 | (BF16 ? 1u << 7 | 1u << 10 : 0u) | (b_n_major ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ void fma2(float& x, float& y, float s, float c) {  // (x, y) <- (x, y) s + c
+  uint64_t v, ss, cc;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(ss), "l"(cc));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ void add2(float& ax, float& ay, float x, float y) {
+  uint64_t a, v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(ax), "f"(ay));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(v));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(ax), "=f"(ay) : "l"(a));
+}
+
+constexpr float kRaise = 8.f;  // log2 of how far a weight may pass 1 before the maximum is raised
+
+template <bool BF16>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    paged_many_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = smem + 2 * kTileBytes;
+  ManySmem& sh = *reinterpret_cast<ManySmem*>(ring + kRing * kTileBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned* const err = p.c.error;
+  grid_dep_launch();
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.meta_full[i], 1);
+      mbar_init(&sh.meta_empty[i], 9);  // eight softmax warps, the product warp
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+    }
+    mbar_init(&sh.q_full, 8);
+    mbar_init(&sh.unit_done, 1);
+    mbar_init(&sh.join, 8);
+    mbar_init(&sh.drain, 1);
+    sh.failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tc_alloc(&sh.tmem);
+  tc_fence_before();
+  plan_start<kManyRows>(p, &sh.plan);  // ends with __syncthreads
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  auto failed = [&] { return *(volatile int*)&sh.failed != 0; };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  if (warp == 8) {
+    // ---- loads
+    unsigned bad = 0;
+    int item = 0, units = 0;  // ring items (a K or a V tile each) and units so far
+    auto publish = [&](const UnitMeta& u) -> bool {
+      const int mi = units & 1;
+      if (units >= 2) wait_or_fail(&sh.meta_empty[mi], ((units >> 1) - 1) & 1, &sh.failed, err);
+      if (__any_sync(0xffffffffu, failed())) return false;
+      if (lane == 0) {
+        sh.meta[mi] = u;
+        mbar_arrive(&sh.meta_full[mi]);
+      }
+      ++units;
+      return true;
+    };
+    bool ok = true;
+    plan_walk<kManyRows>(p, &sh.plan, [&](const UnitMeta& u) -> bool {
+      if (!(ok = publish(u))) return false;
+      auto lookup = [&](int k) {
+        const int place = u.key0 + k * kKeyTile + lane * p.c.page;
+        return k < u.n && lane * p.c.page < kKeyTile && place < u.key_end ? page_of(p, u.seq, place, &bad) : -1;
+      };
+      int next = lookup(0);
+      for (int k = 0; k < u.n; ++k) {
+        const int page = next;
+        next = lookup(k + 1);  // in flight while this tile waits for room
+        const int bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * p.c.page * kHeadDim * 2;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++item) {
+          const int st = item % kRing;
+          if (item >= kRing) wait_or_fail(&sh.kv_empty[st], (item / kRing - 1) & 1, &sh.failed, err);
+          if (__any_sync(0xffffffffu, failed())) return ok = false;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], bytes);
+          __syncwarp();
+          if (page >= 0) {
+            const uint32_t dst = smem_addr(ring + st * kTileBytes) + lane * p.c.page * 128;
+            tma_page(dst, kv ? &vmap : &kmap, &sh.kv_full[st], 0, u.kh, page);
+            tma_page(dst + kPanelBytes, kv ? &vmap : &kmap, &sh.kv_full[st], 64, u.kh, page);
+          }
+        }
+      }
+      return true;
+    });
+    if (ok) {
+      UnitMeta end = {};
+      publish(end);
+    }
+    if (bad) atomicOr(err, bad);
+    // no copy is in flight when the block ends, also where the others gave up
+    for (int i = max(item - kRing, 0); i < item; ++i)
+      if (!mbar_wait_bounded(&sh.kv_full[i % kRing], (i / kRing) & 1)) break;
+  } else if (warp == 9) {
+    // ---- products
+    if (lane == 0) {
+      const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
+      constexpr uint32_t idesc_s = instr_desc<BF16>(false), idesc_o = instr_desc<BF16>(true);
+      int tile0 = 0;             // tiles of earlier units
+      uint32_t pc[2] = {0, 0};   // weights taken from each half
+      for (int unit = 0;; ++unit) {
+        wait_or_fail(&sh.meta_full[unit & 1], (unit >> 1) & 1, &sh.failed, err);
+        if (failed()) break;
+        const int n = sh.meta[unit & 1].n;
+        const bool both = sh.meta[unit & 1].rows > kHalf;
+        mbar_arrive(&sh.meta_empty[unit & 1]);
+        if (n == 0) break;
+        wait_or_fail(&sh.q_full, unit & 1, &sh.failed, err);
+        auto wait_item = [&](int it) { wait_or_fail(&sh.kv_full[it % kRing], (it / kRing) & 1, &sh.failed, err); };
+        auto scores = [&](int s, int tile) {  // S_s = Q K^T, the keys of a tile
+          const uint32_t k_addr = ring_addr + (2 * tile % kRing) * kTileBytes, qa = q_addr + (both ? s : 0) * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = (k >> 2) * kPanelBytes + (k & 3) * 32;
+            tc_mma_ss(tmem + s * 128, smem_desc(qa + off, 16, 1024), smem_desc(k_addr + off, 16, 1024), idesc_s, k > 0);
+          }
+          tc_commit(&sh.s_full[s]);
+        };
+        auto values = [&](int s, int tile, bool acc) {  // O_s += P_s V
+          const uint32_t v_addr = ring_addr + ((2 * tile + 1) % kRing) * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, smem_desc(v_addr + k * 2048, kPanelBytes, 1024), idesc_o,
+                      acc || k > 0);
+        };
+        auto wait_weights = [&](int s) {
+          wait_or_fail(&sh.p_full[s], pc[s] & 1, &sh.failed, err);
+          ++pc[s];
+          tc_fence_after();
+        };
+        tc_fence_after();
+        if (both) {
+          wait_item(2 * tile0);
+          if (failed()) break;
+          scores(0, tile0);
+          scores(1, tile0);
+          tc_commit(&sh.kv_empty[2 * tile0 % kRing]);
+          for (int j = 0; j < n && !failed(); ++j) {
+            const int t = tile0 + j;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              wait_weights(s);
+              if (s == 0) wait_item(2 * t + 1);
+              if (failed()) break;
+              values(s, t, j > 0);
+              if (s == 1) tc_commit(&sh.kv_empty[(2 * t + 1) % kRing]);
+              if (j + 1 < n) {
+                if (s == 0) wait_item(2 * t + 2);
+                if (failed()) break;
+                scores(s, t + 1);
+                if (s == 1) tc_commit(&sh.kv_empty[(2 * t + 2) % kRing]);
+              }
+            }
+          }
+        } else {
+          for (int j = 0; j < min(n, 2); ++j) {
+            wait_item(2 * (tile0 + j));
+            if (failed()) break;
+            scores(j, tile0 + j);
+            tc_commit(&sh.kv_empty[2 * (tile0 + j) % kRing]);
+          }
+          for (int j = 0; j < n && !failed(); ++j) {
+            const int t = tile0 + j, s = j & 1;
+            wait_weights(s);
+            wait_item(2 * t + 1);
+            if (failed()) break;
+            values(s, t, j > 1);
+            tc_commit(&sh.kv_empty[(2 * t + 1) % kRing]);
+            if (j + 2 < n) {
+              wait_item(2 * t + 4);
+              if (failed()) break;
+              scores(s, t + 2);
+              tc_commit(&sh.kv_empty[(2 * t + 4) % kRing]);
+            }
+          }
+        }
+        if (failed()) break;
+        tc_commit(&sh.unit_done);
+        tile0 += n;
+      }
+      // every product has ended before TMEM is given back
+      tc_commit(&sh.drain);
+      mbar_wait_bounded(&sh.drain, 0);
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ---- softmax: half `s`, a row a thread
+    const int s = warp >> 2, t = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of TMEM
+    const uint32_t s_addr = tmem + lanes + s * 128, o_addr = tmem + lanes + 256 + s * 128;
+    int tile0 = 0;
+    uint32_t sc = 0, joins = 0;
+    auto join = [&] {  // the eight softmax warps meet
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.join);
+      wait_or_fail(&sh.join, joins & 1, &sh.failed, err);
+      ++joins;
+      __syncwarp();
+    };
+    for (int unit = 0;; ++unit) {
+      wait_or_fail(&sh.meta_full[unit & 1], (unit >> 1) & 1, &sh.failed, err);
+      __syncwarp();
+      if (__any_sync(0xffffffffu, failed())) break;
+      const UnitMeta m = sh.meta[unit & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.meta_empty[unit & 1]);
+      if (m.n == 0) break;
+      const bool both = m.rows > kHalf;
+      // Q: a half's 128 rows, or each 64 of the one half's; rows behind the unit's are zeros
+      {
+        const int r_base = both ? s * kHalf : 0, q_rows = both ? kHalf : kHalf / 2, q0 = both ? 0 : s * (kHalf / 2);
+        const uint32_t q_tile = smem_addr(smem) + (both ? s : 0) * kTileBytes;
+#pragma unroll 4
+        for (int i = t; i < q_rows * 16; i += kHalf) {
+          const int r = q0 + (i >> 4), ch = i & 15, row = m.row0 + r_base + r;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (r_base + r < m.rows)
+            v = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(m.tok0 + row / p.Gq) * p.qs0 +
+                                                     (long long)(m.kh * p.Gq + row % p.Gq) * p.qs1) + ch);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(panel_addr(q_tile, r, ch)), "r"(v.x), "r"(v.y), "r"(v.z),
+                       "r"(v.w)
+                       : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+      }
+      const int r = (both ? s * kHalf : 0) + t;  // row of the unit
+      const bool live = r < m.rows;
+      const int lim = live ? unit_row_limit(p, m, r) : 0x7fffffff;
+      float ref = 0.f, l = 0.f;  // the maximum in use (in units of log2), the sum
+      bool seen = false;         // whether ref is a maximum yet
+      const int step = both ? 1 : 2;
+      for (int j = both ? 0 : s; j < m.n; j += step) {
+        wait_or_fail(&sh.s_full[s], sc & 1, &sh.failed, err);
+        ++sc;
+        __syncwarp();
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc_ld32(x + 32 * i, s_addr + 32 * i);
+        tc_wait_ld();
+        float* f = reinterpret_cast<float*>(x);
+        const int key0 = m.key0 + j * kKeyTile, seen_here = lim - key0;
+        if (__any_sync(0xffffffffu, seen_here < kKeyTile)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) f[i] = i < seen_here ? f[i] : -INFINITY;
+        }
+        float mx[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+        for (int i = 4; i < 124; i += 8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], f[124 + q]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        // raise the maximum?  O of this half is complete up to the tile before: its product was issued before these scores
+        float alpha = 1.f;
+        if (top > ref + kRaise || (!seen && top != -INFINITY)) {
+          alpha = seen ? ex2f_(ref - top) : 1.f;  // nothing but zeros so far: no factor
+          ref = top;
+          seen = true;
+          l *= alpha;
+        }
+        if (j >= step && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[32];
+            tc_ld32(o, o_addr + 32 * i);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tc_st32(o_addr + 32 * i, o);
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float a = f[64 * h + 2 * i], b = f[64 * h + 2 * i + 1];
+            fma2(a, b, p.scale_log2, -ref);
+            a = ex2f_(a);
+            b = ex2f_(b);
+            add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], a, b);
+            w[i] = pack2<BF16>(a, b);
+          }
+          tc_st32(s_addr + 32 * h, w);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const int valid = m.key_end - key0;
+        if (valid < kKeyTile && (!both || s == 0)) {
+          // the last tile's values behind the last key: 0 * NaN is NaN, so they are zeroed before the product
+          const int vi = 2 * (tile0 + j) + 1;
+          wait_or_fail(&sh.kv_full[vi % kRing], (vi / kRing) & 1, &sh.failed, err);
+          const uint32_t v_tile = smem_addr(ring + (vi % kRing) * kTileBytes);
+          for (int i = t; i < (kKeyTile - valid) * 16; i += kHalf)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(panel_addr(v_tile, valid + (i >> 4), i & 15)), "r"(0)
+                         : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[s]);
+      }
+      // ---- the unit's result
+      wait_or_fail(&sh.unit_done, unit & 1, &sh.failed, err);
+      __syncwarp();
+      tc_fence_after();
+      if (__any_sync(0xffffffffu, failed())) break;
+      const bool joined = !both && m.n > 1;  // two results of the same rows
+      if (!seen) ref = -INFINITY;
+      float4* dump = reinterpret_cast<float4*>(smem);  // [32][128 rows]: Q is free
+      if (joined && s == 1) {
+        sh.ml[t] = make_float2(ref, l);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[32];
+          tc_ld32(o, o_addr + 32 * i);
+          tc_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dump[(8 * i + k) * kHalf + t] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                        __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+        }
+      }
+      if (joined) join();
+      if (both || s == 0) {
+        float fa = 1.f, fb = 0.f, M = ref, L = l;
+        if (joined) {
+          const float2 o = sh.ml[t];
+          M = fmaxf(ref, o.x);
+          const float z = M == -INFINITY ? 0.f : M;
+          fa = ex2f_(ref - z);
+          fb = ex2f_(o.x - z);
+          L = l * fa + o.y * fb;
+        }
+        const int row = m.row0 + r;
+        const long long at = (long long)(m.tok0 + row / p.Gq) * p.Hq + m.kh * p.Gq + row % p.Gq;
+        const long long rec = m.dest == kToRow ? (m.prefix ? 0 : (long long)p.N * p.Hq) + at : (long long)m.dest * p.part.R + r;
+        const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
+        if (live && m.dest != kToOut) (m.dest == kToRow ? p.row_ml : p.part.ml)[rec] = make_float2(M, L);
+        float* const acc = (m.dest == kToRow ? p.row_acc : p.part.acc) + rec * kHeadDim;
+        uint16_t* const out = p.out + at * kHeadDim;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[32];
+          tc_ld32(o, o_addr + 32 * i);
+          tc_wait_ld();
+          float* v = reinterpret_cast<float*>(o);
+          if (joined) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 y = dump[(8 * i + k) * kHalf + t];
+              v[4 * k] = v[4 * k] * fa + y.x * fb;
+              v[4 * k + 1] = v[4 * k + 1] * fa + y.y * fb;
+              v[4 * k + 2] = v[4 * k + 2] * fa + y.z * fb;
+              v[4 * k + 3] = v[4 * k + 3] * fa + y.w * fb;
+            }
+          }
+          if (live) {
+            if (m.dest == kToOut) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(out + 32 * i + 8 * k) =
+                    make_uint4(pack2<BF16>(v[8 * k] * inv, v[8 * k + 1] * inv), pack2<BF16>(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                               pack2<BF16>(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                               pack2<BF16>(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<float4*>(acc + 32 * i + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+        }
+      }
+      if (joined) join();  // the dump has been read: Q may be written again
+      tc_fence_before();
+      tile0 += m.n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tc_dealloc(tmem);
+  grid_dep_wait();
+}
+
+palu_status launch_many(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream) {
+  return bf16 ? launch(paged_many_kernel<true>, p.part.grid, kManyThreads, kManySmemBytes, false, stream,
+                       "paged_many_kernel launch", p, km, vm)
+              : launch(paged_many_kernel<false>, p.part.grid, kManyThreads, kManySmemBytes, false, stream,
+                       "paged_many_kernel launch", p, km, vm);
+}
+
+}  // namespace palu
