@@ -73,20 +73,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     fence_mbar_init();
   }
   plan_start<R>(p, &sh.plan);
-  const int n_tiles = (int)min(sh.plan.w1 - sh.plan.w0, 0x7fffffffLL);
-  if (n_tiles > 0) {
+  if (sh.plan.w1 > sh.plan.w0) {
     if (warp == kFewWarps) {
       // ---- the loading warp
       unsigned bad = 0;
       int it = 0;
+      // room for the next tile: all lanes go on or stop together
+      auto room = [&] {
+        if (it >= kFewStages)
+          wait_or_fail(&sh.empty[it % kFewStages], ((it / kFewStages) - 1) & 1, &sh.failed, p.c.error);
+        return !__any_sync(0xffffffffu, *(volatile int*)&sh.failed);
+      };
       plan_walk<R>(p, &sh.plan, [&](const UnitMeta& u) -> bool {
         for (int k = 0; k < u.n; ++k, ++it) {
           const int st = it % kFewStages, key0 = u.key0 + k * kKeyTile, valid = min(kKeyTile, u.key_end - key0);
           const int pages = (valid + p.c.page - 1) >> p.c.page_shift;
           const int page = lane < pages ? page_of(p, u.seq, key0 + lane * p.c.page, &bad) : 0;
-          if (it >= kFewStages) wait_or_fail(&sh.empty[st], ((it / kFewStages) - 1) & 1, &sh.failed, p.c.error);
-          // all lanes stop together
-          if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) return false;
+          if (!room()) return false;
           if (lane == 0) {
             sh.meta[st] = TileMeta{u, key0, valid, k == 0, k == u.n - 1};
             mbar_arrive_expect_tx(&sh.full[st], pages * p.c.page * kHeadDim * 4);
@@ -102,9 +105,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         return true;
       });
+      const bool ended = room();
+      if (ended && lane == 0) {  // a tile of no keys ends the line
+        sh.meta[it % kFewStages].valid = 0;
+        mbar_arrive(&sh.full[it % kFewStages]);
+      }
       if (bad) atomicOr(p.c.error, bad);
-      // no copy is in flight when the block ends, also where the others gave up
-      for (int k = max(it - kFewStages, 0); k < it; ++k)
+      // no copy is in flight when the block ends, also where the others gave up (the stage that the end took had
+      // been emptied)
+      for (int k = max(it - kFewStages + (ended ? 1 : 0), 0); k < it; ++k)
         if (!mbar_wait_bounded(&sh.full[k % kFewStages], (k / kFewStages) & 1)) break;
     } else {
       // ---- 16 tokens of each tile a warp
@@ -122,11 +131,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ++joins;
         __syncwarp();
       };
-      for (int it = 0; it < n_tiles; ++it) {
+      for (int it = 0;; ++it) {
         const int st = it % kFewStages;
         wait_or_fail(&sh.full[st], (it / kFewStages) & 1, &sh.failed, p.c.error);
+        if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) break;
         const TileMeta& tm = sh.meta[st];
         const int valid = tm.valid, key0 = tm.key0, last = tm.last;
+        if (valid == 0) break;
         if (tm.first) {
           m = tm.u;
 #pragma unroll
@@ -288,114 +299,226 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   grid_dep_wait();
 }
 
-// Joins a row's parts: a warp a row, four channels a lane.  Rows whose unit
-// was complete in one CTA, with no prefix to join, are already in the output.
-struct CombineParams {
+// ---- joining.  Eight warps a CTA: all on one row, every eighth part each, where
+// rows are few and may have up to a part an SM (a single long sequence); else
+// a warp a row, unless a row turns out to have many parts after all.  Lanes hold
+// four channels.  Parts are joined in a fixed order: the result repeats bit
+// for bit.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinFew = 16;       // parts up to which a warp joins alone
+constexpr int kJoinRows = 4096;    // rows up to which each gets a CTA: beyond, parts = SMs * 256 / rows are few
+
+struct JoinScratch {
+  float o[kJoinWarps][kHeadDim];
+  float2 ml[kJoinWarps];
+};
+
+struct Joined {
+  float M, L, o[4];
+};
+
+// Parts k0, k0 + step, ... < n of a row; part(k, &ml, &acc) says where part k lies.
+template <class F>
+__device__ __forceinline__ Joined join_parts(int k0, int n, int step, F&& part) {
+  const int lane = threadIdx.x & 31;
+  Joined j = {-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+  // four parts' loads in flight
+  for (int k = k0; k < n; k += 4 * step) {
+    float2 v[4];
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = make_float2(-INFINITY, 0.f);
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k + i * step < n) {
+        const float2* ml;
+        const float* acc;
+        part(k + i * step, ml, acc);
+        v[i] = __ldcg(ml);
+        x[i] = __ldcg(reinterpret_cast<const float4*>(acc) + lane);
+      }
+    }
+    const float M = fmaxf(fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)), j.M);
+    const float ref = M == -INFINITY ? 0.f : M, a = ex2f_(j.M - ref);
+    j.M = M;
+    j.L *= a;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) j.o[c] *= a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = ex2f_(v[i].x - ref);
+      j.L += v[i].y * f;
+      j.o[0] += x[i].x * f;
+      j.o[1] += x[i].y * f;
+      j.o[2] += x[i].z * f;
+      j.o[3] += x[i].w * f;
+    }
+  }
+  return j;
+}
+
+// All eight warps of the CTA on one row.
+template <class F>
+__device__ __forceinline__ Joined join_parts_cta(JoinScratch* sc, int n, F&& part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Joined mine = join_parts(warp, n, kJoinWarps, part);
+  __syncthreads();  // the row before has been read
+  if (lane == 0) sc->ml[warp] = make_float2(mine.M, mine.L);
+  *reinterpret_cast<float4*>(sc->o[warp] + 4 * lane) = make_float4(mine.o[0], mine.o[1], mine.o[2], mine.o[3]);
+  __syncthreads();
+  Joined j = {-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) j.M = fmaxf(j.M, sc->ml[w].x);
+  const float ref = j.M == -INFINITY ? 0.f : j.M;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = ex2f_(sc->ml[w].x - ref);
+    const float4 x = *reinterpret_cast<const float4*>(sc->o[w] + 4 * lane);
+    j.L += sc->ml[w].y * f;
+    j.o[0] += x.x * f;
+    j.o[1] += x.y * f;
+    j.o[2] += x.z * f;
+    j.o[3] += x.w * f;
+  }
+  return j;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void write_row(uint16_t* out, const Joined& j) {
+  const float inv = j.L > 0.f ? 1.f / j.L : j.L == 0.f ? 0.f : j.L;
+  *reinterpret_cast<uint2*>(out + 4 * (threadIdx.x & 31)) =
+      make_uint2(pack2<BF16>(j.o[0] * inv, j.o[1] * inv), pack2<BF16>(j.o[2] * inv, j.o[3] * inv));
+}
+
+// Without a prefix: CTA (x, y) joins the rows from y * STEP on (STEP 1 or 8 of
+// them) of the unit that attention CTA x began and a later one ended.
+// Everything else is in the output already.
+template <bool BF16, int STEP>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const AttnParams a) {
+  __shared__ JoinScratch sc;
+  const int warp = threadIdx.x >> 5, c = blockIdx.x;
+  grid_dep_wait();
+  const UnitMeta* u = a.part.begun + c;
+  const int rows = __ldcg(&u->rows), r0 = blockIdx.y * STEP;
+  if (r0 >= rows) return;
+  const int n = __ldcg(&u->parts), row0 = __ldcg(&u->row0), tok0 = __ldcg(&u->tok0), kh = __ldcg(&u->kh);
+  const int R = a.part.R;
+  int r = 0;
+  auto part = [&](int k, const float2*& ml, const float*& acc) {
+    const long long rec = (long long)(2 * (c + k) + (k == 0)) * R + r;
+    ml = a.part.ml + rec;
+    acc = a.part.acc + rec * kHeadDim;
+  };
+  auto out = [&] {
+    const int row = row0 + r;
+    return a.out + ((long long)(tok0 + row / a.Gq) * a.Hq + kh * a.Gq + row % a.Gq) * kHeadDim;
+  };
+  if (STEP > 1 && n <= kJoinFew) {
+    r = r0 + warp;
+    if (r < rows) write_row<BF16>(out(), join_parts(0, n, 1, part));
+  } else {
+    for (r = r0; r < min(rows, r0 + STEP); ++r) {
+      const Joined j = join_parts_cta(&sc, n, part);
+      if (warp == 0) write_row<BF16>(out(), j);
+    }
+  }
+}
+
+// With a prefix: every row has a part or more of it, and of its own keys.
+struct JoinRowsParams {
   AttnParams a;
   PartSet prefix, own;
 };
-constexpr int kCombineWarps = 4;
 
-template <bool BF16>
-__global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const CombineParams p) {
+template <int R>
+__device__ __forceinline__ void own_place(const JoinRowsParams& p, const SeqSpan& s, int b, int kh, int lr, long long* f,
+                                          int* n, int* t) {
   const AttnParams& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-  if (row >= (long long)a.N * a.Hq) {
-    grid_dep_wait();
-    return;
-  }
-  const int tok = (int)(row / a.Hq), h = (int)(row - (long long)tok * a.Hq), kh = h / a.Gq, gi = h - kh * a.Gq;
-  // the row's place in the plan does not depend on the attention: only its parts do
-  if (tok >= __ldg(a.offsets + a.c.batch)) {
-    grid_dep_wait();
-    return;
-  }
-  const int b = find_sequence(a.offsets, a.c.batch, tok, lane & 15, (lane & 16) ? 0xffff0000u : 0x0000ffffu);
-  unsigned bad = 0;
-  const SeqSpan s = seq_span(a, b, &bad);
-  const int i = tok - s.tok0;
-  uint16_t* out = a.out + row * kHeadDim;
+  const int rt = lr / R, rows = min(R, s.n * a.Gq - rt * R);
+  *n = own_tiles(s, rt * R, rows, a.Gq, a.S0);
+  *t = LineCost<R>::tile(rows);
+  *f = __ldcg(p.own.plan + 1 + b) + seq_ticks<R>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R>(rows, *n) +
+       LineCost<R>::kUnit;
+}
+template <int R>
+__device__ __forceinline__ void prefix_place(const JoinRowsParams& p, int kh, int lr, long long* f, int* n, int* t) {
+  const AttnParams& a = p.a;
+  const int all_rows = a.N * a.Gq, rts = (all_rows + R - 1) / R, rt = lr / R;
+  *n = prefix_tiles_of(a.S0);
+  *t = LineCost<R>::tile(min(R, all_rows - rt * R));
+  *f = kh * prefix_ticks<R>(all_rows, rts, *n) + prefix_ticks<R>(all_rows, rt, *n) + LineCost<R>::kUnit;
+}
+
+template <bool BF16, int STEP>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const JoinRowsParams p) {
+  __shared__ JoinScratch sc;
+  const AttnParams& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row_first = (long long)blockIdx.x * STEP, rows_all = (long long)a.N * a.Hq;
+  const int end = __ldg(a.offsets + a.c.batch);
   grid_dep_wait();
-  if (i < 0 || i >= s.n) {
-    *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0u, 0u);
-    return;
-  }
-  const int lim = row_limit(s, i);
-  // parts of one kind: CTAs first .. last of its launch hold them, or one record a row does
+  // Where a row's parts lie: CTAs first .. first + n - 1 of the launch that had its unit, or one record of the row.
   struct Parts {
     int first, n, r;
-    bool whole;
-    long long W, u0;
   };
-  auto parts_of = [&](const PartSet& ps, long long u0, int tiles, int r) {
-    Parts q;
-    q.W = __ldcg(ps.plan);
-    q.u0 = u0;
-    q.r = r;
-    q.first = (int)(u0 / q.W);
-    q.n = tiles ? (int)((u0 + tiles - 1) / q.W) - q.first + 1 : 0;
-    q.whole = q.n == 1;
-    return q;
+  struct Row {
+    Parts pre, own;
+    bool live;  // there is something to write
+    long long row;
   };
-  Parts own = {}, pre = {};
-  {
-    const int R = p.own.R, lr = i * a.Gq + gi, rt = lr / R;
-    int tiles = 0;
-    long long u0 = __ldcg(p.own.plan + 1 + b);
-    for (int t = 0; t <= rt; ++t) {
-      const int last = min((t + 1) * R, s.n * a.Gq) - 1, keys = row_limit(s, last / a.Gq) - a.S0;
-      tiles = keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 0;
-      u0 += (long long)tiles * (t < rt ? a.c.kv_heads : kh);
-    }
-    own = parts_of(p.own, u0, tiles, lr - rt * R);
-    if (own.whole && a.S0 == 0) return;
-  }
-  if (a.S0 > 0) {
-    const int R = p.prefix.R, lr = tok * a.Gq + gi, rt = lr / R, rts = (a.N * a.Gq + R - 1) / R;
-    const long long t0 = prefix_tiles_of(a.S0);
-    pre = parts_of(p.prefix, ((long long)kh * rts + rt) * t0, (int)t0, lr - rt * R);
-  }
-  const int n = pre.n + own.n;
-  const float2* ml;
-  const float* ac;
-  auto part = [&](int k) {  // where part k lies
-    const bool is_pre = k < pre.n;
-    const PartSet& ps = is_pre ? p.prefix : p.own;
-    const Parts& q = is_pre ? pre : own;
-    const long long c = q.first + (is_pre ? k : k - pre.n);
-    const long long rec = q.whole ? (is_pre ? 0 : (long long)a.N * a.Hq) + row
-                                  : (2 * c + (c * q.W > q.u0 ? 0 : 1)) * ps.R + q.r;
-    ml = (q.whole ? a.row_ml : ps.ml) + rec;
-    ac = (q.whole ? a.row_acc : ps.acc) + rec * kHeadDim;
+  auto place = [&](long long row) {
+    Row w = {};
+    w.row = row;
+    if (row >= rows_all) return w;
+    const int tok = (int)(row / a.Hq), h = (int)(row - (long long)tok * a.Hq), kh = h / a.Gq, gi = h - kh * a.Gq;
+    if (tok >= end) return w;
+    w.live = true;
+    const int b = find_sequence(a.offsets, a.c.batch, tok, lane & 15, (lane & 16) ? 0xffff0000u : 0x0000ffffu);
+    unsigned bad = 0;
+    const SeqSpan s = seq_span(a, b, &bad);
+    const int i = tok - s.tok0;
+    if (i < 0 || i >= s.n || row_limit(s, i) <= 0) return w;  // no parts: zeros
+    auto parts = [](const PartSet& ps, long long f, int n, int t, int r) {
+      const long long W = __ldcg(ps.plan);
+      const int first = (int)(f / W);
+      return Parts{first, n ? (int)((f + (long long)(n - 1) * t) / W) - first + 1 : 0, r};
+    };
+    long long f;
+    int n, t;
+    const int lr = i * a.Gq + gi, gr = tok * a.Gq + gi;
+    if (p.own.R == 8) own_place<8>(p, s, b, kh, lr, &f, &n, &t);
+    else if (p.own.R == 16) own_place<16>(p, s, b, kh, lr, &f, &n, &t);
+    else own_place<kManyRows>(p, s, b, kh, lr, &f, &n, &t);
+    w.own = parts(p.own, f, n, t, lr % p.own.R);
+    if (p.prefix.R == 8) prefix_place<8>(p, kh, gr, &f, &n, &t);
+    else if (p.prefix.R == 16) prefix_place<16>(p, kh, gr, &f, &n, &t);
+    else prefix_place<kManyRows>(p, kh, gr, &f, &n, &t);
+    w.pre = parts(p.prefix, f, n, t, gr % p.prefix.R);
+    return w;
   };
-  float M = -INFINITY;
-  if (lim > 0) {
-    for (int k = lane; k < n; k += 32) {
-      part(k);
-      M = fmaxf(M, __ldcg(&ml->x));
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  }
-  float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  if (lim > 0 && M != -INFINITY) {
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      part(k);
-      const float2 v = __ldcg(ml);
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(ac) + lane);
-      const float f = ex2f_(v.x - M);
-      L += v.y * f;
-      o[0] += x.x * f;
-      o[1] += x.y * f;
-      o[2] += x.z * f;
-      o[3] += x.w * f;
+  Row w = {};
+  auto part = [&](int k, const float2*& ml, const float*& acc) {
+    const bool pre = k < w.pre.n;
+    const PartSet& ps = pre ? p.prefix : p.own;
+    const Parts& q = pre ? w.pre : w.own;
+    const int c = pre ? k : k - w.pre.n;
+    const bool whole = q.n == 1;
+    const long long rec = whole ? (pre ? 0 : rows_all) + w.row : (long long)(2 * (q.first + c) + (c == 0)) * ps.R + q.r;
+    ml = (whole ? a.row_ml : ps.ml) + rec;
+    acc = (whole ? a.row_acc : ps.acc) + rec * kHeadDim;
+  };
+  if (STEP > 1) {
+    w = place(row_first + warp);
+    if (!__syncthreads_or(w.pre.n + w.own.n > kJoinFew)) {
+      if (w.live) write_row<BF16>(a.out + w.row * kHeadDim, join_parts(0, w.pre.n + w.own.n, 1, part));
+      return;
     }
   }
-  const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
-  *reinterpret_cast<uint2*>(out + 4 * lane) =
-      make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
+  for (int r = 0; r < STEP; ++r) {
+    w = place(row_first + r);
+    const Joined j = join_parts_cta(&sc, w.pre.n + w.own.n, part);
+    if (warp == 0 && w.live) write_row<BF16>(a.out + w.row * kHeadDim, j);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -436,7 +559,7 @@ struct AttnLayout {
   bool shared;       // the prefix is a part of its own
   bool one_launch;   // both parts on the kernel for many rows
   int R_prefix, R_own;
-  size_t plan_p, ml_p, acc_p, plan_o, ml_o, acc_o, row_ml, row_acc, total;
+  size_t plan_p, begun_p, ml_p, acc_p, plan_o, begun_o, ml_o, acc_o, row_ml, row_acc, total;
 };
 
 static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_t q_heads, int32_t max_new,
@@ -464,9 +587,11 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   };
   const bool two = l->shared && !l->one_launch;
   l->plan_p = two ? take(sizeof(long long) * (1 + (size_t)c->batch)) : 0;
+  l->begun_p = two ? take(slots / 2 * sizeof(UnitMeta)) : 0;
   l->ml_p = two ? take(slots * l->R_prefix * sizeof(float2)) : 0;
   l->acc_p = two ? take(slots * l->R_prefix * kHeadDim * sizeof(float)) : 0;
   l->plan_o = take(sizeof(long long) * (1 + (size_t)c->batch));
+  l->begun_o = take(slots / 2 * sizeof(UnitMeta));
   l->ml_o = take(slots * l->R_own * sizeof(float2));
   l->acc_o = take(slots * l->R_own * kHeadDim * sizeof(float));
   l->row_ml = l->shared ? take(2 * (size_t)tokens * q_heads * sizeof(float2)) : 0;
@@ -543,10 +668,11 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
   const int grid = device_sm_count();
   const PartSet own = {reinterpret_cast<float2*>(ws + l.ml_o), reinterpret_cast<float*>(ws + l.acc_o),
-                       reinterpret_cast<long long*>(ws + l.plan_o), grid, l.R_own};
+                       reinterpret_cast<long long*>(ws + l.plan_o), reinterpret_cast<UnitMeta*>(ws + l.begun_o), grid, l.R_own};
   const PartSet prefix = l.one_launch ? own
                                       : PartSet{reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
-                                                reinterpret_cast<long long*>(ws + l.plan_p), grid, l.R_prefix};
+                                                reinterpret_cast<long long*>(ws + l.plan_p), reinterpret_cast<UnitMeta*>(ws + l.begun_p), grid,
+                                                l.R_prefix};
   const bool bf16 = cache->dtype == PALU_TYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (l.shared && !l.one_launch) {
@@ -558,9 +684,28 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   p.do_prefix = l.one_launch;
   p.do_own = 1;
   if ((st = launch_part(p, km, vm, bf16, l.shared && !l.one_launch, s)) != PALU_OK) return st;
-  CombineParams cp = {p, prefix, own};
+  if (!l.shared) {
+    if (l.R_own < kManyRows) {
+      const dim3 jgrid(grid, l.R_own);
+      return bf16 ? launch(paged_join_units_kernel<true, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p)
+                  : launch(paged_join_units_kernel<false, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p);
+    }
+    const dim3 jgrid(grid, l.R_own / kJoinWarps);
+    return bf16 ? launch(paged_join_units_kernel<true, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
+                         "paged_join_units_kernel launch", p)
+                : launch(paged_join_units_kernel<false, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
+                         "paged_join_units_kernel launch", p);
+  }
+  const JoinRowsParams jp = {p, prefix, own};
   const long long rows = (long long)p.N * p.Hq;
-  const int cgrid = (int)((rows + kCombineWarps - 1) / kCombineWarps);
-  return bf16 ? launch(paged_combine_kernel<true>, cgrid, 32 * kCombineWarps, 0, true, s, "paged_combine_kernel launch", cp)
-              : launch(paged_combine_kernel<false>, cgrid, 32 * kCombineWarps, 0, true, s, "paged_combine_kernel launch", cp);
+  if (rows <= kJoinRows)
+    return bf16 ? launch(paged_join_rows_kernel<true, 1>, dim3((unsigned)rows), 32 * kJoinWarps, 0, true, s,
+                         "paged_join_rows_kernel launch", jp)
+                : launch(paged_join_rows_kernel<false, 1>, dim3((unsigned)rows), 32 * kJoinWarps, 0, true, s,
+                         "paged_join_rows_kernel launch", jp);
+  const dim3 jgrid((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
+  return bf16 ? launch(paged_join_rows_kernel<true, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
+                       "paged_join_rows_kernel launch", jp)
+              : launch(paged_join_rows_kernel<false, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
+                       "paged_join_rows_kernel launch", jp);
 }

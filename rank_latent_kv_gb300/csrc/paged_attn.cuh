@@ -11,13 +11,14 @@
 // the kernel that takes them:
 //   prefix units (KV head, row tile): all rows of the batch, keys [0, S0);
 //   own units (sequence, row tile, KV head): keys [S0, the last row's place].
-// Units in this order, each as many 128-key tiles long as its keys are, make
-// one line of tiles; CTA c of a persistent grid takes tiles [c W, (c+1) W) of
-// it, so every SM has the same number of tiles whatever the lengths.  A CTA's
+// Units in this order make one line, measured in ticks: a unit takes a fixed
+// number for its beginning and end, then some for each of its 128-key tiles
+// (LineCost).  CTA c of a persistent grid takes the tiles that begin in
+// [c W, (c+1) W), so every SM has the same work whatever the lengths.  A CTA's
 // stretch begins with at most one unit that an earlier CTA began and ends with
-// at most one that a later CTA ends: two partial results a CTA at most.
-// Units inside are complete: they go straight to the output, or, where the
-// prefix and the own keys have still to be joined, to one record a row each.
+// at most one that a later CTA ends: two partial results a CTA at most.  Units
+// inside are complete: they go straight to the output, or, where the prefix
+// and the own keys have still to be joined, to one record a row each.
 #pragma once
 
 #include <cuda.h>
@@ -30,11 +31,29 @@ constexpr int kKeyTile = 128;
 constexpr int kTileBytes = kKeyTile * kHeadDim * 2;  // 32 KB of keys or values
 constexpr int kPanelBytes = kTileBytes / 2;          // 64 of the 128 channels, rows of 128 swizzled bytes
 
+// A CTA's stretch of a unit: `n` tiles from key0 on, as the loading warp hands
+// it to the others.
+struct UnitMeta {
+  int key0;     // place of the first key
+  int key_end;  // behind the unit's last key (inside the stretch's last tile, or behind it)
+  int n;        // tiles; 0: the line has ended
+  int kh;       // KV head
+  int row0;     // first row of the row tile, among the unit set's rows
+  int rows;     // rows in it
+  int tok0;     // token of row 0 of the set
+  int base;     // own units: the place of the set's first new token
+  int seq;      // row of the page table
+  int prefix;   // a prefix unit: each row's own limit is looked up
+  int dest;     // slot, kToOut or kToRow
+  int parts;    // CTAs that hold a part of the unit, where this is its first one
+};
+
 // Partial results of one kernel launch: 2 slots a CTA, each R rows.
 struct PartSet {
-  float2* ml;      // [2 grid][R] (m, l)
-  float* acc;      // [2 grid][R][128]
-  long long* plan; // [0]: W; [1 + b]: first tile of sequence b's own units
+  float2* ml;       // [2 grid][R] (m, l)
+  float* acc;       // [2 grid][R][128]
+  long long* plan;  // [0]: W; [1 + b]: where sequence b's own units begin
+  UnitMeta* begun;  // [grid]: the unit that CTA c begins and a later one ends (rows 0: none)
   int grid, R;
 };
 
@@ -51,6 +70,21 @@ struct AttnParams {
   int S0;           // shared tokens
   int do_prefix, do_own;
   float scale_log2;
+};
+
+// What a unit costs, in ticks, in the kernel with row tiles of R.
+template <int R>
+struct LineCost {
+  static constexpr int kUnit = 1;
+  static __host__ __device__ int tile(int rows) { return 1; }
+  static constexpr int kMaxTile = 1;
+};
+constexpr int kManyRows = 256;
+template <>
+struct LineCost<kManyRows> {
+  static constexpr int kUnit = 4;
+  static __host__ __device__ int tile(int rows) { return rows > kManyRows / 2 ? 2 : 1; }
+  static constexpr int kMaxTile = 2;
 };
 
 // A sequence's rows and length; n = 0 for one whose offsets make no sense.
@@ -73,47 +107,51 @@ __device__ __forceinline__ SeqSpan seq_span(const AttnParams& p, int b, unsigned
 // Tokens that row r (token r / Gq of the sequence) sees: may be <= 0.
 __device__ __forceinline__ int row_limit(const SeqSpan& s, int token) { return s.len - s.n + token + 1; }
 
-// 128-key tiles of own units in row tile rt.
-template <int R>
-__device__ __forceinline__ int own_tiles(const SeqSpan& s, int rt, int Gq, int S0) {
-  const int last = min((rt + 1) * R, s.n * Gq) - 1;
-  const int keys = row_limit(s, last / Gq) - S0;
+// 128-key tiles of an own unit with rows [row0, row0 + rows) of a sequence.
+__device__ __forceinline__ int own_tiles(const SeqSpan& s, int row0, int rows, int Gq, int S0) {
+  const int keys = row_limit(s, (row0 + rows - 1) / Gq) - S0;
   return keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 0;
 }
 
-// Tiles of all own units of a sequence.
+// Ticks of a unit of n tiles.
 template <int R>
-__device__ __forceinline__ long long seq_tiles(const SeqSpan& s, int Gq, int S0, int kv_heads) {
-  long long t = 0;
-  for (int rt = 0; rt * R < s.n * Gq; ++rt) t += own_tiles<R>(s, rt, Gq, S0);
-  return t * kv_heads;
+__device__ __forceinline__ long long unit_ticks(int rows, int n) {
+  return n ? LineCost<R>::kUnit + (long long)n * LineCost<R>::tile(rows) : 0;
 }
 
-__host__ __device__ inline long long prefix_tiles_of(int S0) { return (S0 + kKeyTile - 1) / kKeyTile; }
+// Ticks of a sequence's own units before row tile `rts`.
+template <int R>
+__device__ __forceinline__ long long seq_ticks(const SeqSpan& s, int rts, int Gq, int S0, int kv_heads) {
+  long long t = 0;
+  for (int rt = 0; rt < rts; ++rt) {
+    const int rows = min(R, s.n * Gq - rt * R);
+    t += unit_ticks<R>(rows, own_tiles(s, rt * R, rows, Gq, S0));
+  }
+  return t * kv_heads;
+}
+template <int R>
+__device__ __forceinline__ long long seq_ticks(const SeqSpan& s, int Gq, int S0, int kv_heads) {
+  return seq_ticks<R>(s, (s.n * Gq + R - 1) / R, Gq, S0, kv_heads);
+}
+
+// Ticks of one KV head's prefix units before row tile `rts` (all: rts row tiles).
+template <int R>
+__device__ __forceinline__ long long prefix_ticks(int all_rows, int rts, int tiles) {
+  const int full = min(rts, all_rows / R);
+  long long t = full * unit_ticks<R>(R, tiles);
+  if (rts > full) t += unit_ticks<R>(all_rows - full * R, tiles);
+  return t;
+}
+
+__host__ __device__ inline int prefix_tiles_of(int S0) { return (S0 + kKeyTile - 1) / kKeyTile; }
 
 // Where a finished unit goes.
 enum { kToOut = -1, kToRow = -2 };
 
-// A CTA's stretch of a unit: `n` tiles from key0 on, as the loading warp hands
-// it to the others.
-struct UnitMeta {
-  int key0;     // place of the first key
-  int key_end;  // behind the unit's last key (inside the stretch's last tile, or behind it)
-  int n;        // tiles; 0: the line has ended
-  int kh;       // KV head
-  int row0;     // first row of the row tile, among the unit set's rows
-  int rows;     // rows in it
-  int tok0;     // token of row 0 of the set
-  int base;     // own units: the place of the set's first new token
-  int seq;      // row of the page table
-  int prefix;   // a prefix unit: each row's own limit is looked up
-  int dest;     // slot, kToOut or kToRow
-};
-
 // The CTA's stretch of the line, found by the whole CTA (blockDim.x threads).
 struct PlanScratch {
   long long warp_sum[16];
-  long long w0, w1, base;
+  long long w0, w1, W, base;
   int b;
 };
 
@@ -121,14 +159,25 @@ template <int R>
 __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc) {
   const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, nwarp = nthr >> 5;
   const int B = p.c.batch, Hkv = p.c.kv_heads;
-  const long long units0 = p.do_prefix ? (long long)Hkv * (((long long)p.N * p.Gq + R - 1) / R) : 0;
-  const long long prefix = units0 * prefix_tiles_of(p.S0);
+  const int all_rows = p.N * p.Gq;
+  const long long prefix =
+      p.do_prefix ? Hkv * prefix_ticks<R>(all_rows, (all_rows + R - 1) / R, prefix_tiles_of(p.S0)) : 0;
   const int per = (B + nthr - 1) / nthr;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   unsigned bad = 0;
   long long mine = 0;
   if (p.do_own)
-    for (int b = b0; b < b1; ++b) mine += seq_tiles<R>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
+    for (int b = b0; b < b1; ++b) {
+      const SeqSpan s = seq_span(p, b, &bad);
+      mine += seq_ticks<R>(s, p.Gq, p.S0, Hkv);
+      // without a prefix nothing joins parts of every row: rows that see nothing are zeroed here
+      if (p.S0 == 0 && b % (int)gridDim.x == (int)blockIdx.x) {
+        const int o0 = max(__ldg(p.offsets + b), 0), o1 = min(__ldg(p.offsets + b + 1), p.N);
+        const int z1 = s.n ? min(o1, o0 + max(s.n - s.len, 0)) : o1;
+        for (long long i = (long long)o0 * p.Hq * (kHeadDim / 8); i < (long long)z1 * p.Hq * (kHeadDim / 8); ++i)
+          reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
   long long incl = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
@@ -144,17 +193,18 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
     total += sc->warp_sum[w];
   }
   before += incl - mine;
-  const long long W = max((total + gridDim.x - 1) / gridDim.x, 1LL);
+  // a stretch is never shorter than a tile, so that every CTA between a unit's first and last holds a part of it
+  const long long W = max((total + gridDim.x - 1) / gridDim.x, (long long)LineCost<R>::kMaxTile);
   const long long w0 = (long long)blockIdx.x * W, w1 = min(w0 + W, total);
   if (p.do_own) {
-    // the thread whose sequences hold the CTA's first own tile walks them; CTA 0 writes the plan down
+    // the thread whose sequences hold the CTA's first own tick walks them; CTA 0 writes the plan down
     const long long at = max(w0, prefix);
     const bool here = at < w1 && at >= before && at < before + mine;
     if (here || blockIdx.x == 0) {
       long long base = before;
       for (int b = b0; b < b1; ++b) {
         if (blockIdx.x == 0) p.part.plan[1 + b] = base;
-        const long long t = seq_tiles<R>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
+        const long long t = seq_ticks<R>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
         if (here && at >= base && at < base + t) {
           sc->b = b;
           sc->base = base;
@@ -167,68 +217,80 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
   if (tid == 0) {
     sc->w0 = w0;
     sc->w1 = w1;
+    sc->W = W;
     if (blockIdx.x == 0) p.part.plan[0] = W;
+    p.part.begun[blockIdx.x].rows = 0;
   }
   __syncthreads();
 }
 
-// Calls unit(meta) for each unit that the CTA's stretch of the line touches, in
-// order, until it returns false: run by one warp, all its lanes.
+// Calls unit(meta) for each unit of which the CTA's stretch of the line has
+// tiles, in order, until it returns false: run by one warp, all its lanes.
 template <int R, class F>
 __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch* sc, F&& unit) {
   const int Hkv = p.c.kv_heads;
-  const long long w1 = sc->w1;
-  long long pos = sc->w0;
-  const int tiles0 = (int)prefix_tiles_of(p.S0);
-  const int all_rows = p.N * p.Gq;
-  const int rts = (all_rows + R - 1) / R;
-  const long long prefix = p.do_prefix ? (long long)Hkv * rts * tiles0 : 0;
+  const long long w0 = sc->w0, w1 = sc->w1;
   const int cta = blockIdx.x;
-  UnitMeta m;
-  // the unit [u0, u0 + n) and the stretch of it that starts at pos
+  UnitMeta m = {};
+  // the tiles of a unit [u0, u0 + ticks) that begin in [w0, w1)
   auto run_unit = [&](long long u0, int n, int key_base, int key_end) -> bool {
-    const int k0 = (int)(pos - u0);
-    const int k1 = (int)min((long long)n, k0 + (w1 - pos));
+    const int t = LineCost<R>::tile(m.rows);
+    const long long f = u0 + LineCost<R>::kUnit;
+    auto before = [&](long long x) { return x <= f ? 0 : (int)min((long long)n, (x - f + t - 1) / t); };
+    const int k0 = before(w0), k1 = before(w1);
+    if (k0 == k1) return true;
     m.dest = k0 > 0 ? 2 * cta : k1 < n ? 2 * cta + 1 : p.S0 > 0 ? kToRow : kToOut;
     m.key0 = key_base + k0 * kKeyTile;
     m.key_end = key_end;
     m.n = k1 - k0;
-    pos += m.n;
+    if (m.dest == 2 * cta + 1) {
+      m.parts = (int)((f + (long long)(n - 1) * t) / sc->W) - cta + 1;
+      if ((threadIdx.x & 31) == 0) p.part.begun[cta] = m;
+    }
     return unit(m);
   };
-  while (pos < w1 && pos < prefix) {
-    const int u = (int)(pos / tiles0);
-    m.kh = u / rts;
-    const int rt = u - m.kh * rts;
-    m.row0 = rt * R;
-    m.rows = min(R, all_rows - m.row0);
+  long long base = 0;
+  if (p.do_prefix) {
+    const int all_rows = p.N * p.Gq, rts = (all_rows + R - 1) / R, tiles = prefix_tiles_of(p.S0);
+    const long long head = prefix_ticks<R>(all_rows, rts, tiles), full = unit_ticks<R>(R, tiles);
     m.tok0 = m.base = m.seq = 0;
     m.prefix = 1;
-    if (!run_unit((long long)u * tiles0, tiles0, 0, p.S0)) return;
+    if (w0 < head * Hkv) {
+      m.kh = (int)(w0 / head);
+      int rt = (int)min((w0 - m.kh * head) / full, (long long)rts - 1);
+      for (; m.kh < Hkv; ++m.kh, rt = 0)
+        for (; rt < rts; ++rt) {
+          const long long u0 = m.kh * head + rt * full;
+          if (u0 >= w1) return;
+          m.row0 = rt * R;
+          m.rows = min(R, all_rows - m.row0);
+          if (!run_unit(u0, tiles, 0, p.S0)) return;
+        }
+    }
   }
-  if (!p.do_own || pos >= w1) return;
-  long long base = sc->base;
+  if (!p.do_own || sc->b < 0) return;
+  base = sc->base;
   unsigned bad = 0;
-  for (int b = sc->b; b >= 0 && b < p.c.batch && pos < w1; ++b) {
+  for (int b = sc->b; b < p.c.batch; ++b) {
     const SeqSpan s = seq_span(p, b, &bad);
     m.tok0 = s.tok0;
     m.base = s.len - s.n;
     m.seq = b;
     m.prefix = 0;
     for (int rt = 0; rt * R < s.n * p.Gq; ++rt) {
-      const int n = own_tiles<R>(s, rt, p.Gq, p.S0);
-      if (!n) continue;
-      if (pos >= base + (long long)n * Hkv) {
-        base += (long long)n * Hkv;
-        continue;
-      }
       m.row0 = rt * R;
       m.rows = min(R, s.n * p.Gq - m.row0);
+      const int n = own_tiles(s, m.row0, m.rows, p.Gq, p.S0);
+      if (!n) continue;
+      const long long ticks = unit_ticks<R>(m.rows, n);
       const int end = row_limit(s, (m.row0 + m.rows - 1) / p.Gq);
-      for (m.kh = (int)((pos - base) / n); m.kh < Hkv && pos < w1; ++m.kh)
-        if (!run_unit(base + (long long)m.kh * n, n, p.S0, end)) return;
-      base += (long long)n * Hkv;
-      if (pos >= w1) return;
+      m.kh = w0 > base ? (int)min((w0 - base) / ticks, (long long)Hkv) : 0;
+      for (; m.kh < Hkv; ++m.kh) {
+        const long long u0 = base + m.kh * ticks;
+        if (u0 >= w1) return;
+        if (!run_unit(u0, n, p.S0, end)) return;
+      }
+      base += ticks * Hkv;
     }
   }
 }
@@ -288,7 +350,7 @@ __device__ __forceinline__ void wait_or_fail(uint64_t* bar, uint32_t parity, int
 // A launch; `dependent`: it may begin while the one before it on the stream still
 // runs, and waits for it inside.
 template <class K, class... Args>
-palu_status launch(K kernel, int grid, int threads, int smem, bool dependent, cudaStream_t stream, const char* what,
+palu_status launch(K kernel, dim3 grid, int threads, int smem, bool dependent, cudaStream_t stream, const char* what,
                           Args... args) {
   int per_sm = 0;
   palu_status st = kernel_occupancy(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
@@ -297,7 +359,7 @@ palu_status launch(K kernel, int grid, int threads, int smem, bool dependent, cu
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -307,7 +369,6 @@ palu_status launch(K kernel, int grid, int threads, int smem, bool dependent, cu
 }
 
 // The kernel for many rows (paged_many.cu).
-constexpr int kManyRows = 256;
 palu_status launch_many(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 
 }  // namespace palu

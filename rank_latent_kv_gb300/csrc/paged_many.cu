@@ -16,8 +16,7 @@
 //   overwrite their S as 16-bit pairs and enter the second product from there.
 //   Shared memory: Q0 Q1 (32 KB each), a ring of five 32 KB tiles that holds
 //   K and V of successive key tiles in turn.
-//   Warps 0-3, 4-7: the halves' softmax; warp 8: loads; warp 9: products;
-//   warps 10, 11 fill the third warpgroup and do nothing.
+//   Warps 0-3, 4-7: the halves' softmax; warp 8: loads; warp 9: products.
 //
 // The running maximum is raised only when it grows by more than 2^8 (the
 // weights then stay below 2^8, far inside fp16): the accumulator in TMEM is
@@ -30,20 +29,16 @@
 
 namespace palu {
 
-// Twelve warps launch with 168 registers a thread, 3 * 168 = 504 a lane of the
-// three warpgroups; the softmax warpgroups, which hold a row of 128 scores,
-// then take 208 each and leave 88 to the third (208 + 208 + 88 = 504).
-constexpr int kManyThreads = 384;
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kManyThreads = 320;
 constexpr int kRing = 5;
 constexpr int kHalf = 128;
+constexpr int kStageBytes = 32 * 36 * 4;  // a warp's 32 rows of 32 columns, padded against bank conflicts
 
 struct ManySmem {
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t meta_full[2], meta_empty[2];
   uint64_t q_full, s_full[2], p_full[2], unit_done, join, drain;
   UnitMeta meta[2];
-  float2 ml[kHalf];  // second half's (m, l) when the halves are joined
   PlanScratch plan;
   uint32_t tmem;
   int failed;
@@ -61,6 +56,15 @@ __device__ __forceinline__ void tc_dealloc(uint32_t t) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// One lane of a converged warp.  Products and commits are issued under it by a warp whose control flow is uniform:
+// under a branch on the lane number the compiler has to assume several lanes, and a product took 110 clocks to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -91,17 +95,36 @@ __device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tc_ld16(uint32_t* r, uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+// The loads before it have arrived: r passes through, so that nothing that uses it moves in front.
+__device__ __forceinline__ void tc_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+  tc_wait_ld16(r);
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: byte offsets between
@@ -170,8 +193,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const uint32_t tmem = sh.tmem;
   auto failed = [&] { return *(volatile int*)&sh.failed != 0; };
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == 8) {
     // ---- loads
     unsigned bad = 0;
@@ -225,99 +246,105 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (!mbar_wait_bounded(&sh.kv_full[i % kRing], (i / kRing) & 1)) break;
   } else if (warp == 9) {
     // ---- products
-    if (lane == 0) {
-      const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
-      constexpr uint32_t idesc_s = instr_desc<BF16>(false), idesc_o = instr_desc<BF16>(true);
-      int tile0 = 0;             // tiles of earlier units
-      uint32_t pc[2] = {0, 0};   // weights taken from each half
-      for (int unit = 0;; ++unit) {
-        wait_or_fail(&sh.meta_full[unit & 1], (unit >> 1) & 1, &sh.failed, err);
-        if (failed()) break;
-        const int n = sh.meta[unit & 1].n;
-        const bool both = sh.meta[unit & 1].rows > kHalf;
-        mbar_arrive(&sh.meta_empty[unit & 1]);
-        if (n == 0) break;
-        wait_or_fail(&sh.q_full, unit & 1, &sh.failed, err);
-        auto wait_item = [&](int it) { wait_or_fail(&sh.kv_full[it % kRing], (it / kRing) & 1, &sh.failed, err); };
-        auto scores = [&](int s, int tile) {  // S_s = Q K^T, the keys of a tile
-          const uint32_t k_addr = ring_addr + (2 * tile % kRing) * kTileBytes, qa = q_addr + (both ? s : 0) * kTileBytes;
+    const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
+    constexpr uint32_t idesc_s = instr_desc<BF16>(false), idesc_o = instr_desc<BF16>(true);
+    // all lanes wait and see the same outcome, so the control flow is uniform
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      wait_or_fail(bar, parity, &sh.failed, err);
+      return __any_sync(0xffffffffu, failed()) == 0;
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+    };
+    int tile0 = 0;            // tiles of earlier units
+    uint32_t pc[2] = {0, 0};  // weights taken from each half
+    for (int unit = 0;; ++unit) {
+      if (!wait(&sh.meta_full[unit & 1], (unit >> 1) & 1)) break;
+      const int n = sh.meta[unit & 1].n;
+      const bool both = sh.meta[unit & 1].rows > kHalf;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.meta_empty[unit & 1]);
+      if (n == 0 || !wait(&sh.q_full, unit & 1)) break;
+      tc_fence_after();
+      auto wait_item = [&](int it) { return wait(&sh.kv_full[it % kRing], (it / kRing) & 1); };
+      auto scores = [&](int s, int tile) {  // S_s = Q K^T, the keys of a tile
+        const uint32_t k_addr = ring_addr + (2 * tile % kRing) * kTileBytes, qa = q_addr + (both ? s : 0) * kTileBytes;
+        const uint64_t da = smem_desc(qa, 16, 1024), db = smem_desc(k_addr, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * kPanelBytes + (k & 3) * 32;
-            tc_mma_ss(tmem + s * 128, smem_desc(qa + off, 16, 1024), smem_desc(k_addr + off, 16, 1024), idesc_s, k > 0);
+            const uint32_t off = ((k >> 2) * kPanelBytes + (k & 3) * 32) >> 4;
+            tc_mma_ss(tmem + s * 128, da + off, db + off, idesc_s, k > 0);
           }
           tc_commit(&sh.s_full[s]);
-        };
-        auto values = [&](int s, int tile, bool acc) {  // O_s += P_s V
-          const uint32_t v_addr = ring_addr + ((2 * tile + 1) % kRing) * kTileBytes;
+        }
+        __syncwarp();
+      };
+      auto values = [&](int s, int tile, bool acc) {  // O_s += P_s V
+        const uint64_t db = smem_desc(ring_addr + ((2 * tile + 1) % kRing) * kTileBytes, kPanelBytes, 1024);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, smem_desc(v_addr + k * 2048, kPanelBytes, 1024), idesc_o,
-                      acc || k > 0);
-        };
-        auto wait_weights = [&](int s) {
-          wait_or_fail(&sh.p_full[s], pc[s] & 1, &sh.failed, err);
-          ++pc[s];
-          tc_fence_after();
-        };
+            tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, db + (k * 2048 >> 4), idesc_o, acc || k > 0);
+        }
+        __syncwarp();
+      };
+      auto wait_weights = [&](int s) {
+        const bool ok = wait(&sh.p_full[s], pc[s] & 1);
+        ++pc[s];
         tc_fence_after();
-        if (both) {
-          wait_item(2 * tile0);
-          if (failed()) break;
-          scores(0, tile0);
-          scores(1, tile0);
-          tc_commit(&sh.kv_empty[2 * tile0 % kRing]);
-          for (int j = 0; j < n && !failed(); ++j) {
-            const int t = tile0 + j;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              wait_weights(s);
-              if (s == 0) wait_item(2 * t + 1);
-              if (failed()) break;
-              values(s, t, j > 0);
-              if (s == 1) tc_commit(&sh.kv_empty[(2 * t + 1) % kRing]);
-              if (j + 1 < n) {
-                if (s == 0) wait_item(2 * t + 2);
-                if (failed()) break;
-                scores(s, t + 1);
-                if (s == 1) tc_commit(&sh.kv_empty[(2 * t + 2) % kRing]);
-              }
-            }
+        return ok;
+      };
+      bool ok = true;
+      if (both) {
+        ok = wait_item(2 * tile0);
+        if (!ok) break;
+        scores(0, tile0);
+        scores(1, tile0);
+        commit(&sh.kv_empty[2 * tile0 % kRing]);
+        for (int j = 0; j < n && ok; ++j) {
+          const int t = tile0 + j;
+          if (!(ok = wait_weights(0) && wait_item(2 * t + 1))) break;
+          values(0, t, j > 0);
+          if (j + 1 < n) {
+            if (!(ok = wait_item(2 * t + 2))) break;
+            scores(0, t + 1);
           }
-        } else {
-          for (int j = 0; j < min(n, 2); ++j) {
-            wait_item(2 * (tile0 + j));
-            if (failed()) break;
-            scores(j, tile0 + j);
-            tc_commit(&sh.kv_empty[2 * (tile0 + j) % kRing]);
-          }
-          for (int j = 0; j < n && !failed(); ++j) {
-            const int t = tile0 + j, s = j & 1;
-            wait_weights(s);
-            wait_item(2 * t + 1);
-            if (failed()) break;
-            values(s, t, j > 1);
-            tc_commit(&sh.kv_empty[(2 * t + 1) % kRing]);
-            if (j + 2 < n) {
-              wait_item(2 * t + 4);
-              if (failed()) break;
-              scores(s, t + 2);
-              tc_commit(&sh.kv_empty[(2 * t + 4) % kRing]);
-            }
+          if (!(ok = wait_weights(1))) break;
+          values(1, t, j > 0);
+          commit(&sh.kv_empty[(2 * t + 1) % kRing]);
+          if (j + 1 < n) {
+            scores(1, t + 1);
+            commit(&sh.kv_empty[(2 * t + 2) % kRing]);
           }
         }
-        if (failed()) break;
-        tc_commit(&sh.unit_done);
-        tile0 += n;
+      } else {
+        for (int j = 0; j < min(n, 2); ++j) {
+          if (!(ok = wait_item(2 * (tile0 + j)))) break;
+          scores(j, tile0 + j);
+          commit(&sh.kv_empty[2 * (tile0 + j) % kRing]);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int t = tile0 + j, s = j & 1;
+          if (!(ok = wait_weights(s) && wait_item(2 * t + 1))) break;
+          values(s, t, j > 1);
+          commit(&sh.kv_empty[(2 * t + 1) % kRing]);
+          if (j + 2 < n) {
+            if (!(ok = wait_item(2 * t + 4))) break;
+            scores(s, t + 2);
+            commit(&sh.kv_empty[(2 * t + 4) % kRing]);
+          }
+        }
       }
-      // every product has ended before TMEM is given back
-      tc_commit(&sh.drain);
-      mbar_wait_bounded(&sh.drain, 0);
+      if (!ok) break;
+      commit(&sh.unit_done);
+      tile0 += n;
     }
-    __syncwarp();
-  }
+    // every product has ended before TMEM is given back
+    commit(&sh.drain);
+    mbar_wait_bounded(&sh.drain, 0);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ---- softmax: half `s`, a row a thread
     const int s = warp >> 2, t = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of TMEM
@@ -335,26 +362,25 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       wait_or_fail(&sh.meta_full[unit & 1], (unit >> 1) & 1, &sh.failed, err);
       __syncwarp();
       if (__any_sync(0xffffffffu, failed())) break;
-      const UnitMeta m = sh.meta[unit & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.meta_empty[unit & 1]);
+      const UnitMeta& m = sh.meta[unit & 1];
       if (m.n == 0) break;
       const bool both = m.rows > kHalf;
       // Q: a half's 128 rows, or each 64 of the one half's; rows behind the unit's are zeros
       {
         const int r_base = both ? s * kHalf : 0, q_rows = both ? kHalf : kHalf / 2, q0 = both ? 0 : s * (kHalf / 2);
         const uint32_t q_tile = smem_addr(smem) + (both ? s : 0) * kTileBytes;
-#pragma unroll 4
         for (int i = t; i < q_rows * 16; i += kHalf) {
           const int r = q0 + (i >> 4), ch = i & 15, row = m.row0 + r_base + r;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (r_base + r < m.rows)
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(m.tok0 + row / p.Gq) * p.qs0 +
-                                                     (long long)(m.kh * p.Gq + row % p.Gq) * p.qs1) + ch);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(panel_addr(q_tile, r, ch)), "r"(v.x), "r"(v.y), "r"(v.z),
-                       "r"(v.w)
+          const bool there = r_base + r < m.rows;
+          const uint16_t* src = p.q + (there ? (long long)(m.tok0 + row / p.Gq) * p.qs0 +
+                                                   (long long)(m.kh * p.Gq + row % p.Gq) * p.qs1 + ch * 8
+                                             : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(panel_addr(q_tile, r, ch)), "l"(src),
+                       "r"(there ? 16 : 0)
                        : "memory");
         }
+        cp_async_commit();
+        cp_async_wait<0>();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
@@ -370,24 +396,31 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ++sc;
         __syncwarp();
         tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc_ld32(x + 32 * i, s_addr + 32 * i);
-        tc_wait_ld();
-        float* f = reinterpret_cast<float*>(x);
+        // The scores are read twice, 32 at a time (the next 32 on their way meanwhile), once for the maximum and once
+        // for the weights: held in registers in between, 128 a thread, they spilled, and with shared memory as large
+        // as it is here a spilled register comes back from L2 (11,000 clocks a tile instead of about 2,000).
+        uint32_t x[2][32];
         const int key0 = m.key0 + j * kKeyTile, seen_here = lim - key0;
-        if (__any_sync(0xffffffffu, seen_here < kKeyTile)) {
+        const bool cut = __any_sync(0xffffffffu, seen_here < kKeyTile);
+        auto masked = [&](uint32_t* r, int c) {
+          float* f = reinterpret_cast<float*>(r);
 #pragma unroll
-          for (int i = 0; i < 128; ++i) f[i] = i < seen_here ? f[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) f[i] = 32 * c + i < seen_here ? f[i] : -INFINITY;
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tc_ld32(x[0], s_addr);
+        tc_wait_ld(x[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tc_ld32(x[(c + 1) & 1], s_addr + (32 * (c + 1) & 127));  // behind the last: the first again
+          if (cut) masked(x[c & 1], c);
+          const float* f = reinterpret_cast<const float*>(x[c & 1]);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
+          tc_wait_ld(x[(c + 1) & 1]);
         }
-        float mx[4] = {f[0], f[1], f[2], f[3]};
-#pragma unroll
-        for (int i = 4; i < 124; i += 8) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], f[124 + q]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         // raise the maximum?  O of this half is complete up to the tile before: its product was issued before these scores
         float alpha = 1.f;
@@ -398,30 +431,34 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           l *= alpha;
         }
         if (j >= step && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[16];
+            tc_ld16(o, o_addr + 16 * i);
+            tc_wait_ld16(o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[32];
-            tc_ld32(o, o_addr + 32 * i);
-            tc_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tc_st32(o_addr + 32 * i, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tc_st16(o_addr + 16 * i, o);
           }
         }
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int c = 0; c < 4; ++c) {
+          if (c < 3) tc_ld32(x[(c + 1) & 1], s_addr + 32 * (c + 1));
+          if (cut) masked(x[c & 1], c);
+          float* f = reinterpret_cast<float*>(x[c & 1]);
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float a = f[64 * h + 2 * i], b = f[64 * h + 2 * i + 1];
+          for (int i = 0; i < 16; ++i) {
+            float a = f[2 * i], b = f[2 * i + 1];
             fma2(a, b, p.scale_log2, -ref);
             a = ex2f_(a);
             b = ex2f_(b);
             add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], a, b);
             w[i] = pack2<BF16>(a, b);
           }
-          tc_st32(s_addr + 32 * h, w);
+          if (c < 3) tc_wait_ld(x[(c + 1) & 1]);
+          tc_st16(s_addr + 16 * c, w);  // into columns whose scores have been read
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         const int valid = m.key_end - key0;
@@ -445,75 +482,96 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       __syncwarp();
       tc_fence_after();
       if (__any_sync(0xffffffffu, failed())) break;
-      const bool joined = !both && m.n > 1;  // two results of the same rows
+      // A unit of up to 128 rows has an accumulator of even and one of odd tiles (if it had more than one), in the
+      // same lanes of TMEM; the halves exchange their maxima and sums and each takes 64 columns of the joined rows.
+      // Of a larger unit each half has its own rows.  A warp turns 32 columns of its 32 rows around in shared memory
+      // (Q is free), so that it stores whole lines.
       if (!seen) ref = -INFINITY;
-      float4* dump = reinterpret_cast<float4*>(smem);  // [32][128 rows]: Q is free
-      if (joined && s == 1) {
-        sh.ml[t] = make_float2(ref, l);
+      float2(*const ml)[kHalf] = reinterpret_cast<float2(*)[kHalf]>(smem + 8 * kStageBytes);  // behind the staging areas
+      float fa = 1.f, fb = 0.f;
+      if (!both) {
+        ml[s][t] = make_float2(ref, l);
+        join();
+        if (m.n > 1) {
+          const float2 o0 = ml[0][t], o1 = ml[1][t];
+          ref = fmaxf(o0.x, o1.x);
+          const float z = ref == -INFINITY ? 0.f : ref;
+          fa = ex2f_(o0.x - z);
+          fb = ex2f_(o1.x - z);
+          l = o0.y * fa + o1.y * fb;
+        } else {
+          ref = ml[0][t].x;
+          l = ml[0][t].y;
+        }
+      }
+      const uint32_t o0_addr = tmem + lanes + 256 + (both ? s * 128 : 0);
+      auto place = [&](int rr) {  // of row rr of the unit
+        const int row = m.row0 + rr;
+        return (long long)(m.tok0 + row / p.Gq) * p.Hq + m.kh * p.Gq + row % p.Gq;
+      };
+      const int dest = m.dest;
+      const long long set = dest == kToRow ? (m.prefix ? 0 : (long long)p.N * p.Hq) : 0;
+      if (dest != kToOut && live && (both || s == 0)) {
+        float2* to = dest == kToRow ? p.row_ml + set + place(r) : p.part.ml + (long long)dest * p.part.R + r;
+        *to = make_float2(ref, l);
+      }
+      const float inv = dest != kToOut ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+      fa *= inv;
+      fb *= inv;
+      float* const stage = reinterpret_cast<float*>(smem + warp * kStageBytes);
+      const int r_warp = (both ? s * kHalf : 0) + 32 * (warp & 3);  // first of the warp's rows
+#pragma unroll 1
+      for (int c = both ? 0 : 64 * s; c < (both ? 128 : 64 * s + 64); c += 32) {
+        uint32_t o[32];
+        float* v = reinterpret_cast<float*>(o);
+        tc_ld32(o, o0_addr + c);
+        tc_wait_ld(o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          tc_ld32(o, o_addr + 32 * i);
-          tc_wait_ld();
+        for (int k = 0; k < 32; ++k) v[k] *= fa;
+        if (!both && m.n > 1) {
+          uint32_t y[32];
+          tc_ld32(y, o0_addr + 128 + c);
+          tc_wait_ld(y);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = fmaf(__uint_as_float(y[k]), fb, v[k]);
+        }
+        __syncwarp();
+        if (dest == kToOut) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(stage + lane * 20 + 4 * k) =
+                make_uint4(pack2<BF16>(v[8 * k], v[8 * k + 1]), pack2<BF16>(v[8 * k + 2], v[8 * k + 3]),
+                           pack2<BF16>(v[8 * k + 4], v[8 * k + 5]), pack2<BF16>(v[8 * k + 6], v[8 * k + 7]));
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // 4 lanes a row
+            const int rr = 8 * k + (lane >> 2);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 20 + 4 * (lane & 3));
+            if (r_warp + rr < m.rows)
+              *reinterpret_cast<uint4*>(p.out + place(r_warp + rr) * kHeadDim + c + 8 * (lane & 3)) = x;
+          }
+        } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            dump[(8 * i + k) * kHalf + t] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                        __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-        }
-      }
-      if (joined) join();
-      if (both || s == 0) {
-        float fa = 1.f, fb = 0.f, M = ref, L = l;
-        if (joined) {
-          const float2 o = sh.ml[t];
-          M = fmaxf(ref, o.x);
-          const float z = M == -INFINITY ? 0.f : M;
-          fa = ex2f_(ref - z);
-          fb = ex2f_(o.x - z);
-          L = l * fa + o.y * fb;
-        }
-        const int row = m.row0 + r;
-        const long long at = (long long)(m.tok0 + row / p.Gq) * p.Hq + m.kh * p.Gq + row % p.Gq;
-        const long long rec = m.dest == kToRow ? (m.prefix ? 0 : (long long)p.N * p.Hq) + at : (long long)m.dest * p.part.R + r;
-        const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
-        if (live && m.dest != kToOut) (m.dest == kToRow ? p.row_ml : p.part.ml)[rec] = make_float2(M, L);
-        float* const acc = (m.dest == kToRow ? p.row_acc : p.part.acc) + rec * kHeadDim;
-        uint16_t* const out = p.out + at * kHeadDim;
+            *reinterpret_cast<float4*>(stage + lane * 36 + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          tc_ld32(o, o_addr + 32 * i);
-          tc_wait_ld();
-          float* v = reinterpret_cast<float*>(o);
-          if (joined) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 y = dump[(8 * i + k) * kHalf + t];
-              v[4 * k] = v[4 * k] * fa + y.x * fb;
-              v[4 * k + 1] = v[4 * k + 1] * fa + y.y * fb;
-              v[4 * k + 2] = v[4 * k + 2] * fa + y.z * fb;
-              v[4 * k + 3] = v[4 * k + 3] * fa + y.w * fb;
-            }
-          }
-          if (live) {
-            if (m.dest == kToOut) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(out + 32 * i + 8 * k) =
-                    make_uint4(pack2<BF16>(v[8 * k] * inv, v[8 * k + 1] * inv), pack2<BF16>(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                               pack2<BF16>(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
-                               pack2<BF16>(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<float4*>(acc + 32 * i + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          for (int k = 0; k < 8; ++k) {  // 8 lanes a row
+            const int rr = 4 * k + (lane >> 3);
+            const float4 x = *reinterpret_cast<const float4*>(stage + rr * 36 + 4 * (lane & 7));
+            if (r_warp + rr < m.rows) {
+              float* acc = dest == kToRow ? p.row_acc + (set + place(r_warp + rr)) * kHeadDim
+                                          : p.part.acc + ((long long)dest * p.part.R + r_warp + rr) * kHeadDim;
+              *reinterpret_cast<float4*>(acc + c + 4 * (lane & 7)) = x;
             }
           }
         }
       }
-      if (joined) join();  // the dump has been read: Q may be written again
+      join();  // the staging areas have been read: Q may be written again
       tc_fence_before();
       tile0 += m.n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.meta_empty[unit & 1]);
     }
   }
   tc_fence_before();
