@@ -340,11 +340,12 @@ __device__ __forceinline__ uint32_t panel_addr(uint32_t tile, int row, int ch) {
 // A wait that gives up sets the error word, and `failed` for the block: every
 // role then runs on to its end without waiting (what it computes is void).
 __device__ __forceinline__ void wait_or_fail(uint64_t* bar, uint32_t parity, int* failed, unsigned* error) {
-  if (*(volatile int*)failed) return;
-  if (!mbar_wait_bounded(bar, parity)) {
-    *(volatile int*)failed = 1;
-    atomicOr(error, PALU_DEVERR_TIMEOUT);
+  if (mbar_try_wait(bar, parity)) return;
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (*(volatile int*)failed || mbar_try_wait(bar, parity)) return;
   }
+  *(volatile int*)failed = 1;
+  atomicOr(error, PALU_DEVERR_TIMEOUT);
 }
 
 // A launch; `dependent`: it may begin while the one before it on the stream still

@@ -12,11 +12,20 @@
 // 128 rows gives its even tiles to one half and its odd tiles to the other, and
 // the two results are joined at the end.
 //
-//   TMEM (512 columns): S0 S1 O0 O1, 128 fp32 columns each; the weights P
-//   overwrite their S as 16-bit pairs and enter the second product from there.
+//   TMEM (512 columns): S0 S1 O0 O1, 128 fp32 columns each.  The weights P
+//   overwrite their scores as 16-bit pairs and enter the second product from
+//   there, 64 keys as soon as they are ready: the chain scores - maximum -
+//   weights - values of a half is the bound here (two halves take turns), and
+//   this way half of its exponentials overlap with the product.  (Two score
+//   buffers of 64 keys a half would break the chain, but a product 128 x 64 x 16
+//   from shared memory takes the 64 clocks of one 128 x 128 x 16: measured
+//   3,950 clocks a tile pair against a floor of 2,048.)
 //   Shared memory: Q0 Q1 (32 KB each), a ring of five 32 KB tiles that holds
 //   K and V of successive key tiles in turn.
-//   Warps 0-3, 4-7: the halves' softmax; warp 8: loads; warp 9: products.
+//   Warps 0-3, 4-7: the halves' softmax; warp 8: loads; warps 9, 10: the
+//   halves' products.  (The tensor cores take a product only when they are
+//   nearly done with those before it, so a warp that issues for both halves
+//   leaves them idle whenever it waits: 3,250 clocks a tile pair.)
 //
 // The running maximum is raised only when it grows by more than 2^8 (the
 // weights then stay below 2^8, far inside fp16): the accumulator in TMEM is
@@ -29,7 +38,7 @@
 
 namespace palu {
 
-constexpr int kManyThreads = 320;
+constexpr int kManyThreads = 352;
 constexpr int kRing = 5;
 constexpr int kHalf = 128;
 constexpr int kStageBytes = 32 * 36 * 4;  // a warp's 32 rows of 32 columns, padded against bank conflicts
@@ -37,7 +46,7 @@ constexpr int kStageBytes = 32 * 36 * 4;  // a warp's 32 rows of 32 columns, pad
 struct ManySmem {
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t meta_full[2], meta_empty[2];
-  uint64_t q_full, s_full[2], p_full[2], unit_done, join, drain;
+  uint64_t q_full, s_full[2], p_full[2][2], unit_done, join, drain[2], token[2];
   UnitMeta meta[2];
   PlanScratch plan;
   uint32_t tmem;
@@ -125,6 +134,16 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: byte offsets between
@@ -139,7 +158,11 @@ __device__ constexpr uint32_t instr_desc(bool b_n_major) {
   return 1u << 4 | (BF16 ? 1u << 7 | 1u << 10 : 0u) | (b_n_major ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ void fma2(float& x, float& y, float s, float c) {  // (x, y) <- (x, y) s + c
   uint64_t v, ss, cc;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
@@ -171,18 +194,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 1);
+      mbar_init(&sh.kv_empty[i], 2);  // both halves, or one of them twice
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.meta_full[i], 1);
-      mbar_init(&sh.meta_empty[i], 9);  // eight softmax warps, the product warp
+      mbar_init(&sh.meta_empty[i], 10);  // eight softmax warps, two product warps
+      mbar_init(&sh.drain[i], 1);
+      mbar_init(&sh.token[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i][0], 4);
+      mbar_init(&sh.p_full[i][1], 4);
     }
     mbar_init(&sh.q_full, 8);
-    mbar_init(&sh.unit_done, 1);
+    mbar_init(&sh.unit_done, 2);
     mbar_init(&sh.join, 8);
-    mbar_init(&sh.drain, 1);
+    mbar_arrive(&sh.token[0]);  // half 0 has the first turn
     sh.failed = 0;
     fence_mbar_init();
   }
@@ -244,12 +270,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // no copy is in flight when the block ends, also where the others gave up
     for (int i = max(item - kRing, 0); i < item; ++i)
       if (!mbar_wait_bounded(&sh.kv_full[i % kRing], (i / kRing) & 1)) break;
-  } else if (warp == 9) {
-    // ---- products
+  } else if (warp >= 9) {
+    // ---- products of half s
+    const int s = warp - 9;
     const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
     constexpr uint32_t idesc_s = instr_desc<BF16>(false), idesc_o = instr_desc<BF16>(true);
     // all lanes wait and see the same outcome, so the control flow is uniform
     auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       wait_or_fail(bar, parity, &sh.failed, err);
       return __any_sync(0xffffffffu, failed()) == 0;
     };
@@ -258,7 +286,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       __syncwarp();
     };
     int tile0 = 0;            // tiles of earlier units
-    uint32_t pc[2] = {0, 0};  // weights taken from each half
+    uint32_t pc = 0, turns = 0;  // tiles of weights taken; turns had
     for (int unit = 0;; ++unit) {
       if (!wait(&sh.meta_full[unit & 1], (unit >> 1) & 1)) break;
       const int n = sh.meta[unit & 1].n;
@@ -268,9 +296,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (n == 0 || !wait(&sh.q_full, unit & 1)) break;
       tc_fence_after();
       auto wait_item = [&](int it) { return wait(&sh.kv_full[it % kRing], (it / kRing) & 1); };
-      auto scores = [&](int s, int tile) {  // S_s = Q K^T, the keys of a tile
-        const uint32_t k_addr = ring_addr + (2 * tile % kRing) * kTileBytes, qa = q_addr + (both ? s : 0) * kTileBytes;
-        const uint64_t da = smem_desc(qa, 16, 1024), db = smem_desc(k_addr, 16, 1024);
+      const uint32_t qa = q_addr + (both ? s : 0) * kTileBytes;
+      auto scores = [&](int tile) {  // S = Q K^T, the keys of a tile
+        const uint64_t da = smem_desc(qa, 16, 1024), db = smem_desc(ring_addr + (2 * tile % kRing) * kTileBytes, 16, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -281,60 +309,52 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         __syncwarp();
       };
-      auto values = [&](int s, int tile, bool acc) {  // O_s += P_s V
-        const uint64_t db = smem_desc(ring_addr + ((2 * tile + 1) % kRing) * kTileBytes, kPanelBytes, 1024);
+      auto values = [&](int u, int tile, bool acc) {  // O += P_u V, 64 keys of a tile
+        const uint64_t db = smem_desc(ring_addr + ((2 * tile + 1) % kRing) * kTileBytes + u * 8192, kPanelBytes, 1024);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, db + (k * 2048 >> 4), idesc_o, acc || k > 0);
+          for (int k = 0; k < 4; ++k)
+            tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + u * 32 + k * 8, db + (k * 2048 >> 4), idesc_o, acc || k > 0);
         }
         __syncwarp();
       };
-      auto wait_weights = [&](int s) {
-        const bool ok = wait(&sh.p_full[s], pc[s] & 1);
-        ++pc[s];
-        tc_fence_after();
-        return ok;
+      auto release = [&](int it) {  // the half's arrival, or both where a tile is one half's alone
+        if (elect_one()) {
+          tc_commit(&sh.kv_empty[it % kRing]);
+          if (!both) tc_commit(&sh.kv_empty[it % kRing]);
+        }
+        __syncwarp();
       };
+      const int step = both ? 1 : 2, j0 = both ? 0 : s;
       bool ok = true;
-      if (both) {
-        ok = wait_item(2 * tile0);
-        if (!ok) break;
-        scores(0, tile0);
-        scores(1, tile0);
-        commit(&sh.kv_empty[2 * tile0 % kRing]);
-        for (int j = 0; j < n && ok; ++j) {
-          const int t = tile0 + j;
-          if (!(ok = wait_weights(0) && wait_item(2 * t + 1))) break;
-          values(0, t, j > 0);
-          if (j + 1 < n) {
-            if (!(ok = wait_item(2 * t + 2))) break;
-            scores(0, t + 1);
+      if (j0 < n) {
+        if (!wait_item(2 * (tile0 + j0))) break;
+        scores(tile0 + j0);
+        release(2 * (tile0 + j0));
+      }
+      for (int j = j0; j < n; j += step) {
+        const int t = tile0 + j;
+        if (!(ok = wait_item(2 * t + 1) && wait(&sh.p_full[s][0], pc & 1))) break;
+        tc_fence_after();
+        values(0, t, j >= step);
+        const bool more = j + step < n;
+        // The halves take turns with their last values and next scores: left to themselves they fall into step, both in
+        // the softmax and then both waiting for the tensor cores (3,900 clocks a tile pair).
+        if (more && !(ok = wait_item(2 * (t + step)) && (!both || wait(&sh.token[s], turns & 1)))) break;
+        if (!(ok = wait(&sh.p_full[s][1], pc & 1))) break;
+        tc_fence_after();
+        values(1, t, true);
+        ++pc;
+        if (more) {
+          scores(t + step);
+          if (both) {
+            if (lane == 0) mbar_arrive(&sh.token[1 - s]);
+            ++turns;
           }
-          if (!(ok = wait_weights(1))) break;
-          values(1, t, j > 0);
-          commit(&sh.kv_empty[(2 * t + 1) % kRing]);
-          if (j + 1 < n) {
-            scores(1, t + 1);
-            commit(&sh.kv_empty[(2 * t + 2) % kRing]);
-          }
-        }
-      } else {
-        for (int j = 0; j < min(n, 2); ++j) {
-          if (!(ok = wait_item(2 * (tile0 + j)))) break;
-          scores(j, tile0 + j);
-          commit(&sh.kv_empty[2 * (tile0 + j) % kRing]);
-        }
-        for (int j = 0; j < n && ok; ++j) {
-          const int t = tile0 + j, s = j & 1;
-          if (!(ok = wait_weights(s) && wait_item(2 * t + 1))) break;
-          values(s, t, j > 1);
-          commit(&sh.kv_empty[(2 * t + 1) % kRing]);
-          if (j + 2 < n) {
-            if (!(ok = wait_item(2 * t + 4))) break;
-            scores(s, t + 2);
-            commit(&sh.kv_empty[(2 * t + 4) % kRing]);
-          }
+          release(2 * t + 1);
+          release(2 * (t + step));
+        } else {
+          release(2 * t + 1);
         }
       }
       if (!ok) break;
@@ -342,8 +362,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       tile0 += n;
     }
     // every product has ended before TMEM is given back
-    commit(&sh.drain);
-    mbar_wait_bounded(&sh.drain, 0);
+    commit(&sh.drain[s]);
+    mbar_wait_bounded(&sh.drain[s], 0);
   } else {
     // ---- softmax: half `s`, a row a thread
     const int s = warp >> 2, t = tid & 127;
@@ -391,37 +411,57 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       float ref = 0.f, l = 0.f;  // the maximum in use (in units of log2), the sum
       bool seen = false;         // whether ref is a maximum yet
       const int step = both ? 1 : 2;
-      for (int j = both ? 0 : s; j < m.n; j += step) {
+      for (int j = both ? 0 : s; j < m.n; j += step, ++sc) {
+        const int tile_key = m.key0 + j * kKeyTile, valid = m.key_end - tile_key;
+        if (valid < kKeyTile) {
+          // the last tile's values behind the last key: 0 * NaN is NaN, so they are zeroed before the product (by both
+          // halves, where both use them)
+          const int vi = 2 * (tile0 + j) + 1;
+          wait_or_fail(&sh.kv_full[vi % kRing], (vi / kRing) & 1, &sh.failed, err);
+          const uint32_t v_tile = smem_addr(ring + (vi % kRing) * kTileBytes);
+          for (int i = t; i < (kKeyTile - valid) * 16; i += kHalf)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(panel_addr(v_tile, valid + (i >> 4), i & 15)), "r"(0)
+                         : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
         wait_or_fail(&sh.s_full[s], sc & 1, &sh.failed, err);
-        ++sc;
         __syncwarp();
         tc_fence_after();
-        // The scores are read twice, 32 at a time (the next 32 on their way meanwhile), once for the maximum and once
-        // for the weights: held in registers in between, 128 a thread, they spilled, and with shared memory as large
-        // as it is here a spilled register comes back from L2 (11,000 clocks a tile instead of about 2,000).
-        uint32_t x[2][32];
-        const int key0 = m.key0 + j * kKeyTile, seen_here = lim - key0;
+        // The scores of the first 64 keys stay in registers; those of the others pass through twice, for the maximum and
+        // for the weights (a thread with all 128 spills).
+        uint32_t x[64], y[32], w[32];
+        const int seen_here = lim - tile_key;
         const bool cut = __any_sync(0xffffffffu, seen_here < kKeyTile);
-        auto masked = [&](uint32_t* r, int c) {
+        auto masked = [&](uint32_t* r, int c, int n) {
           float* f = reinterpret_cast<float*>(r);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = 32 * c + i < seen_here ? f[i] : -INFINITY;
+          for (int i = 0; i < n; ++i) f[i] = c + i < seen_here ? f[i] : -INFINITY;
         };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tc_ld32(x[0], s_addr);
-        tc_wait_ld(x[0]);
+        auto max_of = [&](const uint32_t* r, int n) {
+          const float* f = reinterpret_cast<const float*>(r);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc_ld32(x[(c + 1) & 1], s_addr + (32 * (c + 1) & 127));  // behind the last: the first again
-          if (cut) masked(x[c & 1], c);
-          const float* f = reinterpret_cast<const float*>(x[c & 1]);
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
+          for (int i = 0; i < n; i += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
-          tc_wait_ld(x[(c + 1) & 1]);
+        };
+        tc_ld32(x, s_addr);
+        tc_ld32(x + 32, s_addr + 32);
+        tc_wait_ld(x);
+        tc_wait_ld(x + 32);
+        tc_ld32(y, s_addr + 64);
+        tc_ld32(w, s_addr + 96);
+        if (cut) masked(x, 0, 64);
+        max_of(x, 64);
+        tc_wait_ld(y);
+        tc_wait_ld(w);
+        if (cut) {
+          masked(y, 64, 32);
+          masked(w, 96, 32);
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        max_of(y, 32);
+        max_of(w, 32);
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * p.scale_log2;
         // raise the maximum?  O of this half is complete up to the tile before: its product was issued before these scores
         float alpha = 1.f;
         if (top > ref + kRaise || (!seen && top != -INFINITY)) {
@@ -430,7 +470,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           seen = true;
           l *= alpha;
         }
-        if (j >= step && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             uint32_t o[16];
@@ -442,40 +482,36 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
         }
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        auto weights = [&](uint32_t* r, int n, uint32_t* out) {
+          float* f = reinterpret_cast<float*>(r);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) tc_ld32(x[(c + 1) & 1], s_addr + 32 * (c + 1));
-          if (cut) masked(x[c & 1], c);
-          float* f = reinterpret_cast<float*>(x[c & 1]);
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < n / 2; ++i) {
             float a = f[2 * i], b = f[2 * i + 1];
             fma2(a, b, p.scale_log2, -ref);
             a = ex2f_(a);
             b = ex2f_(b);
             add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], a, b);
-            w[i] = pack2<BF16>(a, b);
+            out[i] = pack2<BF16>(a, b);
           }
-          if (c < 3) tc_wait_ld(x[(c + 1) & 1]);
-          tc_st16(s_addr + 16 * c, w);  // into columns whose scores have been read
-        }
+        };
+        auto publish = [&](int u) {
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[s][u]);
+        };
+        weights(x, 64, w);
+        tc_st32(s_addr, w);
+        publish(0);
+        tc_ld32(x, s_addr + 64);
+        tc_ld32(x + 32, s_addr + 96);
+        tc_wait_ld(x);
+        tc_wait_ld(x + 32);
+        if (cut) masked(x, 64, 64);
+        weights(x, 64, w);
+        tc_st32(s_addr + 32, w);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        const int valid = m.key_end - key0;
-        if (valid < kKeyTile && (!both || s == 0)) {
-          // the last tile's values behind the last key: 0 * NaN is NaN, so they are zeroed before the product
-          const int vi = 2 * (tile0 + j) + 1;
-          wait_or_fail(&sh.kv_full[vi % kRing], (vi / kRing) & 1, &sh.failed, err);
-          const uint32_t v_tile = smem_addr(ring + (vi % kRing) * kTileBytes);
-          for (int i = t; i < (kKeyTile - valid) * 16; i += kHalf)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(panel_addr(v_tile, valid + (i >> 4), i & 15)), "r"(0)
-                         : "memory");
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[s]);
+        publish(1);
       }
       // ---- the unit's result
       wait_or_fail(&sh.unit_done, unit & 1, &sh.failed, err);
