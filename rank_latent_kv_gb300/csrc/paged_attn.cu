@@ -143,9 +143,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const int rg = nt * 8 + g;
-            const int row = m.row0 + rg;
-            const uint16_t* qh = p.q + (long long)(m.tok0 + row / p.Gq) * p.qs0 +
-                                 (long long)(m.kh * p.Gq + row % p.Gq) * p.qs1;
+            const uint16_t* qh = row_query(p, m, rg);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
               qb[nt][ks][0] = rg < m.rows ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
@@ -275,8 +273,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[i] += x[4 * lane + i] * f;
               }
-              const int row = m.row0 + r;
-              const long long at = (long long)(m.tok0 + row / p.Gq) * p.Hq + m.kh * p.Gq + row % p.Gq;
+              const long long at = row_index(p, m, r);
               if (m.dest == kToOut) {
                 const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
                 uint2 v = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
@@ -305,8 +302,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // four channels.  Parts are joined in a fixed order: the result repeats bit
 // for bit.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinFew = 16;       // parts up to which a warp joins alone
-constexpr int kJoinRows = 4096;    // rows up to which each gets a CTA: beyond, parts = SMs * 256 / rows are few
+constexpr int kJoinFew = 64;       // parts up to which a warp joins alone
+constexpr int kJoinRows = 256;     // rows up to which each gets a CTA
 
 struct JoinScratch {
   float o[kJoinWarps][kHeadDim];
@@ -322,12 +319,13 @@ template <class F>
 __device__ __forceinline__ Joined join_parts(int k0, int n, int step, F&& part) {
   const int lane = threadIdx.x & 31;
   Joined j = {-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
-  // four parts' loads in flight
-  for (int k = k0; k < n; k += 4 * step) {
-    float2 v[4];
-    float4 x[4];
+  // eight parts' loads in flight
+  constexpr int U = 8;
+  for (int k = k0; k < n; k += U * step) {
+    float2 v[U];
+    float4 x[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < U; ++i) {
       v[i] = make_float2(-INFINITY, 0.f);
       x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k + i * step < n) {
@@ -338,14 +336,16 @@ __device__ __forceinline__ Joined join_parts(int k0, int n, int step, F&& part) 
         x[i] = __ldcg(reinterpret_cast<const float4*>(acc) + lane);
       }
     }
-    const float M = fmaxf(fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)), j.M);
+    float M = j.M;
+#pragma unroll
+    for (int i = 0; i < U; ++i) M = fmaxf(M, v[i].x);
     const float ref = M == -INFINITY ? 0.f : M, a = ex2f_(j.M - ref);
     j.M = M;
     j.L *= a;
 #pragma unroll
     for (int c = 0; c < 4; ++c) j.o[c] *= a;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < U; ++i) {
       const float f = ex2f_(v[i].x - ref);
       j.L += v[i].y * f;
       j.o[0] += x[i].x * f;
@@ -401,7 +401,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const
   const UnitMeta* u = a.part.begun + c;
   const int rows = __ldcg(&u->rows), r0 = blockIdx.y * STEP;
   if (r0 >= rows) return;
-  const int n = __ldcg(&u->parts), row0 = __ldcg(&u->row0), tok0 = __ldcg(&u->tok0), kh = __ldcg(&u->kh);
+  const int n = __ldcg(&u->parts);
+  UnitMeta m = {};
+  m.tok = __ldcg(&u->tok);
+  m.g0 = __ldcg(&u->g0);
+  m.kh = __ldcg(&u->kh);
   const int R = a.part.R;
   int r = 0;
   auto part = [&](int k, const float2*& ml, const float*& acc) {
@@ -409,10 +413,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const
     ml = a.part.ml + rec;
     acc = a.part.acc + rec * kHeadDim;
   };
-  auto out = [&] {
-    const int row = row0 + r;
-    return a.out + ((long long)(tok0 + row / a.Gq) * a.Hq + kh * a.Gq + row % a.Gq) * kHeadDim;
-  };
+  auto out = [&] { return a.out + row_index(a, m, r) * kHeadDim; };
   if (STEP > 1 && n <= kJoinFew) {
     r = r0 + warp;
     if (r < rows) write_row<BF16>(out(), join_parts(0, n, 1, part));
@@ -438,15 +439,16 @@ __device__ __forceinline__ void own_place(const JoinRowsParams& p, const SeqSpan
   *n = own_tiles(s, rt * R, rows, a.Gq, a.S0);
   *t = LineCost<R>::tile(rows);
   *f = __ldcg(p.own.plan + 1 + b) + seq_ticks<R>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R>(rows, *n) +
-       LineCost<R>::kUnit;
+       LineCost<R>::unit(rows);
 }
 template <int R>
 __device__ __forceinline__ void prefix_place(const JoinRowsParams& p, int kh, int lr, long long* f, int* n, int* t) {
   const AttnParams& a = p.a;
   const int all_rows = a.N * a.Gq, rts = (all_rows + R - 1) / R, rt = lr / R;
   *n = prefix_tiles_of(a.S0);
-  *t = LineCost<R>::tile(min(R, all_rows - rt * R));
-  *f = kh * prefix_ticks<R>(all_rows, rts, *n) + prefix_ticks<R>(all_rows, rt, *n) + LineCost<R>::kUnit;
+  const int rows = min(R, all_rows - rt * R);
+  *t = LineCost<R>::tile(rows);
+  *f = kh * prefix_ticks<R>(all_rows, rts, *n) + prefix_ticks<R>(all_rows, rt, *n) + LineCost<R>::unit(rows);
 }
 
 template <bool BF16, int STEP>
@@ -455,8 +457,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
   const AttnParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row_first = (long long)blockIdx.x * STEP, rows_all = (long long)a.N * a.Hq;
-  const int end = __ldg(a.offsets + a.c.batch);
-  grid_dep_wait();
   // Where a row's parts lie: CTAs first .. first + n - 1 of the launch that had its unit, or one record of the row.
   struct Parts {
     int first, n, r;
@@ -465,19 +465,31 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     Parts pre, own;
     bool live;  // there is something to write
     long long row;
+    int b, i, kh, gi;  // i < 0: it sees nothing
+    SeqSpan s;
   };
-  auto place = [&](long long row) {
+  const int end = __ldg(a.offsets + a.c.batch);
+  auto find = [&](long long row) {  // from the call's inputs alone
     Row w = {};
     w.row = row;
+    w.i = -1;
     if (row >= rows_all) return w;
-    const int tok = (int)(row / a.Hq), h = (int)(row - (long long)tok * a.Hq), kh = h / a.Gq, gi = h - kh * a.Gq;
+    const int tok = (int)(row / a.Hq), h = (int)(row - (long long)tok * a.Hq);
     if (tok >= end) return w;
     w.live = true;
-    const int b = find_sequence(a.offsets, a.c.batch, tok, lane & 15, (lane & 16) ? 0xffff0000u : 0x0000ffffu);
+    w.kh = h / a.Gq;
+    w.gi = h - w.kh * a.Gq;
+    w.b = find_sequence(a.offsets, a.c.batch, tok, lane & 15, (lane & 16) ? 0xffff0000u : 0x0000ffffu);
     unsigned bad = 0;
-    const SeqSpan s = seq_span(a, b, &bad);
-    const int i = tok - s.tok0;
-    if (i < 0 || i >= s.n || row_limit(s, i) <= 0) return w;  // no parts: zeros
+    w.s = seq_span(a, w.b, &bad);
+    const int i = tok - w.s.tok0;
+    if (i >= 0 && i < w.s.n && row_limit(w.s, i) > 0) w.i = i;
+    return w;
+  };
+  auto place = [&](Row& w) {  // from the attention's plan
+    if (w.i < 0) return;
+    const SeqSpan& s = w.s;
+    const int b = w.b, kh = w.kh, gi = w.gi, i = w.i, tok = s.tok0 + i;
     auto parts = [](const PartSet& ps, long long f, int n, int t, int r) {
       const long long W = __ldcg(ps.plan);
       const int first = (int)(f / W);
@@ -494,9 +506,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     else if (p.prefix.R == 16) prefix_place<16>(p, kh, gr, &f, &n, &t);
     else prefix_place<kManyRows>(p, kh, gr, &f, &n, &t);
     w.pre = parts(p.prefix, f, n, t, gr % p.prefix.R);
-    return w;
   };
-  Row w = {};
+  Row w = find(row_first + (STEP > 1 ? warp : 0));
+  grid_dep_wait();
   auto part = [&](int k, const float2*& ml, const float*& acc) {
     const bool pre = k < w.pre.n;
     const PartSet& ps = pre ? p.prefix : p.own;
@@ -508,14 +520,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     acc = (whole ? a.row_acc : ps.acc) + rec * kHeadDim;
   };
   if (STEP > 1) {
-    w = place(row_first + warp);
+    place(w);
     if (!__syncthreads_or(w.pre.n + w.own.n > kJoinFew)) {
       if (w.live) write_row<BF16>(a.out + w.row * kHeadDim, join_parts(0, w.pre.n + w.own.n, 1, part));
       return;
     }
   }
   for (int r = 0; r < STEP; ++r) {
-    w = place(row_first + r);
+    if (STEP > 1) w = find(row_first + r);
+    place(w);
     const Joined j = join_parts_cta(&sc, w.pre.n + w.own.n, part);
     if (warp == 0 && w.live) write_row<BF16>(a.out + w.row * kHeadDim, j);
   }
@@ -664,6 +677,7 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   p.max_new = max_new;
   p.Hq = q_heads;
   p.Gq = q_heads / cache->kv_heads;
+  p.gq_mul = (65536 + p.Gq - 1) / p.Gq;
   p.S0 = l.shared ? shared_pages * cache->page_size : 0;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
   const int grid = device_sm_count();

@@ -38,10 +38,10 @@ struct UnitMeta {
   int key_end;  // behind the unit's last key (inside the stretch's last tile, or behind it)
   int n;        // tiles; 0: the line has ended
   int kh;       // KV head
-  int row0;     // first row of the row tile, among the unit set's rows
-  int rows;     // rows in it
-  int tok0;     // token of row 0 of the set
-  int base;     // own units: the place of the set's first new token
+  int rows;     // rows of the row tile
+  int tok;      // token of its first row, and that row's query head in the group
+  int g0;
+  int pos;      // own units: the place of that token
   int seq;      // row of the page table
   int prefix;   // a prefix unit: each row's own limit is looked up
   int dest;     // slot, kToOut or kToRow
@@ -67,25 +67,48 @@ struct AttnParams {
   float* row_acc;   // [2][N Hq][128]
   PartSet part;
   int N, max_new, Hq, Gq;
+  int gq_mul;       // ceil(2^16 / Gq)
   int S0;           // shared tokens
   int do_prefix, do_own;
   float scale_log2;
 };
 
-// What a unit costs, in ticks, in the kernel with row tiles of R.
+// What a unit costs, in ticks, in the kernel with row tiles of R: to begin and
+// end it, and a 128-key tile of it.
 template <int R>
 struct LineCost {
-  static constexpr int kUnit = 1;
-  static __host__ __device__ int tile(int rows) { return 1; }
+  static __device__ int unit(int rows) { return 2; }
+  static __device__ int tile(int rows) { return 1; }
   static constexpr int kMaxTile = 1;
 };
+// Measured in units of 850 clocks: 1520 units of 256 rows and 4 tiles take
+// 34,000 clocks each, of 40 rows and 1 or 4 tiles 15,000 and 22,600; a tile of 256
+// rows in a long unit 3,400.
 constexpr int kManyRows = 256;
 template <>
 struct LineCost<kManyRows> {
-  static constexpr int kUnit = 4;
-  static __host__ __device__ int tile(int rows) { return rows > kManyRows / 2 ? 2 : 1; }
-  static constexpr int kMaxTile = 2;
+  static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 24 : 15; }
+  static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 4 : 3; }
+  static constexpr int kMaxTile = 4;
 };
+
+// Row r (of a unit) -> token and query head, r < 256: g0 + r < 320 and Gq <= 64,
+// for which the multiplication is exact (320 * 64 < 2^16).
+__device__ __forceinline__ void row_place(const AttnParams& p, const UnitMeta& m, int r, int* tok, int* head) {
+  const int x = m.g0 + r, t = (x * p.gq_mul) >> 16;
+  *tok = m.tok + t;
+  *head = m.kh * p.Gq + x - t * p.Gq;
+}
+__device__ __forceinline__ long long row_index(const AttnParams& p, const UnitMeta& m, int r) {
+  int tok, head;
+  row_place(p, m, r, &tok, &head);
+  return (long long)tok * p.Hq + head;
+}
+__device__ __forceinline__ const uint16_t* row_query(const AttnParams& p, const UnitMeta& m, int r) {
+  int tok, head;
+  row_place(p, m, r, &tok, &head);
+  return p.q + tok * p.qs0 + head * p.qs1;
+}
 
 // A sequence's rows and length; n = 0 for one whose offsets make no sense.
 struct SeqSpan {
@@ -116,7 +139,7 @@ __device__ __forceinline__ int own_tiles(const SeqSpan& s, int row0, int rows, i
 // Ticks of a unit of n tiles.
 template <int R>
 __device__ __forceinline__ long long unit_ticks(int rows, int n) {
-  return n ? LineCost<R>::kUnit + (long long)n * LineCost<R>::tile(rows) : 0;
+  return n ? LineCost<R>::unit(rows) + (long long)n * LineCost<R>::tile(rows) : 0;
 }
 
 // Ticks of a sequence's own units before row tile `rts`.
@@ -235,7 +258,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
   // the tiles of a unit [u0, u0 + ticks) that begin in [w0, w1)
   auto run_unit = [&](long long u0, int n, int key_base, int key_end) -> bool {
     const int t = LineCost<R>::tile(m.rows);
-    const long long f = u0 + LineCost<R>::kUnit;
+    const long long f = u0 + LineCost<R>::unit(m.rows);
     auto before = [&](long long x) { return x <= f ? 0 : (int)min((long long)n, (x - f + t - 1) / t); };
     const int k0 = before(w0), k1 = before(w1);
     if (k0 == k1) return true;
@@ -253,7 +276,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
   if (p.do_prefix) {
     const int all_rows = p.N * p.Gq, rts = (all_rows + R - 1) / R, tiles = prefix_tiles_of(p.S0);
     const long long head = prefix_ticks<R>(all_rows, rts, tiles), full = unit_ticks<R>(R, tiles);
-    m.tok0 = m.base = m.seq = 0;
+    m.pos = m.seq = 0;
     m.prefix = 1;
     if (w0 < head * Hkv) {
       m.kh = (int)(w0 / head);
@@ -262,8 +285,9 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
         for (; rt < rts; ++rt) {
           const long long u0 = m.kh * head + rt * full;
           if (u0 >= w1) return;
-          m.row0 = rt * R;
-          m.rows = min(R, all_rows - m.row0);
+          m.rows = min(R, all_rows - rt * R);
+          m.tok = rt * R / p.Gq;
+          m.g0 = rt * R - m.tok * p.Gq;
           if (!run_unit(u0, tiles, 0, p.S0)) return;
         }
     }
@@ -273,17 +297,17 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
   unsigned bad = 0;
   for (int b = sc->b; b < p.c.batch; ++b) {
     const SeqSpan s = seq_span(p, b, &bad);
-    m.tok0 = s.tok0;
-    m.base = s.len - s.n;
     m.seq = b;
     m.prefix = 0;
     for (int rt = 0; rt * R < s.n * p.Gq; ++rt) {
-      m.row0 = rt * R;
-      m.rows = min(R, s.n * p.Gq - m.row0);
-      const int n = own_tiles(s, m.row0, m.rows, p.Gq, p.S0);
+      m.rows = min(R, s.n * p.Gq - rt * R);
+      const int n = own_tiles(s, rt * R, m.rows, p.Gq, p.S0);
       if (!n) continue;
       const long long ticks = unit_ticks<R>(m.rows, n);
-      const int end = row_limit(s, (m.row0 + m.rows - 1) / p.Gq);
+      const int end = row_limit(s, (rt * R + m.rows - 1) / p.Gq), i = rt * R / p.Gq;
+      m.tok = s.tok0 + i;
+      m.g0 = rt * R - i * p.Gq;
+      m.pos = s.len - s.n + i;
       m.kh = w0 > base ? (int)min((w0 - base) / ticks, (long long)Hkv) : 0;
       for (; m.kh < Hkv; ++m.kh) {
         const long long u0 = base + m.kh * ticks;
@@ -297,9 +321,10 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
 
 // The limit of a row of the unit: how many of the sequence's tokens it sees.
 __device__ __forceinline__ int unit_row_limit(const AttnParams& p, const UnitMeta& m, int r) {
-  const int tok = (m.row0 + r) / p.Gq;
-  if (!m.prefix) return m.base + tok + 1;
-  // token numbers of the whole call: the row's sequence
+  int tok, head;
+  row_place(p, m, r, &tok, &head);
+  if (!m.prefix) return m.pos + (tok - m.tok) + 1;
+  // the row's sequence
   int lo = 0, hi = p.c.batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;

@@ -236,6 +236,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     };
     bool ok = true;
     plan_walk<kManyRows>(p, &sh.plan, [&](const UnitMeta& u) -> bool {
+      // the unit's queries are on their way to L2 while the unit before it is worked on
+      for (int r = lane; r < u.rows; r += 32) {
+        const uint16_t* q = row_query(p, u, r);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+      }
       if (!(ok = publish(u))) return false;
       auto lookup = [&](int k) {
         const int place = u.key0 + k * kKeyTile + lane * p.c.page;
@@ -390,11 +396,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         const int r_base = both ? s * kHalf : 0, q_rows = both ? kHalf : kHalf / 2, q0 = both ? 0 : s * (kHalf / 2);
         const uint32_t q_tile = smem_addr(smem) + (both ? s : 0) * kTileBytes;
         for (int i = t; i < q_rows * 16; i += kHalf) {
-          const int r = q0 + (i >> 4), ch = i & 15, row = m.row0 + r_base + r;
+          const int r = q0 + (i >> 4), ch = i & 15;
           const bool there = r_base + r < m.rows;
-          const uint16_t* src = p.q + (there ? (long long)(m.tok0 + row / p.Gq) * p.qs0 +
-                                                   (long long)(m.kh * p.Gq + row % p.Gq) * p.qs1 + ch * 8
-                                             : 0);
+          const uint16_t* src = there ? row_query(p, m, r_base + r) + ch * 8 : p.q;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(panel_addr(q_tile, r, ch)), "l"(src),
                        "r"(there ? 16 : 0)
                        : "memory");
@@ -541,14 +545,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
       }
       const uint32_t o0_addr = tmem + lanes + 256 + (both ? s * 128 : 0);
-      auto place = [&](int rr) {  // of row rr of the unit
-        const int row = m.row0 + rr;
-        return (long long)(m.tok0 + row / p.Gq) * p.Hq + m.kh * p.Gq + row % p.Gq;
-      };
       const int dest = m.dest;
       const long long set = dest == kToRow ? (m.prefix ? 0 : (long long)p.N * p.Hq) : 0;
       if (dest != kToOut && live && (both || s == 0)) {
-        float2* to = dest == kToRow ? p.row_ml + set + place(r) : p.part.ml + (long long)dest * p.part.R + r;
+        float2* to = dest == kToRow ? p.row_ml + set + row_index(p, m, r) : p.part.ml + (long long)dest * p.part.R + r;
         *to = make_float2(ref, l);
       }
       const float inv = dest != kToOut ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             const int rr = 8 * k + (lane >> 2);
             const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 20 + 4 * (lane & 3));
             if (r_warp + rr < m.rows)
-              *reinterpret_cast<uint4*>(p.out + place(r_warp + rr) * kHeadDim + c + 8 * (lane & 3)) = x;
+              *reinterpret_cast<uint4*>(p.out + row_index(p, m, r_warp + rr) * kHeadDim + c + 8 * (lane & 3)) = x;
           }
         } else {
 #pragma unroll
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             const int rr = 4 * k + (lane >> 3);
             const float4 x = *reinterpret_cast<const float4*>(stage + rr * 36 + 4 * (lane & 7));
             if (r_warp + rr < m.rows) {
-              float* acc = dest == kToRow ? p.row_acc + (set + place(r_warp + rr)) * kHeadDim
+              float* acc = dest == kToRow ? p.row_acc + (set + row_index(p, m, r_warp + rr)) * kHeadDim
                                           : p.part.acc + ((long long)dest * p.part.R + r_warp + rr) * kHeadDim;
               *reinterpret_cast<float4*>(acc + c + 4 * (lane & 7)) = x;
             }
