@@ -281,12 +281,23 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const int s = warp - 9;
     const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
     constexpr uint32_t idesc_s = instr_desc<BF16>(false), idesc_o = instr_desc<BF16>(true);
-    // all lanes wait and see the same outcome, so the control flow is uniform
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-      wait_or_fail(bar, parity, &sh.failed, err);
-      return __any_sync(0xffffffffu, failed()) == 0;
+    // Waits on several barriers at once, one a lane: a wait costs about 150 clocks even when there is nothing to wait
+    // for.  All lanes see the same outcome, so the control flow is uniform.
+    auto wait_all = [&](int count, uint64_t* bar, uint32_t parity) {  // lanes 0 .. count - 1, each its own bar
+      bool done = lane >= count || mbar_try_wait(bar, parity);
+      for (uint32_t i = 0; !__all_sync(0xffffffffu, done); ++i) {
+        if (!done) done = mbar_try_wait(bar, parity);
+        if ((i & 255) == 255 && __any_sync(0xffffffffu, failed() || i > kSpinLimit)) {
+          if (lane == 0 && !failed()) {
+            *(volatile int*)&sh.failed = 1;
+            atomicOr(err, PALU_DEVERR_TIMEOUT);
+          }
+          return false;
+        }
+      }
+      return true;
     };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(1, bar, parity); };
     auto commit = [&](uint64_t* bar) {
       if (elect_one()) tc_commit(bar);
       __syncwarp();
@@ -301,67 +312,68 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (lane == 0) mbar_arrive(&sh.meta_empty[unit & 1]);
       if (n == 0 || !wait(&sh.q_full, unit & 1)) break;
       tc_fence_after();
-      auto wait_item = [&](int it) { return wait(&sh.kv_full[it % kRing], (it / kRing) & 1); };
       const uint32_t qa = q_addr + (both ? s : 0) * kTileBytes;
       auto scores = [&](int tile) {  // S = Q K^T, the keys of a tile
         const uint64_t da = smem_desc(qa, 16, 1024), db = smem_desc(ring_addr + (2 * tile % kRing) * kTileBytes, 16, 1024);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = ((k >> 2) * kPanelBytes + (k & 3) * 32) >> 4;
-            tc_mma_ss(tmem + s * 128, da + off, db + off, idesc_s, k > 0);
-          }
-          tc_commit(&sh.s_full[s]);
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = ((k >> 2) * kPanelBytes + (k & 3) * 32) >> 4;
+          tc_mma_ss(tmem + s * 128, da + off, db + off, idesc_s, k > 0);
         }
-        __syncwarp();
+        tc_commit(&sh.s_full[s]);
       };
       auto values = [&](int u, int tile, bool acc) {  // O += P_u V, 64 keys of a tile
         const uint64_t db = smem_desc(ring_addr + ((2 * tile + 1) % kRing) * kTileBytes + u * 8192, kPanelBytes, 1024);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + u * 32 + k * 8, db + (k * 2048 >> 4), idesc_o, acc || k > 0);
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k)
+          tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + u * 32 + k * 8, db + (k * 2048 >> 4), idesc_o, acc || k > 0);
       };
       auto release = [&](int it) {  // the half's arrival, or both where a tile is one half's alone
-        if (elect_one()) {
-          tc_commit(&sh.kv_empty[it % kRing]);
-          if (!both) tc_commit(&sh.kv_empty[it % kRing]);
-        }
-        __syncwarp();
+        tc_commit(&sh.kv_empty[it % kRing]);
+        if (!both) tc_commit(&sh.kv_empty[it % kRing]);
       };
       const int step = both ? 1 : 2, j0 = both ? 0 : s;
       bool ok = true;
       if (j0 < n) {
-        if (!wait_item(2 * (tile0 + j0))) break;
-        scores(tile0 + j0);
-        release(2 * (tile0 + j0));
+        const int it = 2 * (tile0 + j0);
+        if (!wait(&sh.kv_full[it % kRing], (it / kRing) & 1)) break;
+        if (elect_one()) {
+          scores(tile0 + j0);
+          release(it);
+        }
+        __syncwarp();
       }
       for (int j = j0; j < n; j += step) {
-        const int t = tile0 + j;
-        if (!(ok = wait_item(2 * t + 1) && wait(&sh.p_full[s][0], pc & 1))) break;
-        tc_fence_after();
-        values(0, t, j >= step);
+        const int t = tile0 + j, vi = 2 * t + 1, ki = 2 * (t + step);
         const bool more = j + step < n;
+        ok = wait_all(2, lane ? &sh.kv_full[vi % kRing] : &sh.p_full[s][0], lane ? (vi / kRing) & 1 : pc & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) values(0, t, j >= step);
+        __syncwarp();
         // The halves take turns with their last values and next scores: left to themselves they fall into step, both in
         // the softmax and then both waiting for the tensor cores (3,900 clocks a tile pair).
-        if (more && !(ok = wait_item(2 * (t + step)) && (!both || wait(&sh.token[s], turns & 1)))) break;
-        if (!(ok = wait(&sh.p_full[s][1], pc & 1))) break;
+        ok = wait_all(!more ? 1 : both ? 3 : 2,
+                      lane == 0   ? &sh.p_full[s][1]
+                      : lane == 1 ? &sh.kv_full[ki % kRing]
+                                  : &sh.token[s],
+                      lane == 0 ? pc & 1 : lane == 1 ? (ki / kRing) & 1 : turns & 1);
+        if (!ok) break;
         tc_fence_after();
-        values(1, t, true);
-        ++pc;
-        if (more) {
-          scores(t + step);
-          if (both) {
-            if (lane == 0) mbar_arrive(&sh.token[1 - s]);
-            ++turns;
+        if (elect_one()) {
+          values(1, t, true);
+          if (more) {
+            scores(t + step);
+            if (both) mbar_arrive(&sh.token[1 - s]);
+            release(vi);
+            release(ki);
+          } else {
+            release(vi);
           }
-          release(2 * t + 1);
-          release(2 * (t + step));
-        } else {
-          release(2 * t + 1);
         }
+        __syncwarp();
+        ++pc;
+        if (more && both) ++turns;
       }
       if (!ok) break;
       commit(&sh.unit_done);
