@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p, POINTER
 
 import torch
@@ -133,21 +134,19 @@ _SIGNATURES = {
     "palu_kivi_decode_workspace_size": (c_int32, [_P(palu_kivi_cache), c_int32, _P(c_size_t)]),
     "palu_kivi_decode_attn": (c_int32, [_P(palu_kivi_cache), c_void_p, c_int32, c_float, c_void_p, c_int32,
                                         c_void_p, c_size_t, c_void_p]),
-    "palu_qk_norm_rope": (c_int32, [_P(palu_qk_transform), c_int32, c_int64, c_int64, c_int32, c_int32, c_void_p,
-                                    _P(c_int64), c_void_p, _P(c_int64), c_void_p, c_void_p, c_void_p, c_void_p,
-                                    c_void_p]),
-    "palu_paged_cache_init": (c_int32, [_P(palu_paged_cache), c_int32, c_int32, c_int32, c_int64, c_void_p, _P(c_int64),
-                                        c_void_p, _P(c_int64), c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
-    "palu_paged_append": (c_int32, [_P(palu_paged_cache), _P(palu_qk_transform), c_int64, c_void_p, c_int32, c_void_p,
-                                    _P(c_int64), c_void_p, _P(c_int64), c_void_p, _P(c_int64), c_void_p, c_void_p,
-                                    c_void_p]),
-    "palu_paged_attn_workspace_size": (c_int32, [_P(palu_paged_cache), c_int64, c_int32, c_int32, c_int32,
-                                                 _P(c_size_t)]),
-    "palu_paged_attn": (c_int32, [_P(palu_paged_cache), c_int64, c_void_p, c_int32, c_int32, c_void_p, _P(c_int64),
-                                  c_int32, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
-    "palu_paged_sync": (c_int32, [_P(palu_paged_cache), _P(c_uint32), c_void_p]),
-    "palu_draft_verify": (c_int32, [c_int64, c_int32, c_int64, c_void_p, _P(c_int64), c_void_p, _P(c_int64), c_void_p,
-                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    # arrays of strides and the transform are passed as packed bytes: cheaper a call than ctypes objects
+    "palu_qk_norm_rope": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "palu_paged_cache_init": (c_int32, [_P(palu_paged_cache), c_int32, c_int32, c_int32, c_int64, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
+    "palu_paged_append": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "palu_paged_attn_workspace_size": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_int32, _P(c_size_t)]),
+    "palu_paged_attn": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_float,
+                                  c_void_p, c_void_p, c_size_t, c_void_p]),
+    "palu_paged_sync": (c_int32, [c_void_p, _P(c_uint32), c_void_p]),
+    "palu_draft_verify": (c_int32, [c_int64, c_int32, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
 }
 
 _lib = None
@@ -482,61 +481,90 @@ def palu_kivi_decode_attn(cache: palu_kivi_cache, q, out, workspace, softmax_sca
 # ------------------------------------------------------------------ the serving step (include/paged.h, include/draft.h)
 
 _TYPES = {torch.float16: PALU_TYPE_F16, torch.bfloat16: PALU_TYPE_BF16}
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_pack2, _pack3 = struct.Struct("2q").pack, struct.Struct("3q").pack
+_pack_transform = struct.Struct("PPPqiifi").pack    # palu_qk_transform
 
 
-def _need_rows(t, name, shape, dtype, device):
-    """A token-major operand: any strides with contiguous channels and 16-byte aligned rows (entries of `shape` that
-    are None match any extent).  Returns its leading strides, of an extent-1 dimension 0: torch leaves those open."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
-    got = t.shape
-    if len(got) != len(shape) or any(e is not None and e != s for e, s in zip(shape, got)):
-        raise ValueError(f"{name} has shape {tuple(got)}; expected {tuple('*' if e is None else e for e in shape)}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    lead = [s if n > 1 else 0 for s, n in zip(st[:-1], got)]
-    if t.data_ptr() % 16 or any(s % 8 for s in lead):
-        raise ValueError(f"{name}'s rows must be 16-byte aligned (strides {st})")
-    return (c_int64 * len(lead))(*lead)
+# These calls take a few microseconds on the GPU, so their checks are written for the case that all is well: one
+# expression a tensor, and the function that says what is wrong only where something is.
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _need_on(t, name, shape, dtype, device):
-    """A contiguous operand of one type on one device."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}; expected {dtype} {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _need_device(t, name):
-    """The library launches on the current device: its operands must be there."""
+def _here(t, name):
+    """The tensor's device index, which has to be the current one: the library launches there."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = t.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, which is not the current device")
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
     return dev
 
 
-def _transform(dtype, device, cos_sin, q_weight, k_weight, eps, interleaved):
-    t = palu_qk_transform()
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need_on(w, name, (D,), dtype, device)
-            setattr(t, name, w.data_ptr())
+def _is(t, shape, dtype, dev):
+    """A contiguous tensor of this shape (a tuple) and type on this device."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _refuse(t, name, shape, dtype, dev):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)} on cuda:{dev}, contiguous")
+
+
+def _need_is(t, name, shape, dtype, dev):
+    if not _is(t, shape, dtype, dev):
+        _refuse(t, name, shape, dtype, dev)
+
+
+def _rows(t, name, shape, dtype, dev):
+    """A token-major operand of this shape: any strides with contiguous channels and 16-byte aligned rows.  Returns its
+    leading strides (0 for a dimension of one element: torch leaves that one open)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor")
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)} on cuda:{dev}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    if 1 in shape:
+        st = [s if n > 1 else 0 for s, n in zip(st, shape)]
+    align = t.data_ptr() >> 1
+    for s in st[:-1]:
+        align |= s
+    if align & 7:
+        raise ValueError(f"{name}'s rows must be 16-byte aligned (strides {t.stride()})")
+    return st
+
+
+def _shape_of(t, name, dims):
+    """The shape of a tensor with this many dimensions, the last of them the head's channels."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    shape = t.shape
+    if len(shape) != dims or shape[-1] != D:
+        raise ValueError(f"{name} has shape {tuple(shape)}; expected {dims} dimensions, the last of {D}")
+    return shape
+
+
+def _transform(dtype, dev, cos_sin, q_weight, k_weight, eps, interleaved):
+    """palu_qk_transform as bytes."""
+    qw = kw = cs = n = rope = 0
+    if q_weight is not None:
+        _need_is(q_weight, "q_weight", (D,), dtype, dev)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _need_is(k_weight, "k_weight", (D,), dtype, dev)
+        kw = k_weight.data_ptr()
     if cos_sin is not None:
         if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be a tensor [positions, rope_dim]")
-        _need_on(cos_sin, "cos_sin", tuple(cos_sin.shape), torch.float32, device)
-        t.cos_sin, (t.n_positions, t.rope_dim) = cos_sin.data_ptr(), cos_sin.shape
-    t.interleaved = 1 if interleaved else 0
-    t.eps = eps
-    return t
+        n, rope = cos_sin.shape
+        _need_is(cos_sin, "cos_sin", (n, rope), _F32, dev)
+        cs = cos_sin.data_ptr()
+    return _pack_transform(qw, kw, cs, n, rope, 1 if interleaved else 0, eps, 0)
 
 
 def qk_norm_rope(q, k, positions, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -546,31 +574,33 @@ def qk_norm_rope(q, k, positions, cos_sin=None, q_weight=None, k_weight=None, ep
     int64 [B, T], cos_sin fp32 [n_positions, rope_dim] (cosines, then sines).  Returns (q_out [B, Hq, T, 128],
     k_out [B, Hkv, T, 128]), the layout the caches take.  error: int32 [1] on the device, collecting
     PALU_DEVERR_POSITION; the rows of such a token are NaN."""
-    dev = _need_device(q, "q")
-    if q.dtype not in _TYPES:
-        raise ValueError(f"q has dtype {q.dtype}; expected torch.float16 or torch.bfloat16")
+    dev = _here(q, "q")
     dt = q.dtype
-    qs = _need_rows(q, "q", (None, None, None, D), dt, dev)
-    B, T, Hq, _ = q.shape
-    ks = _need_rows(k, "k", (B, T, None, D), dt, dev)
-    Hk = k.shape[2]
+    if dt not in _TYPES:
+        raise ValueError(f"q has dtype {dt}; expected torch.float16 or torch.bfloat16")
+    B, T, Hq, _ = shape = _shape_of(q, "q", 4)
+    qs = _rows(q, "q", shape, dt, dev)
+    Hk = _shape_of(k, "k", 4)[2]
+    ks = _rows(k, "k", (B, T, Hk, D), dt, dev)
     tr = _transform(dt, dev, cos_sin, q_weight, k_weight, eps, interleaved)
+    pos = 0
     if cos_sin is not None:
-        _need_on(positions, "positions", (B, T), torch.int64, dev)
+        _need_is(positions, "positions", (B, T), _I64, dev)
+        pos = positions.data_ptr()
     if error is not None:
-        _need_on(error, "error", (1,), torch.int32, dev)
+        _need_is(error, "error", (1,), _I32, dev)
     if q_out is None:
-        q_out = torch.empty((B, Hq, T, D), dtype=dt, device=dev)
+        q_out = torch.empty((B, Hq, T, D), dtype=dt, device=q.device)
     else:
-        _need_on(q_out, "q_out", (B, Hq, T, D), dt, dev)
+        _need_is(q_out, "q_out", (B, Hq, T, D), dt, dev)
     if k_out is None:
-        k_out = torch.empty((B, Hk, T, D), dtype=dt, device=dev)
+        k_out = torch.empty((B, Hk, T, D), dtype=dt, device=q.device)
     else:
-        _need_on(k_out, "k_out", (B, Hk, T, D), dt, dev)
+        _need_is(k_out, "k_out", (B, Hk, T, D), dt, dev)
     if B and T:
-        _check(lib().palu_qk_norm_rope(ctypes.byref(tr), _TYPES[dt], B, T, Hq, Hk, q.data_ptr(), qs, k.data_ptr(), ks,
-                                       positions.data_ptr() if cos_sin is not None else None, q_out.data_ptr(),
-                                       k_out.data_ptr(), None if error is None else error.data_ptr(), _stream(stream)))
+        _check(lib().palu_qk_norm_rope(tr, _TYPES[dt], B, T, Hq, Hk, q.data_ptr(), _pack3(*qs[:3]), k.data_ptr(),
+                                       _pack3(*ks[:3]), pos, q_out.data_ptr(), k_out.data_ptr(),
+                                       None if error is None else error.data_ptr(), _raw_stream(stream, dev)))
     return q_out, k_out
 
 
@@ -581,32 +611,35 @@ class PagedCache:
     [B]: the program's own, read by every call; change them in place to hand out pages and to roll tokens back."""
 
     def __init__(self, k_pages, v_pages, page_table, lengths):
-        dev = _need_device(k_pages, "k_pages")
+        dev = _here(k_pages, "k_pages")
         if k_pages.dtype not in _TYPES:
             raise ValueError(f"k_pages has dtype {k_pages.dtype}; expected torch.float16 or torch.bfloat16")
-        self.dtype, self.device = k_pages.dtype, dev
-        _need_rows(k_pages, "k_pages", (None, None, None, D), self.dtype, dev)
-        _need_rows(v_pages, "v_pages", tuple(k_pages.shape), self.dtype, dev)
-        n_pages, self.kv_heads, self.page_size, _ = k_pages.shape
+        self.dtype, self.device, self._dev = k_pages.dtype, k_pages.device, dev
+        n_pages, self.kv_heads, self.page_size, _ = shape = _shape_of(k_pages, "k_pages", 4)
+        _rows(k_pages, "k_pages", shape, self.dtype, dev)
+        _rows(v_pages, "v_pages", shape, self.dtype, dev)
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be a tensor [batch, width]")
         self.batch, self.width = page_table.shape
-        _need_on(page_table, "page_table", (self.batch, self.width), torch.int32, dev)
-        _need_on(lengths, "lengths", (self.batch,), torch.int64, dev)
+        _need_is(page_table, "page_table", (self.batch, self.width), _I32, dev)
+        _need_is(lengths, "lengths", (self.batch,), _I64, dev)
         self.k_pages, self.v_pages, self.page_table, self.lengths = k_pages, v_pages, page_table, lengths
-        self.error = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.error = torch.zeros(1, dtype=_I32, device=self.device)
 
         def strides(t):  # of a dimension of one element: anything that is aligned
-            return (c_int64 * 3)(*[s if n > 1 else D for s, n in zip(t.stride()[:3], t.shape)])
+            return _pack3(*[s if n > 1 else D for s, n in zip(t.stride()[:3], shape)])
         self.c = palu_paged_cache()
         _check(lib().palu_paged_cache_init(ctypes.byref(self.c), _TYPES[self.dtype], self.kv_heads, self.page_size, n_pages,
                                            k_pages.data_ptr(), strides(k_pages), v_pages.data_ptr(), strides(v_pages),
                                            page_table.data_ptr(), self.batch, self.width, lengths.data_ptr(),
                                            self.error.data_ptr()))
+        self._c = ctypes.addressof(self.c)
+        self._offsets = (self.batch + 1,)
 
-    def _here(self):
-        if self.device.index != torch.cuda.current_device():
+    def _on_current(self):
+        if self._dev != torch._C._cuda_getDevice():
             raise ValueError(f"the cache is on {self.device}, which is not the current device")
+        return self._dev
 
     def append(self, k, v, offsets, q=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                positions=None, q_out=None, stream=None):
@@ -614,37 +647,38 @@ class PagedCache:
         the last tokens of sequence b (lengths[b] counts them already).  Keys, and q [N, Hq, 128] where given, are
         normalised and rotated as in qk_norm_rope, by default at each token's place.  Returns q_out (None without q);
         rows behind offsets[B] are left as they were."""
-        self._here()
-        dt, dev = self.dtype, self.device
-        ks = _need_rows(k, "k", (None, self.kv_heads, D), dt, dev)
-        n = k.shape[0]
-        vs = _need_rows(v, "v", (n, self.kv_heads, D), dt, dev)
-        _need_on(offsets, "offsets", (self.batch + 1,), torch.int32, dev)
+        dev, dt = self._on_current(), self.dtype
+        n = _shape_of(k, "k", 3)[0]
+        shape = (n, self.kv_heads, D)
+        ks = _rows(k, "k", shape, dt, dev)
+        vs = _rows(v, "v", shape, dt, dev)
+        if not _is(offsets, self._offsets, _I32, dev):
+            _refuse(offsets, "offsets", self._offsets, _I32, dev)
         tr = _transform(dt, dev, cos_sin, q_weight, k_weight, eps, interleaved)
         if positions is not None:
-            _need_on(positions, "positions", (n,), torch.int64, dev)
-        qs, hq = None, 0
+            _need_is(positions, "positions", (n,), _I64, dev)
+        qp = qs = out = None
+        hq = 0
         if q is not None:
-            qs = _need_rows(q, "q", (n, None, D), dt, dev)
-            hq = q.shape[1]
+            hq = _shape_of(q, "q", 3)[1]
+            qs = _pack2(*_rows(q, "q", (n, hq, D), dt, dev)[:2])
             if q_out is None:
-                q_out = torch.empty((n, hq, D), dtype=dt, device=dev)
+                q_out = torch.empty((n, hq, D), dtype=dt, device=self.device)
             else:
-                _need_on(q_out, "q_out", (n, hq, D), dt, dev)
+                _need_is(q_out, "q_out", (n, hq, D), dt, dev)
+            qp, out = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("q_out is given without q")
         if n:
-            _check(lib().palu_paged_append(ctypes.byref(self.c), ctypes.byref(tr), n, offsets.data_ptr(), hq,
-                                           None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                           None if positions is None else positions.data_ptr(),
-                                           None if q is None else q_out.data_ptr(), _stream(stream)))
+            _check(lib().palu_paged_append(self._c, tr, n, offsets.data_ptr(), hq, qp, qs, k.data_ptr(), _pack2(*ks[:2]),
+                                           v.data_ptr(), _pack2(*vs[:2]), None if positions is None else positions.data_ptr(),
+                                           out, _raw_stream(stream, dev)))
         return q_out
 
     def attend_workspace(self, tokens, q_heads, max_new, shared_pages=0):
         """A workspace for attend calls of up to these sizes (calls that share one must not overlap on the GPU)."""
         n = c_size_t()
-        _check(lib().palu_paged_attn_workspace_size(ctypes.byref(self.c), max(tokens, 1), q_heads, max_new, shared_pages,
-                                                    ctypes.byref(n)))
+        _check(lib().palu_paged_attn_workspace_size(self._c, max(tokens, 1), q_heads, max_new, shared_pages, ctypes.byref(n)))
         return _dev_bytes(n.value, self.device)
 
     def attend(self, q, offsets, max_new, shared_pages=0, softmax_scale=0.0, workspace=None, out=None, stream=None):
@@ -652,30 +686,30 @@ class PagedCache:
         at place t, attends to tokens 0 .. t of its sequence.  max_new: the most rows a sequence has.  shared_pages:
         leading page-table entries that are the same in every row; they are read once for the batch.  Returns out
         [N, Hq, 128]; rows behind offsets[B] are left as they were."""
-        self._here()
-        dev = self.device
-        qs = _need_rows(q, "q", (None, None, D), self.dtype, dev)
-        n, hq, _ = q.shape
-        _need_on(offsets, "offsets", (self.batch + 1,), torch.int32, dev)
+        dev = self._on_current()
+        n, hq, _ = shape = _shape_of(q, "q", 3)
+        qs = _rows(q, "q", shape, self.dtype, dev)
+        if not _is(offsets, self._offsets, _I32, dev):
+            _refuse(offsets, "offsets", self._offsets, _I32, dev)
         if out is None:
-            out = torch.empty((n, hq, D), dtype=self.dtype, device=dev)
+            out = torch.empty(shape, dtype=self.dtype, device=self.device)
         else:
-            _need_on(out, "out", (n, hq, D), self.dtype, dev)
+            _need_is(out, "out", shape, self.dtype, dev)
         if n == 0:
             return out
         if workspace is None:
             workspace = self.attend_workspace(n, hq, max_new, shared_pages)
-        else:
-            _need_on(workspace, "workspace", tuple(workspace.shape), torch.uint8, dev)
-        _check(lib().palu_paged_attn(ctypes.byref(self.c), n, offsets.data_ptr(), max_new, hq, q.data_ptr(), qs,
-                                     shared_pages, softmax_scale, out.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel(), _stream(stream)))
+        elif not _is(workspace, workspace.shape, torch.uint8, dev):
+            _refuse(workspace, "workspace", workspace.shape, torch.uint8, dev)
+        _check(lib().palu_paged_attn(self._c, n, offsets.data_ptr(), max_new, hq, q.data_ptr(), _pack2(*qs[:2]), shared_pages,
+                                     softmax_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                     _raw_stream(stream, dev)))
         return out
 
     def sync(self, stream=None):
         """Synchronise; raises PaluError if the device error word was set (and clears it)."""
         e = c_uint32()
-        _check(lib().palu_paged_sync(ctypes.byref(self.c), ctypes.byref(e), _stream(stream)))
+        _check(lib().palu_paged_sync(self._c, ctypes.byref(e), _raw_stream(stream, self._dev)))
         return e.value
 
 
@@ -685,45 +719,55 @@ def draft_verify(target, draft, drafts, accept_u, sample_u, n_drafts=None, lengt
     [B, k], accept_u fp32 [B, k] and sample_u fp32 [B] in [0, 1), n_drafts int32 [B] (default k each), lengths int64 [B]
     with all drafts counted.  Returns (tokens int64 [B, k+1]: the kept drafts, one drawn token, -1; n_kept int32 [B];
     new_lengths int64 [B], or None without lengths)."""
-    dev = _need_device(target, "target")
+    dev = _here(target, "target")
     if not isinstance(drafts, torch.Tensor) or drafts.dim() != 2:
         raise ValueError("drafts must be a tensor [batch, k]")
-    B, k = drafts.shape
-    _need_on(drafts, "drafts", (B, k), torch.int64, dev)
-    if target.dtype != torch.float32 or target.dim() != 3 or tuple(target.shape[:2]) != (B, k + 1) or \
-            (target.shape[2] > 1 and target.stride(2) != 1):
-        raise ValueError(f"target is {target.dtype} {tuple(target.shape)}; expected torch.float32 {(B, k + 1, '*')} with "
-                         "contiguous rows")
-    V = target.shape[2]
-    ds = None
+    B, k = shape = drafts.shape
+    rows = (B,)
+    _need_is(drafts, "drafts", shape, _I64, dev)
+
+    def table(t, name, n):  # rows of contiguous fp32 values
+        if t.dtype is not _F32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != n or t.get_device() != dev:
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected torch.float32 {(B, n, '*')} on cuda:{dev}")
+        st = t.stride()
+        if st[2] != 1 and t.shape[2] > 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return _pack2(st[0], st[1])
+    ts, V = table(target, "target", k + 1), target.shape[2]
+    dp = ds = None
     if draft is not None:
-        if not isinstance(draft, torch.Tensor) or draft.device != dev or draft.dtype != torch.float32 or \
-                tuple(draft.shape) != (B, k, V) or (V > 1 and draft.stride(2) != 1):
-            raise ValueError(f"draft must be torch.float32 {(B, k, V)} on {dev} with contiguous rows")
-        ds = (c_int64 * 2)(*draft.stride()[:2])
-    _need_on(accept_u, "accept_u", (B, k), torch.float32, dev)
-    _need_on(sample_u, "sample_u", (B,), torch.float32, dev)
+        if not isinstance(draft, torch.Tensor):
+            raise ValueError("draft must be a tensor or None")
+        ds, dp = table(draft, "draft", k), draft.data_ptr()
+        if draft.shape[2] != V:
+            raise ValueError(f"draft has {draft.shape[2]} values a row and target {V}")
+    _need_is(accept_u, "accept_u", shape, _F32, dev)
+    _need_is(sample_u, "sample_u", rows, _F32, dev)
+    np_ = lp = nlp = None
     if n_drafts is not None:
-        _need_on(n_drafts, "n_drafts", (B,), torch.int32, dev)
-    for t, name, shape, dt in ((tokens, "tokens", (B, k + 1), torch.int64), (n_kept, "n_kept", (B,), torch.int32),
-                               (lengths, "lengths", (B,), torch.int64), (new_lengths, "new_lengths", (B,), torch.int64)):
-        if t is not None:
-            _need_on(t, name, shape, dt, dev)
-    if new_lengths is not None and lengths is None:
-        raise ValueError("new_lengths is given without lengths")
+        _need_is(n_drafts, "n_drafts", rows, _I32, dev)
+        np_ = n_drafts.data_ptr()
     if tokens is None:
-        tokens = torch.empty((B, k + 1), dtype=torch.int64, device=dev)
+        tokens = torch.empty((B, k + 1), dtype=_I64, device=target.device)
+    else:
+        _need_is(tokens, "tokens", (B, k + 1), _I64, dev)
     if n_kept is None:
-        n_kept = torch.empty(B, dtype=torch.int32, device=dev)
-    if lengths is not None and new_lengths is None:
-        new_lengths = torch.empty(B, dtype=torch.int64, device=dev)
+        n_kept = torch.empty(rows, dtype=_I32, device=target.device)
+    else:
+        _need_is(n_kept, "n_kept", rows, _I32, dev)
+    if lengths is not None:
+        _need_is(lengths, "lengths", rows, _I64, dev)
+        if new_lengths is None:
+            new_lengths = torch.empty(rows, dtype=_I64, device=target.device)
+        else:
+            _need_is(new_lengths, "new_lengths", rows, _I64, dev)
+        lp, nlp = lengths.data_ptr(), new_lengths.data_ptr()
+    elif new_lengths is not None:
+        raise ValueError("new_lengths is given without lengths")
     if B:
-        _check(lib().palu_draft_verify(B, k, V, target.data_ptr(), (c_int64 * 2)(*target.stride()[:2]),
-                                       None if draft is None else draft.data_ptr(), ds, drafts.data_ptr(),
-                                       None if n_drafts is None else n_drafts.data_ptr(), accept_u.data_ptr(),
-                                       sample_u.data_ptr(), None if lengths is None else lengths.data_ptr(),
-                                       tokens.data_ptr(), n_kept.data_ptr(),
-                                       None if lengths is None else new_lengths.data_ptr(), _stream(stream)))
+        _check(lib().palu_draft_verify(B, k, V, target.data_ptr(), ts, dp, ds, drafts.data_ptr(), np_, accept_u.data_ptr(),
+                                       sample_u.data_ptr(), lp, tokens.data_ptr(), n_kept.data_ptr(), nlp,
+                                       _raw_stream(stream, dev)))
     return tokens, n_kept, new_lengths
 
 

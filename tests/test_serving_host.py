@@ -33,6 +33,10 @@ int main(void) {
         subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), src, "-o", exe], check=True)
         vals = list(map(int, subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()))
     t, c = palu.palu_qk_transform, palu.palu_paged_cache
+    packed = palu._pack_transform(1, 2, 3, 4, 5, 6, 7.5, 0)
+    x = t.from_buffer_copy(packed)
+    assert len(packed) == vals[0] and (x.q_weight, x.k_weight, x.cos_sin, x.n_positions, x.rope_dim, x.interleaved, x.eps) == \
+        (1, 2, 3, 4, 5, 6, 7.5)
     assert vals == [ctypes.sizeof(t), t.eps.offset, ctypes.sizeof(c), c.k_strides.offset, c.page_table.offset, c.error.offset]
 
 
