@@ -8,12 +8,12 @@
 // The token is the first whose running sum of w(t) = max(p(t) - q(t), 0)
 // passes u * total.  With 150,000 tokens most gaps between running sums are
 // far below one fp32 ulp of the total, so fp32 sums would pick other tokens
-// than the exact sums; fp64 sums would be right, but cost five fp64
-// instructions a value at 2 lanes a clock and SM: about 80 us for 64
-// rows of 152,065, against 12 us of reading.  So each lane keeps an unevaluated
-// pair of floats: the difference as its rounded value and exact remainder,
-// the sum with its error terms (about 17 fp32 instructions a value); fp64
-// starts with one value per lane.  The pair is right to about 2^-46 of the sum.
+// than the exact sums.  fp64 is no way out here: at 2 lanes a clock and SM the
+// five fp64 instructions a value would take about 80 us for 64 rows of 152,065,
+// against 12 us of reading.  So everything is an unevaluated pair of floats:
+// a difference is its rounded value and the exact remainder, a sum carries its
+// rounding errors along (about 17 fp32 instructions a value), right to about
+// 2^-45 of the sum.
 #include <algorithm>
 
 #include "draft.h"
@@ -22,9 +22,6 @@
 namespace palu {
 
 constexpr int kDraftCluster = 8;
-constexpr int kDraftWarps = 16;
-constexpr int kDraftThreads = 32 * kDraftWarps;
-constexpr int kDraftSegs = kDraftCluster * kDraftWarps;  // a row is cut into one segment a warp
 constexpr int kDraftMax = 256;
 
 struct DraftParams {
@@ -56,18 +53,58 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void store_remote_f64(double* local, uint32_t rank, double v) {
+__device__ __forceinline__ void store_remote(float2* local, uint32_t rank, float2 v) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
-__global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(kDraftThreads, 2)
-    draft_verify_kernel(const DraftParams d) {
-  __shared__ double sums[2][kDraftSegs];  // one set a pass: the second pass never waits for readers of the first
-  __shared__ double wsum[kDraftWarps];
-  __shared__ int first_out;   // first draft that is not kept
-  __shared__ int found;       // drawn token
+// Sums as pairs (x + y, |y| at most half an ulp of x).
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+  float s, e, h, r;
+  two_sum(a.x, b.x, s, e);
+  e = __fadd_rn(e, __fadd_rn(a.y, b.y));
+  two_sum(s, e, h, r);
+  return make_float2(h, r);
+}
+__device__ __forceinline__ float2 pair_scale(float2 a, float u) {
+  float p, e, h, r;
+  two_prod(a.x, u, p, e);
+  e = __fmaf_rn(a.y, u, e);
+  two_sum(p, e, h, r);
+  return make_float2(h, r);
+}
+__device__ __forceinline__ bool pair_above(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
+__device__ __forceinline__ float2 shfl_up(float2 v, int x) {
+  return make_float2(__shfl_up_sync(0xffffffffu, v.x, x), __shfl_up_sync(0xffffffffu, v.y, x));
+}
+__device__ __forceinline__ float2 shfl(float2 v, int src) {
+  return make_float2(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src));
+}
+// Inclusive sums over the lanes.
+__device__ __forceinline__ float2 warp_scan(float2 v, int lane) {
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const float2 y = shfl_up(v, x);
+    if (lane >= x) v = pair_add(y, v);
+  }
+  return v;
+}
+// The sum before this lane.
+__device__ __forceinline__ float2 before_lane(float2 incl, int lane) {
+  const float2 y = shfl_up(incl, 1);
+  return lane ? y : make_float2(0.f, 0.f);
+}
+
+// WARPS a CTA: a row is cut into one segment a warp of the cluster.
+template <int WARPS>
+__global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(32 * WARPS, 512 / (16 * WARPS)) draft_verify_kernel(const DraftParams d) {
+  constexpr int SEGS = kDraftCluster * WARPS, PER_LANE = SEGS / 32, THREADS = 32 * WARPS;
+  __shared__ float2 sums[2][SEGS];  // one set a pass: the second pass never waits for readers of the first
+  __shared__ float2 wsum[WARPS];
+  __shared__ float2 before, target;
+  __shared__ int first_out;         // first draft that is not kept
+  __shared__ int found, win;        // drawn token; its segment
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const long long b = blockIdx.x / kDraftCluster;
@@ -77,16 +114,16 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(kDraftTh
     found = 0x7fffffff;
   }
   __syncthreads();
-  if (tid < n) {
-    const long long x = d.drafts[b * d.k + tid];
+  for (int i = tid; i < n; i += THREADS) {
+    const long long x = d.drafts[b * d.k + i];
     bool keep = false;
     if (x >= 0 && x < d.V) {
-      const float p = d.target[b * d.ts0 + tid * d.ts1 + x];
-      const float q = d.draft ? d.draft[b * d.ds0 + tid * d.ds1 + x] : 1.f;
+      const float p = d.target[b * d.ts0 + i * d.ts1 + x];
+      const float q = d.draft ? d.draft[b * d.ds0 + i * d.ds1 + x] : 1.f;
       // 24 x 24 bits: the product is exact in fp64
-      keep = (double)d.accept_u[b * d.k + tid] * (double)q < (double)p;
+      keep = (double)d.accept_u[b * d.k + i] * (double)q < (double)p;
     }
-    if (!keep) atomicMin(&first_out, tid);
+    if (!keep) atomicMin(&first_out, i);
   }
   __syncthreads();
   const int a = first_out;
@@ -94,107 +131,109 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(kDraftTh
   const float* qrow = (a < n && d.draft) ? d.draft + b * d.ds0 + a * d.ds1 : nullptr;
   // without draft probabilities the refused token itself has weight 0
   long long skip = (a < n && !d.draft) ? d.drafts[b * d.k + a] : -1;
-  const int seg0 = (int)rank * kDraftWarps + warp;
+  const int seg0 = (int)rank * WARPS + warp;
   const long long t0 = (long long)seg0 * d.seg, t1 = min(t0 + d.seg, (long long)d.V);
-  double total = 0.0, before = 0.0;
-  int win = -1;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     float s = 0.f, e = 0.f;
-    long long t = t0 + lane;
-    // eight loads of each row in flight a lane
-    for (; t + 7 * 32 < t1; t += 8 * 32) {
-      float p[8], q[8];
+    // eight values of each row a lane at a time, the next eight on their way meanwhile; behind the segment's end lanes
+    // read its last value, with weight 0
+    const int len = (int)(t1 - t0), skip_at = skip >= t0 && skip < t1 ? (int)(skip - t0) : -1;
+    const float *pseg = prow + t0, *qseg = qrow ? qrow + t0 : nullptr;
+    auto load = [&](int t, float (&p)[8], float (&q)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = prow[t + 32 * i];
+      for (int i = 0; i < 8; ++i) p[i] = __ldcs(pseg + min(t + 32 * i, len - 1));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = qrow ? qrow[t + 32 * i] : 0.f;
+      for (int i = 0; i < 8; ++i) q[i] = qseg ? __ldcs(qseg + min(t + 32 * i, len - 1)) : 0.f;
+    };
+    auto add = [&](int t, const float (&p)[8], const float (&q)[8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float hi, lo, r;
-        draft_weight(t + 32 * i == skip ? 0.f : p[i], q[i], hi, lo);
+        draft_weight(t + 32 * i == skip_at || t + 32 * i >= len ? 0.f : p[i], q[i], hi, lo);
         two_sum(s, hi, s, r);
         e = __fadd_rn(e, __fadd_rn(r, lo));
       }
-    }
-    for (; t < t1; t += 32) {
-      float hi, lo, r;
-      draft_weight(t == skip ? 0.f : prow[t], qrow ? qrow[t] : 0.f, hi, lo);
-      two_sum(s, hi, s, r);
-      e = __fadd_rn(e, __fadd_rn(r, lo));
-    }
-    double sum = (double)s + (double)e;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane < kDraftCluster) store_remote_f64(&sums[pass][seg0], lane, sum);
-    cluster_sync();
-    // every warp finds the segment of the drawn token: four segments a lane
-    double v[kDraftSegs / 32], run = 0.0;
-#pragma unroll
-    for (int i = 0; i < kDraftSegs / 32; ++i) run += (v[i] = sums[pass][lane * (kDraftSegs / 32) + i]);
-    double incl = run;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, incl, x);
-      if (lane >= x) incl += y;
-    }
-    total = __shfl_sync(0xffffffffu, incl, 31);
-    const double target = (double)d.sample_u[b] * total;
-    double c = incl - run;
-    int mine = kDraftSegs;
-    double mine_before = 0.0;
-#pragma unroll
-    for (int i = 0; i < kDraftSegs / 32; ++i) {
-      if (mine == kDraftSegs && v[i] > 0.0 && c + v[i] > target) {
-        mine = lane * (kDraftSegs / 32) + i;
-        mine_before = c;
+    };
+    if (len > 0) {
+      float p0[8], q0[8], p1[8], q1[8];
+      load(lane, p0, q0);
+      for (int t = lane; t < len; t += 16 * 32) {
+        if (t + 8 * 32 < len) load(t + 8 * 32, p1, q1);
+        add(t, p0, q0);
+        if (t + 8 * 32 >= len) break;
+        if (t + 16 * 32 < len) load(t + 16 * 32, p0, q0);
+        add(t + 8 * 32, p1, q1);
       }
-      c += v[i];
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, mine < kDraftSegs);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      win = __shfl_sync(0xffffffffu, mine, src);
-      before = __shfl_sync(0xffffffffu, mine_before, src);
-      break;
+    float2 sum = pair_add(make_float2(s, 0.f), make_float2(e, 0.f));
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+      sum = pair_add(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, x), __shfl_xor_sync(0xffffffffu, sum.y, x)));
+    if (lane < kDraftCluster) store_remote(&sums[pass][seg0], lane, sum);
+    cluster_sync();
+    // the first warp of every CTA finds the segment of the drawn token
+    if (warp == 0) {
+      float2 v[PER_LANE], run = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < PER_LANE; ++i) run = pair_add(run, v[i] = sums[pass][lane * PER_LANE + i]);
+      const float2 incl = warp_scan(run, lane), total = shfl(incl, 31), want = pair_scale(total, d.sample_u[b]);
+      float2 c = before_lane(incl, lane), mine_before = c;
+      int mine = SEGS;
+#pragma unroll
+      for (int i = 0; i < PER_LANE; ++i) {
+        const float2 next = pair_add(c, v[i]);
+        if (mine == SEGS && v[i].x > 0.f && pair_above(next, want)) {
+          mine = lane * PER_LANE + i;
+          mine_before = c;
+        }
+        c = next;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, mine < SEGS);
+      const int src = hit ? __ffs(hit) - 1 : 0;
+      const int seg = __shfl_sync(0xffffffffu, mine, src);
+      const float2 bef = shfl(mine_before, src);
+      if (lane == 0) {
+        win = hit ? seg : -1;
+        before = bef;
+        target = want;
+      }
     }
+    __syncthreads();
     // no weight over zero: the target's own row, once (the refused token counts again)
-    if (a == n) break;
+    if (win >= 0 || a == n) break;
+    __syncthreads();
     qrow = nullptr;
     skip = -1;
   }
   // the CTA that holds the segment (or the first one, without any) answers
-  if (win >= 0 ? (win / kDraftWarps != (int)rank) : (rank != 0)) return;
+  const int w = win;
+  if (w >= 0 ? (w / WARPS != (int)rank) : (rank != 0)) return;
   int token = -1;
-  if (win >= 0) {
-    const double target = (double)d.sample_u[b] * total;
-    const long long w0 = (long long)win * d.seg, w1 = min(w0 + d.seg, (long long)d.V);
-    const int per = (int)((w1 - w0 + kDraftThreads - 1) / kDraftThreads);
+  if (w >= 0) {
     // `per` consecutive values a thread, their sums scanned over the CTA
+    const long long w0 = (long long)w * d.seg, w1 = min(w0 + d.seg, (long long)d.V);
+    const int per = (int)((w1 - w0 + THREADS - 1) / THREADS);
     const long long a0 = w0 + (long long)tid * per, a1 = min(a0 + per, w1);
-    double own = 0.0;
+    float2 own = make_float2(0.f, 0.f);
     int last = -1;
     for (long long t = a0; t < a1; ++t) {
       float hi, lo;
       draft_weight(t == skip ? 0.f : prow[t], qrow ? qrow[t] : 0.f, hi, lo);
       if (hi > 0.f) last = (int)t;
-      own += (double)hi + (double)lo;
+      own = pair_add(own, make_float2(hi, lo));
     }
-    double incl = own;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, incl, x);
-      if (lane >= x) incl += y;
-    }
+    const float2 incl = warp_scan(own, lane);
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    double c = before + (incl - own);
-    for (int w = 0; w < warp; ++w) c += wsum[w];
+    const float2 warps = warp_scan(lane < WARPS ? wsum[lane] : make_float2(0.f, 0.f), lane);
+    const float2 base = warp ? shfl(warps, warp - 1) : make_float2(0.f, 0.f);
+    float2 c = pair_add(pair_add(before, base), before_lane(incl, lane));
     for (long long t = a0; t < a1; ++t) {
       float hi, lo;
       draft_weight(t == skip ? 0.f : prow[t], qrow ? qrow[t] : 0.f, hi, lo);
-      c += (double)hi + (double)lo;
-      if (hi > 0.f && c > target) {
+      c = pair_add(c, make_float2(hi, lo));
+      if (hi > 0.f && pair_above(c, target)) {
         atomicMin(&found, (int)t);
         break;
       }
@@ -212,7 +251,7 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(kDraftTh
       token = found;
     }
   }
-  for (int i = tid; i <= d.k; i += kDraftThreads)
+  for (int i = tid; i <= d.k; i += THREADS)
     d.tokens[b * (d.k + 1) + i] = i < a ? d.drafts[b * d.k + i] : i == a ? token : -1;
   if (tid == 0) {
     d.n_kept[b] = a;
@@ -261,7 +300,14 @@ extern "C" palu_status palu_draft_verify(int64_t batch, int32_t k, int64_t vocab
   p.new_lengths = reinterpret_cast<long long*>(new_lengths);
   p.k = k;
   p.V = (int)vocab;
-  p.seg = (int)((vocab + kDraftSegs - 1) / kDraftSegs);
-  draft_verify_kernel<<<(unsigned)(batch * kDraftCluster), kDraftThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Few sequences: more warps a CTA shorten the row's way.  Many: smaller CTAs, so that 64 sequences are one wave.
+  const bool few = batch * kDraftCluster <= device_sm_count();
+  const int segs = kDraftCluster * (few ? 16 : 8);
+  p.seg = (int)((vocab + segs - 1) / segs);
+  if (few)
+    draft_verify_kernel<16><<<(unsigned)(batch * kDraftCluster), 512, 0, st>>>(p);
+  else
+    draft_verify_kernel<8><<<(unsigned)(batch * kDraftCluster), 256, 0, st>>>(p);
   return cuda_check(cudaGetLastError(), "draft_verify_kernel launch");
 }
