@@ -3,12 +3,15 @@
 // values, into pages (palu_paged_append).
 //
 // The work is copying: 256-byte rows in, the same number out, a few flops a
-// channel.  A half-warp takes a run of up to four heads of one token: a lane
-// holds 8 channels (one 16-byte load) of each row, all four rows in flight at
-// once, and the token's angles and the norm's weights stay in registers for
-// the run.  The sum of squares is a 4-step butterfly over the 16 lanes; the
-// other half of a half-split pair sits rope_dim/16 lanes away and comes by
-// shuffle, still packed.  fp32 throughout, one rounding at the store.
+// channel.  A CTA takes 16 consecutive tokens of a run of up to four heads, a
+// half-warp a token: it reads 1 KB a token and writes 4 KB a head where the
+// output is head-major.  A lane holds both members of four pairs (two 8-byte
+// pieces of a row: with 16 contiguous bytes a lane the half-split pairs came by
+// shuffle, and instructions, not memory, were the bound: 67 us for 16,384
+// tokens of 24 + 8 heads), all four rows in flight at once; the token's angles
+// and the norm's weights stay in registers for the run.  The sum of squares is
+// a 4-step butterfly over the 16 lanes.  fp32 throughout, one rounding at the
+// store.
 #include <math.h>
 
 #include <algorithm>
@@ -34,15 +37,17 @@ struct QkParams {
   PagedView c;
 };
 
-// One row of 8 channels a lane: the norm (weight w, where there is one), then the rotation.
+// A row's two pieces of four channels a lane: the norm (by w, where there is
+// one), then the rotation of the lane's four pairs: (x0, x4) .. (x3, x7), or
+// (x0, x1) .. (x6, x7) when interleaved.
 template <bool BF16, bool INTERLEAVED>
-__device__ __forceinline__ uint4 transform_row(const uint4 raw, bool norm, const uint4 w, bool turn, const float (&co)[8],
-                                               const float (&si)[8], int half_lanes, float eps, int lane, unsigned mask) {
+__device__ __forceinline__ void transform_row(uint2& lo, uint2& hi, bool norm, const float (&w)[8], bool turn,
+                                              const float4& co, const float4& si, float eps, unsigned mask) {
   float x[8];
-  const uint32_t* rp = reinterpret_cast<const uint32_t*>(&raw);
+  const uint32_t raw[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<BF16>(rp[i]);
+    const float2 f = unpack2<BF16>(raw[i]);
     x[2 * i] = f.x;
     x[2 * i + 1] = f.y;
   }
@@ -52,51 +57,31 @@ __device__ __forceinline__ uint4 transform_row(const uint4 raw, bool norm, const
     for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
 #pragma unroll
     for (int m = 8; m; m >>= 1) s += __shfl_xor_sync(mask, s, m);
-    const float r = 1.f / sqrtf(s * (1.f / kHeadDim) + eps);
-    const uint32_t* wp = reinterpret_cast<const uint32_t*>(&w);
+    const float r = rsqrtf(s * (1.f / kHeadDim) + eps);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<BF16>(wp[i]);
-      x[2 * i] = x[2 * i] * r * f.x;
-      x[2 * i + 1] = x[2 * i + 1] * r * f.y;
-    }
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
   }
   if (turn) {
-    if (INTERLEAVED) {
-      if (lane < 2 * half_lanes) {
+    const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = a * co[i] - b * si[i];
-          x[2 * i + 1] = b * co[i] + a * si[i];
-        }
-      }
-    } else {
-      // first half: a cos - b sin with b from `half_lanes` up; second: b cos + a sin with a from below
-      const bool low = lane < half_lanes, in = lane < 2 * half_lanes;
-      const int src = low ? lane + half_lanes : in ? lane - half_lanes : lane;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_sync(mask, x[i], src, 16);
-        x[i] = in ? fmaf(low ? -other : other, si[i], x[i] * co[i]) : x[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int j = INTERLEAVED ? 2 * i : i, k = INTERLEAVED ? 2 * i + 1 : i + 4;
+      const float a = x[j], b = x[k];
+      x[j] = a * c[i] - b * s[i];
+      x[k] = b * c[i] + a * s[i];
     }
   }
-  uint4 out;
-  uint32_t* op = reinterpret_cast<uint32_t*>(&out);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) op[i] = pack2<BF16>(x[2 * i], x[2 * i + 1]);
-  return out;
+  lo = make_uint2(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]));
+  hi = make_uint2(pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
 }
 
 template <bool BF16, bool INTERLEAVED, bool PAGED>
 __global__ void __launch_bounds__(kAppendThreads) qk_transform_kernel(const QkParams p) {
   const int lane = threadIdx.x & 15;
   const unsigned mask = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
-  const long long item = (long long)blockIdx.x * (kAppendThreads / 16) + (threadIdx.x >> 4);
-  if (item >= p.rows * p.runs) return;
-  const long long row = item / p.runs;
-  const int run = (int)(item - row * p.runs);
+  const int tile = blockIdx.x / p.runs, run = blockIdx.x - tile * p.runs;
+  const long long row = (long long)tile * (kAppendThreads / 16) + (threadIdx.x >> 4);
+  if (row >= p.rows) return;
   // which heads: queries, keys, then (paged form) values
   const int kind = run < p.q_runs ? 0 : run < p.q_runs + p.k_runs ? 1 : 2;
   const int h0 = (kind == 0 ? run : kind == 1 ? run - p.q_runs : run - p.q_runs - p.k_runs) * kRunHeads;
@@ -106,10 +91,17 @@ __global__ void __launch_bounds__(kAppendThreads) qk_transform_kernel(const QkPa
                         : kind == 1 ? p.k + bi * p.ks0 + ti * p.ks1 + (long long)h0 * p.ks2
                                     : p.v + ti * p.vs1 + (long long)h0 * p.vs2;
   const long long hs = kind == 0 ? p.qs2 : kind == 1 ? p.ks2 : p.vs2;
-  uint4 raw[kRunHeads];
+  // the lane's channels: ca .. ca+3 and cb .. cb+3
+  const bool pairs = lane < (p.tr.rope_dim >> 3);
+  const int ca = !INTERLEAVED && pairs ? 4 * lane : 8 * lane;
+  const int cb = !INTERLEAVED && pairs ? (p.tr.rope_dim >> 1) + 4 * lane : 8 * lane + 4;
+  uint2 lo[kRunHeads], hi[kRunHeads];
 #pragma unroll
   for (int i = 0; i < kRunHeads; ++i)
-    if (i < nh) raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * hs) + lane);
+    if (i < nh) {
+      lo[i] = __ldcs(reinterpret_cast<const uint2*>(src + i * hs + ca));
+      hi[i] = __ldcs(reinterpret_cast<const uint2*>(src + i * hs + cb));
+    }
 
   // the token's place, and whether it may be written
   long long pos = 0, page = 0;
@@ -131,36 +123,32 @@ __global__ void __launch_bounds__(kAppendThreads) qk_transform_kernel(const QkPa
       if (page < 0 || page >= p.c.n_pages) bad = PALU_DEVERR_PAGE;
     }
   }
-  const bool turn = kind < 2 && p.tr.cos_sin != nullptr;
-  float co[8], si[8];
-  const int half_lanes = p.tr.rope_dim >> 4;
+  const bool turn = kind < 2 && pairs;
+  float4 co = {}, si = {};
   if (p.tr.cos_sin != nullptr) {
     if (p.positions) pos = __ldg(p.positions + row);
     if (!bad && (pos < 0 || pos >= p.tr.n_positions)) bad = PALU_DEVERR_POSITION;
-    if (!bad && turn && lane < 2 * half_lanes) {
-      const float* cs = p.tr.cos_sin + pos * p.tr.rope_dim;
-      const int half = p.tr.rope_dim >> 1;
-      if (INTERLEAVED) {
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs + 4 * lane));
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * lane));
-        co[0] = c0.x, co[1] = c0.y, co[2] = c0.z, co[3] = c0.w;
-        si[0] = s0.x, si[1] = s0.y, si[2] = s0.z, si[3] = s0.w;
-      } else {
-        const int l = lane < half_lanes ? lane : lane - half_lanes;
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs + 8 * l)), c1 = __ldg(reinterpret_cast<const float4*>(cs + 8 * l + 4));
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs + half + 8 * l)),
-                     s1 = __ldg(reinterpret_cast<const float4*>(cs + half + 8 * l + 4));
-        co[0] = c0.x, co[1] = c0.y, co[2] = c0.z, co[3] = c0.w, co[4] = c1.x, co[5] = c1.y, co[6] = c1.z, co[7] = c1.w;
-        si[0] = s0.x, si[1] = s0.y, si[2] = s0.z, si[3] = s0.w, si[4] = s1.x, si[5] = s1.y, si[6] = s1.z, si[7] = s1.w;
-      }
+    if (!bad && turn) {
+      const float* cs = p.tr.cos_sin + pos * p.tr.rope_dim + 4 * lane;
+      co = __ldg(reinterpret_cast<const float4*>(cs));
+      si = __ldg(reinterpret_cast<const float4*>(cs + (p.tr.rope_dim >> 1)));
     }
   }
   if (bad && lane == 0 && p.error) atomicOr(p.error, bad);
   if (bad && PAGED && kind > 0) return;  // nothing of it is appended
 
   const uint16_t* wsrc = static_cast<const uint16_t*>(kind == 0 ? p.tr.q_weight : kind == 1 ? p.tr.k_weight : nullptr);
-  uint4 w = {};
-  if (wsrc) w = __ldg(reinterpret_cast<const uint4*>(wsrc) + lane);
+  float w[8] = {};
+  if (wsrc) {
+    const uint2 wl = __ldg(reinterpret_cast<const uint2*>(wsrc + ca)), wh = __ldg(reinterpret_cast<const uint2*>(wsrc + cb));
+    const uint32_t raw[4] = {wl.x, wl.y, wh.x, wh.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2<BF16>(raw[i]);
+      w[2 * i] = f.x;
+      w[2 * i + 1] = f.y;
+    }
+  }
   uint16_t* dst;
   long long ds;  // between heads
   if (PAGED) {
@@ -182,20 +170,19 @@ __global__ void __launch_bounds__(kAppendThreads) qk_transform_kernel(const QkPa
 #pragma unroll
   for (int i = 0; i < kRunHeads; ++i) {
     if (i < nh) {  // the same for all 16 lanes
-      uint4 o = raw[i];
       if (bad)
-        o = make_uint4(nan2, nan2, nan2, nan2);
+        lo[i] = hi[i] = make_uint2(nan2, nan2);
       else if (kind < 2)
-        o = transform_row<BF16, INTERLEAVED>(raw[i], wsrc != nullptr, w, turn, co, si, half_lanes, p.tr.eps, lane, mask);
-      *(reinterpret_cast<uint4*>(dst + i * ds) + lane) = o;
+        transform_row<BF16, INTERLEAVED>(lo[i], hi[i], wsrc != nullptr, w, turn, co, si, p.tr.eps, mask);
+      *reinterpret_cast<uint2*>(dst + i * ds + ca) = lo[i];
+      *reinterpret_cast<uint2*>(dst + i * ds + cb) = hi[i];
     }
   }
 }
 
 template <bool BF16, bool PAGED>
 static palu_status launch_transform(const QkParams& p, cudaStream_t stream) {
-  const long long items = p.rows * p.runs;
-  const long long grid = (items + kAppendThreads / 16 - 1) / (kAppendThreads / 16);
+  const long long grid = (p.rows + kAppendThreads / 16 - 1) / (kAppendThreads / 16) * p.runs;
   if (grid > 0x7fffffff) return fail(PALU_ERR_UNSUPPORTED, "too many rows for one call");
   if (p.tr.interleaved)
     qk_transform_kernel<BF16, true, PAGED><<<(unsigned)grid, kAppendThreads, 0, stream>>>(p);
@@ -255,6 +242,7 @@ extern "C" palu_status palu_qk_norm_rope(const palu_qk_transform* transform, int
     return fail(PALU_ERR_INVALID_ARG, "positions must be given, 8-byte aligned, with a table");
   QkParams p = {};
   p.tr = *transform;
+  if (!p.tr.cos_sin) p.tr.rope_dim = 0;  // no pairs
   p.q = static_cast<const uint16_t*>(q);
   p.k = static_cast<const uint16_t*>(k);
   p.qs0 = q_strides[0], p.qs1 = q_strides[1], p.qs2 = q_strides[2];
@@ -336,6 +324,7 @@ extern "C" palu_status palu_paged_append(const palu_paged_cache* cache, const pa
   if ((uintptr_t)positions & 7) return fail(PALU_ERR_INVALID_ARG, "positions must be 8-byte aligned");
   QkParams p = {};
   p.tr = *transform;
+  if (!p.tr.cos_sin) p.tr.rope_dim = 0;  // no pairs
   p.q = static_cast<const uint16_t*>(q);
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);

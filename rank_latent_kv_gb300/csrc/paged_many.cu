@@ -111,6 +111,18 @@ __device__ __forceinline__ void tc_ld16(uint32_t* r, uint32_t addr) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The loads before it have arrived: r passes through, so that nothing that uses it moves in front.
 __device__ __forceinline__ void tc_wait_ld16(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -284,9 +296,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // Waits on several barriers at once, one a lane: a wait costs about 150 clocks even when there is nothing to wait
     // for.  All lanes see the same outcome, so the control flow is uniform.
     auto wait_all = [&](int count, uint64_t* bar, uint32_t parity) {  // lanes 0 .. count - 1, each its own bar
-      bool done = lane >= count || mbar_try_wait(bar, parity);
+      bool done = lane >= count || mbar_test_wait(bar, parity);
       for (uint32_t i = 0; !__all_sync(0xffffffffu, done); ++i) {
-        if (!done) done = mbar_try_wait(bar, parity);
+        if (!done) done = i < 64 ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);  // it is usually near
         if ((i & 255) == 255 && __any_sync(0xffffffffu, failed() || i > kSpinLimit)) {
           if (lane == 0 && !failed()) {
             *(volatile int*)&sh.failed = 1;
