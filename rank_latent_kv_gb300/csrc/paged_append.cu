@@ -8,7 +8,7 @@
 // output is head-major.  A lane holds both members of four pairs (two 8-byte
 // pieces of a row: with 16 contiguous bytes a lane the half-split pairs came by
 // shuffle, and instructions, not memory, were the bound: 67 us for 16,384
-// tokens of 24 + 8 heads), all four rows in flight at once; the token's angles
+// tokens of 24 + 8 heads instead of 55, 5.0 TB/s), all four rows in flight at once; the token's angles
 // and the norm's weights stay in registers for the run.  The sum of squares is
 // a 4-step butterfly over the 16 lanes.  fp32 throughout, one rounding at the
 // store.
@@ -76,7 +76,7 @@ __device__ __forceinline__ void transform_row(uint2& lo, uint2& hi, bool norm, c
 }
 
 template <bool BF16, bool INTERLEAVED, bool PAGED>
-__global__ void __launch_bounds__(kAppendThreads) qk_transform_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 5) qk_transform_kernel(const QkParams p) {
   const int lane = threadIdx.x & 15;
   const unsigned mask = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
   const int tile = blockIdx.x / p.runs, run = blockIdx.x - tile * p.runs;
@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kAppendThreads) qk_transform_kernel(const QkPa
 #pragma unroll
   for (int i = 0; i < kRunHeads; ++i)
     if (i < nh) {
-      lo[i] = __ldcs(reinterpret_cast<const uint2*>(src + i * hs + ca));
-      hi[i] = __ldcs(reinterpret_cast<const uint2*>(src + i * hs + cb));
+      lo[i] = __ldg(reinterpret_cast<const uint2*>(src + i * hs + ca));
+      hi[i] = __ldg(reinterpret_cast<const uint2*>(src + i * hs + cb));
     }
 
   // the token's place, and whether it may be written

@@ -85,6 +85,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         return !__any_sync(0xffffffffu, *(volatile int*)&sh.failed);
       };
       plan_walk<R>(p, &sh.plan, [&](const UnitMeta& u) -> bool {
+        if (lane < u.rows) {  // the unit's queries, to L2 while the tiles before it are worked on
+          const uint16_t* q = row_query(p, u, lane);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+        }
         for (int k = 0; k < u.n; ++k, ++it) {
           const int st = it % kFewStages, key0 = u.key0 + k * kKeyTile, valid = min(kKeyTile, u.key_end - key0);
           const int pages = (valid + p.c.page - 1) >> p.c.page_shift;
