@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = nt * 8 + 2 * c + e;
-              lim[nt][e] = r < m.rows ? unit_row_limit(p, m, r) : 0;
+              lim[nt][e] = r < m.rows ? unit_row_limit(p, sh.plan, m, r) : 0;
               m_run[nt][e] = -INFINITY;
               l_run[nt][e] = 0.f;
             }

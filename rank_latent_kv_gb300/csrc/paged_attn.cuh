@@ -77,19 +77,20 @@ struct AttnParams {
 // end it, and a 128-key tile of it.
 template <int R>
 struct LineCost {
-  static __device__ int unit(int rows) { return 2; }
-  static __device__ int tile(int rows) { return 1; }
+  static __device__ int unit(int rows) { return 2; }  // 5,700 clocks
+  static __device__ int tile(int rows) { return 1; }  // 2,900
   static constexpr int kMaxTile = 1;
 };
-// Measured in units of 850 clocks: 1520 units of 256 rows and 4 tiles take
-// 34,000 clocks each, of 40 rows and 1 or 4 tiles 15,000 and 22,600; a tile of 256
-// rows in a long unit 3,400.
+// In units of 200 clocks, measured: 1520 units of 256 rows and 4 tiles take
+// 34,000 clocks each, of 40 rows and 1 or 4 tiles 15,000 and 22,600; in long
+// units a tile of 256 rows takes 3,100 and one of up to 128 rows 2,900 (the
+// time of its 64 KB at memory speed).
 constexpr int kManyRows = 256;
 template <>
 struct LineCost<kManyRows> {
-  static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 24 : 15; }
-  static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 4 : 3; }
-  static constexpr int kMaxTile = 4;
+  static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 100 : 60; }
+  static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 16 : 14; }
+  static constexpr int kMaxTile = 16;
 };
 
 // Row r (of a unit) -> token and query head, r < 256: g0 + r < 320 and Gq <= 64,
@@ -154,6 +155,10 @@ __device__ __forceinline__ long long seq_ticks(const SeqSpan& s, int rts, int Gq
 }
 template <int R>
 __device__ __forceinline__ long long seq_ticks(const SeqSpan& s, int Gq, int S0, int kv_heads) {
+  if (s.n * Gq <= R) {  // one row tile, the usual case: its last token sees everything
+    const int keys = s.n ? s.len - S0 : 0;
+    return unit_ticks<R>(s.n * Gq, keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 0) * kv_heads;
+  }
   return seq_ticks<R>(s, (s.n * Gq + R - 1) / R, Gq, S0, kv_heads);
 }
 
@@ -176,6 +181,7 @@ struct PlanScratch {
   long long warp_sum[16];
   long long w0, w1, W, base;
   int b;
+  int cut_prefix;  // a sequence does not see the whole prefix with all of its new tokens
 };
 
 template <int R>
@@ -189,9 +195,16 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   unsigned bad = 0;
   long long mine = 0;
-  if (p.do_own)
+  if (tid == 0) {
+    sc->b = -1;
+    sc->cut_prefix = 0;
+  }
+  __syncthreads();
+  if (p.do_own || p.do_prefix)
     for (int b = b0; b < b1; ++b) {
       const SeqSpan s = seq_span(p, b, &bad);
+      if (s.n && row_limit(s, 0) < p.S0) sc->cut_prefix = 1;
+      if (!p.do_own) continue;
       mine += seq_ticks<R>(s, p.Gq, p.S0, Hkv);
       // without a prefix nothing joins parts of every row: rows that see nothing are zeroed here
       if (p.S0 == 0 && b % (int)gridDim.x == (int)blockIdx.x) {
@@ -208,7 +221,6 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
     if (lane >= x) incl += y;
   }
   if (lane == 31) sc->warp_sum[warp] = incl;
-  if (tid == 0) sc->b = -1;
   __syncthreads();
   long long before = prefix, total = prefix;
   for (int w = 0; w < nwarp; ++w) {
@@ -227,7 +239,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
       long long base = before;
       for (int b = b0; b < b1; ++b) {
         if (blockIdx.x == 0) p.part.plan[1 + b] = base;
-        const long long t = seq_ticks<R>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
+        const long long t = per == 1 ? mine : seq_ticks<R>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
         if (here && at >= base && at < base + t) {
           sc->b = b;
           sc->base = base;
@@ -320,7 +332,8 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
 }
 
 // The limit of a row of the unit: how many of the sequence's tokens it sees.
-__device__ __forceinline__ int unit_row_limit(const AttnParams& p, const UnitMeta& m, int r) {
+__device__ __forceinline__ int unit_row_limit(const AttnParams& p, const PlanScratch& sc, const UnitMeta& m, int r) {
+  if (m.prefix && !sc.cut_prefix) return p.S0;
   int tok, head;
   row_place(p, m, r, &tok, &head);
   if (!m.prefix) return m.pos + (tok - m.tok) + 1;

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
       const int r = (both ? s * kHalf : 0) + t;  // row of the unit
       const bool live = r < m.rows;
-      const int lim = live ? unit_row_limit(p, m, r) : 0x7fffffff;
+      const int lim = live ? unit_row_limit(p, sh.plan, m, r) : 0x7fffffff;
       float ref = 0.f, l = 0.f;  // the maximum in use (in units of log2), the sum
       bool seen = false;         // whether ref is a maximum yet
       const int step = both ? 1 : 2;
