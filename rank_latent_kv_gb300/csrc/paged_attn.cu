@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     sh.failed = 0;
     fence_mbar_init();
   }
-  plan_start<R>(p, &sh.plan);
+  plan_start<R, kFewThreads>(p, &sh.plan, tid);  // all threads meet in it
   if (sh.plan.w1 > sh.plan.w0) {
     if (warp == kFewWarps) {
       // ---- the loading warp

@@ -176,7 +176,8 @@ __host__ __device__ inline int prefix_tiles_of(int S0) { return (S0 + kKeyTile -
 // Where a finished unit goes.
 enum { kToOut = -1, kToRow = -2 };
 
-// The CTA's stretch of the line, found by the whole CTA (blockDim.x threads).
+// The CTA's stretch of the line, found by THREADS of its threads, tid 0 ..
+// THREADS - 1, which meet at named barrier 3.
 struct PlanScratch {
   long long warp_sum[16];
   long long w0, w1, W, base;
@@ -184,9 +185,11 @@ struct PlanScratch {
   int cut_prefix;  // a sequence does not see the whole prefix with all of its new tokens
 };
 
-template <int R>
-__device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc) {
-  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, nwarp = nthr >> 5;
+template <int R, int THREADS>
+__device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc, int tid) {
+  constexpr int nthr = THREADS, nwarp = THREADS / 32;
+  const int warp = tid >> 5, lane = tid & 31;
+  auto meet = [] { asm volatile("bar.sync 3, %0;" ::"n"(THREADS) : "memory"); };
   const int B = p.c.batch, Hkv = p.c.kv_heads;
   const int all_rows = p.N * p.Gq;
   const long long prefix =
@@ -199,7 +202,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
     sc->b = -1;
     sc->cut_prefix = 0;
   }
-  __syncthreads();
+  meet();
   if (p.do_own || p.do_prefix)
     for (int b = b0; b < b1; ++b) {
       const SeqSpan s = seq_span(p, b, &bad);
@@ -221,8 +224,9 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
     if (lane >= x) incl += y;
   }
   if (lane == 31) sc->warp_sum[warp] = incl;
-  __syncthreads();
+  meet();
   long long before = prefix, total = prefix;
+#pragma unroll
   for (int w = 0; w < nwarp; ++w) {
     if (w < warp) before += sc->warp_sum[w];
     total += sc->warp_sum[w];
@@ -256,7 +260,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc)
     if (blockIdx.x == 0) p.part.plan[0] = W;
     p.part.begun[blockIdx.x].rows = 0;
   }
-  __syncthreads();
+  meet();
 }
 
 // Calls unit(meta) for each unit of which the CTA's stretch of the line has

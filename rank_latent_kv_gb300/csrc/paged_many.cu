@@ -226,9 +226,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
   if (warp == 9) tc_alloc(&sh.tmem);
   tc_fence_before();
-  plan_start<kManyRows>(p, &sh.plan);  // ends with __syncthreads
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // planned by the warps that load and issue: the others would only wait for the same code to arrive
+  if (warp >= 8) plan_start<kManyRows, kManyThreads - 256>(p, &sh.plan, tid - 256);
   auto failed = [&] { return *(volatile int*)&sh.failed != 0; };
 
   if (warp == 8) {
