@@ -40,11 +40,15 @@ namespace palu {
 
 constexpr int kManyThreads = 352;
 constexpr int kRing = 5;
+// Two arrival barriers a ring slot, used in turn: where the halves have tiles of their own, one may ask for an item
+// while the slot's item before it, the other half's, is still on its way, and one barrier's parity could not tell the
+// two apart.
+constexpr int kFull = 2 * kRing;
 constexpr int kHalf = 128;
 constexpr int kStageBytes = 32 * 36 * 4;  // a warp's 32 rows of 32 columns, padded against bank conflicts
 
 struct ManySmem {
-  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t kv_full[kFull], kv_empty[kRing];
   uint64_t meta_full[2], meta_empty[2];
   uint64_t q_full, s_full[2], p_full[2][2], unit_done, join, drain[2], token[2];
   UnitMeta meta[2];
@@ -204,8 +208,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   unsigned* const err = p.c.error;
   grid_dep_launch();
   if (tid == 0) {
+    for (int i = 0; i < kFull; ++i) mbar_init(&sh.kv_full[i], 1);
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 2);  // both halves, or one of them twice
     }
     for (int i = 0; i < 2; ++i) {
@@ -271,12 +275,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const int st = item % kRing;
           if (item >= kRing) wait_or_fail(&sh.kv_empty[st], (item / kRing - 1) & 1, &sh.failed, err);
           if (__any_sync(0xffffffffu, failed())) return ok = false;
-          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], bytes);
+          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[item % kFull], bytes);
           __syncwarp();
           if (page >= 0) {
             const uint32_t dst = smem_addr(ring + st * kTileBytes) + lane * p.c.page * 128;
-            tma_page(dst, kv ? &vmap : &kmap, &sh.kv_full[st], 0, u.kh, page);
-            tma_page(dst + kPanelBytes, kv ? &vmap : &kmap, &sh.kv_full[st], 64, u.kh, page);
+            tma_page(dst, kv ? &vmap : &kmap, &sh.kv_full[item % kFull], 0, u.kh, page);
+            tma_page(dst + kPanelBytes, kv ? &vmap : &kmap, &sh.kv_full[item % kFull], 64, u.kh, page);
           }
         }
       }
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     if (bad) atomicOr(err, bad);
     // no copy is in flight when the block ends, also where the others gave up
     for (int i = max(item - kRing, 0); i < item; ++i)
-      if (!mbar_wait_bounded(&sh.kv_full[i % kRing], (i / kRing) & 1)) break;
+      if (!mbar_wait_bounded(&sh.kv_full[i % kFull], (i / kFull) & 1)) break;
   } else if (warp >= 9) {
     // ---- products of half s
     const int s = warp - 9;
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       bool ok = true;
       if (j0 < n) {
         const int it = 2 * (tile0 + j0);
-        if (!wait(&sh.kv_full[it % kRing], (it / kRing) & 1)) break;
+        if (!wait(&sh.kv_full[it % kFull], (it / kFull) & 1)) break;
         if (elect_one()) {
           scores(tile0 + j0);
           release(it);
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       for (int j = j0; j < n; j += step) {
         const int t = tile0 + j, vi = 2 * t + 1, ki = 2 * (t + step);
         const bool more = j + step < n;
-        ok = wait_all(2, lane ? &sh.kv_full[vi % kRing] : &sh.p_full[s][0], lane ? (vi / kRing) & 1 : pc & 1);
+        ok = wait_all(2, lane ? &sh.kv_full[vi % kFull] : &sh.p_full[s][0], lane ? (vi / kFull) & 1 : pc & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) values(0, t, j >= step);
@@ -369,9 +373,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         // the softmax and then both waiting for the tensor cores (3,900 clocks a tile pair).
         ok = wait_all(!more ? 1 : both ? 3 : 2,
                       lane == 0   ? &sh.p_full[s][1]
-                      : lane == 1 ? &sh.kv_full[ki % kRing]
+                      : lane == 1 ? &sh.kv_full[ki % kFull]
                                   : &sh.token[s],
-                      lane == 0 ? pc & 1 : lane == 1 ? (ki / kRing) & 1 : turns & 1);
+                      lane == 0 ? pc & 1 : lane == 1 ? (ki / kFull) & 1 : turns & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           // the last tile's values behind the last key: 0 * NaN is NaN, so they are zeroed before the product (by both
           // halves, where both use them)
           const int vi = 2 * (tile0 + j) + 1;
-          wait_or_fail(&sh.kv_full[vi % kRing], (vi / kRing) & 1, &sh.failed, err);
+          wait_or_fail(&sh.kv_full[vi % kFull], (vi / kFull) & 1, &sh.failed, err);
           const uint32_t v_tile = smem_addr(ring + (vi % kRing) * kTileBytes);
           for (int i = t; i < (kKeyTile - valid) * 16; i += kHalf)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(panel_addr(v_tile, valid + (i >> 4), i & 15)), "r"(0)

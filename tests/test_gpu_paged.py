@@ -362,6 +362,32 @@ def test_shared_prefix_does_not_change_the_result(P):
         attend_close(c.attend(q, offsets_of(new), 4, shared_pages=s), ref, mag, torch.bfloat16)
 
 
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("Hk,new", [(1, 5), (2, 40)])
+def test_long_units_on_all_sms(P, page, Hk, new):
+    """More sequences than SMs, each long: the tiles of a unit of up to 128 rows go to two independent halves, those of
+    a larger one to both.  Compared with the same tokens attended one at a time (another kernel); A of the bar is
+    the same attention over |v|."""
+    B, G, S = 160, 8 // Hk if new == 5 else 4, 4096 + 100
+    g = torch.Generator(device=DEV).manual_seed(page + new)
+    width = -(-S // page)
+    ids = torch.randperm(B * width, generator=g, device=DEV).view(B, width).to(torch.int32)
+    k, v = (torch.randn(B * width, Hk, page, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    lengths = S - torch.arange(B, device=DEV, dtype=torch.int64) * 7 % 1000
+    c = P.PagedCache(k, v, ids, lengths)
+    q = torch.randn(B, new, Hk * G, D, generator=g, device=DEV).bfloat16()
+    off = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+    out = [c.attend(q.view(B * new, Hk * G, D), off * new, new).view(q.shape) for _ in range(3)]
+    assert c.sync() == 0 and torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+    eps = torch.finfo(torch.bfloat16).eps
+    for i in sorted({0, 1, new // 2, new - 1}):
+        at = lengths - (new - 1 - i)
+        one = P.PagedCache(k, v, ids, at).attend(q[:, i].contiguous(), off, 1).float()
+        mag = P.PagedCache(k, v.abs(), ids, at).attend(q[:, i].contiguous(), off, 1).float()
+        bar = (eps / 2 + 2.0 ** -12) * mag * (1 + eps) + eps * one.abs() * (1 + eps)   # two roundings of the output
+        assert bool(((out[0][:, i].float() - one).abs() <= bar).all())
+
+
 def test_calls_repeat_bit_for_bit(P):
     pools, dev, c = make_cache(P, torch.float16, [3000, 17, 900], 32, 4, seed=22, shared=0)
     q = torch.randn(15, 12, D, generator=torch.Generator().manual_seed(5)).half().to(DEV)
