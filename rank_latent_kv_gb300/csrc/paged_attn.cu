@@ -497,8 +497,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     const int b = w.b, kh = w.kh, gi = w.gi, i = w.i, tok = s.tok0 + i;
     auto parts = [](const PartSet& ps, long long f, int n, int t, int r) {
       const long long W = __ldcg(ps.plan);
-      const int first = (int)(f / W);
-      return Parts{first, n ? (int)((f + (long long)(n - 1) * t) / W) - first + 1 : 0, r};
+      const int first = div_small(f, W);
+      return Parts{first, n ? div_small(f + (long long)(n - 1) * t, W) - first + 1 : 0, r};
     };
     long long f;
     int n, t;
@@ -571,6 +571,8 @@ static palu_status page_map(CUtensorMap* map, const palu_paged_cache* c, const v
   return PALU_OK;
 }
 
+constexpr int kOneLaunchKeys = 256;  // own keys a sequence up to which one launch takes them with a prefix of many rows
+
 // Sizes that the host can know: which kernel takes the shared and which the
 // own keys, and the workspace's parts.
 struct AttnLayout {
@@ -593,8 +595,13 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     return fail(PALU_ERR_INVALID_ARG, "shared_pages must be in [0, table_width]");
   const int64_t own_rows = std::min<int64_t>(max_new, tokens) * Gq, all_rows = tokens * Gq;
   l->shared = shared_pages > 0 && c->batch > 1;
-  l->R_own = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
   l->R_prefix = all_rows <= 8 ? 8 : all_rows <= 16 ? 16 : kManyRows;
+  l->R_own = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
+  // Few own keys behind a prefix of many rows: one launch for both (256 rows behind 311,296 shared tokens and 1 own token
+  // a sequence: 65 us in two launches, 55 in one; 96 rows behind 8192 and 580 own: 46 and 50).
+  if (l->shared && l->R_prefix == kManyRows &&
+      (int64_t)(c->table_width - shared_pages) * c->page_size <= kOneLaunchKeys)
+    l->R_own = kManyRows;
   l->one_launch = l->shared && l->R_own == kManyRows;  // then the prefix has many rows, too
   const size_t slots = 2 * (size_t)device_sm_count();
   size_t o = 0;

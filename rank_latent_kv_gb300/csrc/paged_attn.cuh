@@ -137,6 +137,15 @@ __device__ __forceinline__ int own_tiles(const SeqSpan& s, int row0, int rows, i
   return keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 0;
 }
 
+// a / b, for quotients below 2^17 (CTAs, KV heads): a float estimate and its
+// correction, where a 64-bit division is a hundred instructions to be fetched.
+__device__ __forceinline__ int div_small(long long a, long long b) {
+  int q = (int)__fdividef((float)a, (float)b);
+  while ((long long)q * b > a) --q;
+  while ((long long)(q + 1) * b <= a) ++q;
+  return q;
+}
+
 // Ticks of a unit of n tiles.
 template <int R>
 __device__ __forceinline__ long long unit_ticks(int rows, int n) {
@@ -275,7 +284,12 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
   auto run_unit = [&](long long u0, int n, int key_base, int key_end) -> bool {
     const int t = LineCost<R>::tile(m.rows);
     const long long f = u0 + LineCost<R>::unit(m.rows);
-    auto before = [&](long long x) { return x <= f ? 0 : (int)min((long long)n, (x - f + t - 1) / t); };
+    // tiles that begin before x
+    auto before = [&](long long x) -> int {
+      if (x <= f) return 0;
+      if (x - f >= (long long)n * t) return n;
+      return ((int)(x - f) + t - 1) / t;  // n * t < 2^28
+    };
     const int k0 = before(w0), k1 = before(w1);
     if (k0 == k1) return true;
     m.dest = k0 > 0 ? 2 * cta : k1 < n ? 2 * cta + 1 : p.S0 > 0 ? kToRow : kToOut;
@@ -283,7 +297,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
     m.key_end = key_end;
     m.n = k1 - k0;
     if (m.dest == 2 * cta + 1) {
-      m.parts = (int)((f + (long long)(n - 1) * t) / sc->W) - cta + 1;
+      m.parts = div_small(f + (long long)(n - 1) * t, sc->W) - cta + 1;
       if ((threadIdx.x & 31) == 0) p.part.begun[cta] = m;
     }
     return unit(m);
@@ -295,8 +309,8 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
     m.pos = m.seq = 0;
     m.prefix = 1;
     if (w0 < head * Hkv) {
-      m.kh = (int)(w0 / head);
-      int rt = (int)min((w0 - m.kh * head) / full, (long long)rts - 1);
+      m.kh = div_small(w0, head);
+      int rt = min(div_small(w0 - m.kh * head, full), rts - 1);
       for (; m.kh < Hkv; ++m.kh, rt = 0)
         for (; rt < rts; ++rt) {
           const long long u0 = m.kh * head + rt * full;
@@ -324,7 +338,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
       m.tok = s.tok0 + i;
       m.g0 = rt * R - i * p.Gq;
       m.pos = s.len - s.n + i;
-      m.kh = w0 > base ? (int)min((w0 - base) / ticks, (long long)Hkv) : 0;
+      m.kh = w0 <= base ? 0 : w0 - base >= ticks * Hkv ? Hkv : div_small(w0 - base, ticks);
       for (; m.kh < Hkv; ++m.kh) {
         const long long u0 = base + m.kh * ticks;
         if (u0 >= w1) return;
