@@ -576,11 +576,38 @@ constexpr int kOneLaunchKeys = 256;  // own keys a sequence up to which one laun
 // Sizes that the host can know: which kernel takes the shared and which the
 // own keys, and the workspace's parts.
 struct AttnLayout {
+  int grid_prefix, grid_own;
   bool shared;       // the prefix is a part of its own
   bool one_launch;   // both parts on the kernel for many rows
   int R_prefix, R_own;
   size_t plan_p, begun_p, ml_p, acc_p, plan_o, begun_o, ml_o, acc_o, row_ml, row_acc, total;
 };
+
+// SMs for the prefix where it and the own keys are two launches: they run side
+// by side, each on SMs of its own, because a launch's beginning and end (about
+// 25,000 and 10,000 clocks: its code has to be fetched) leave the memory idle.
+// The own lengths are not known here: half of what the page table allows.
+static int split_grid(const palu_paged_cache* c, int64_t all_rows, int32_t shared_pages, int R_prefix, int grid) {
+  const int64_t t0 = prefix_tiles_of(shared_pages * c->page_size);
+  const int64_t own = ((int64_t)(c->table_width - shared_pages) * c->page_size / 2 + kKeyTile - 1) / kKeyTile;
+  const int64_t full = all_rows / R_prefix, rest = all_rows % R_prefix;
+  double a;  // clocks of one SM
+  if (R_prefix == kManyRows)
+    a = c->kv_heads * (full * (20000. + 3100. * t0) + (rest > kManyRows / 2 ? 20000. + 3100. * t0 : rest ? 12500. + 2900. * t0 : 0.));
+  else
+    a = c->kv_heads * (5700. + 2900. * t0);
+  const double b = (double)c->batch * c->kv_heads * (5700. + 2900. * own);
+  int best = grid / 2;
+  double least = INFINITY;
+  for (int g = 1; g < grid; ++g) {
+    const double t = std::max(25000. + a / g, 10000. + b / (grid - g));
+    if (t < least) {
+      least = t;
+      best = g;
+    }
+  }
+  return best;
+}
 
 static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_t q_heads, int32_t max_new,
                                int32_t shared_pages, AttnLayout* l) {
@@ -611,6 +638,9 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     return at;
   };
   const bool two = l->shared && !l->one_launch;
+  const int grid = device_sm_count();
+  l->grid_prefix = two && grid > 1 ? split_grid(c, all_rows, shared_pages, l->R_prefix, grid) : grid;
+  l->grid_own = two && grid > 1 ? grid - l->grid_prefix : grid;
   l->plan_p = two ? take(sizeof(long long) * (1 + (size_t)c->batch)) : 0;
   l->begun_p = two ? take(slots / 2 * sizeof(UnitMeta)) : 0;
   l->ml_p = two ? take(slots * l->R_prefix * sizeof(float2)) : 0;
@@ -692,13 +722,13 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   p.gq_mul = (65536 + p.Gq - 1) / p.Gq;
   p.S0 = l.shared ? shared_pages * cache->page_size : 0;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
-  const int grid = device_sm_count();
   const PartSet own = {reinterpret_cast<float2*>(ws + l.ml_o), reinterpret_cast<float*>(ws + l.acc_o),
-                       reinterpret_cast<long long*>(ws + l.plan_o), reinterpret_cast<UnitMeta*>(ws + l.begun_o), grid, l.R_own};
+                       reinterpret_cast<long long*>(ws + l.plan_o), reinterpret_cast<UnitMeta*>(ws + l.begun_o), l.grid_own,
+                       l.R_own};
   const PartSet prefix = l.one_launch ? own
                                       : PartSet{reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
-                                                reinterpret_cast<long long*>(ws + l.plan_p), reinterpret_cast<UnitMeta*>(ws + l.begun_p), grid,
-                                                l.R_prefix};
+                                                reinterpret_cast<long long*>(ws + l.plan_p), reinterpret_cast<UnitMeta*>(ws + l.begun_p),
+                                                l.grid_prefix, l.R_prefix};
   const bool bf16 = cache->dtype == PALU_TYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (l.shared && !l.one_launch) {
@@ -712,11 +742,11 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   if ((st = launch_part(p, km, vm, bf16, l.shared && !l.one_launch, s)) != PALU_OK) return st;
   if (!l.shared) {
     if (l.R_own < kManyRows) {
-      const dim3 jgrid(grid, l.R_own);
+      const dim3 jgrid(l.grid_own, l.R_own);
       return bf16 ? launch(paged_join_units_kernel<true, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p)
                   : launch(paged_join_units_kernel<false, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p);
     }
-    const dim3 jgrid(grid, l.R_own / kJoinWarps);
+    const dim3 jgrid(l.grid_own, l.R_own / kJoinWarps);
     return bf16 ? launch(paged_join_units_kernel<true, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
                          "paged_join_units_kernel launch", p)
                 : launch(paged_join_units_kernel<false, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
