@@ -117,7 +117,7 @@ palu_status palu_paged_cache_init(palu_paged_cache* cache, int32_t dtype, int32_
  *          [tokens, kv_heads, 128]; alignment as in palu_qk_norm_rope.
  *   positions  device int64 [tokens], the positions of the rotation; NULL:
  *          each token's place in its sequence.
- *   q_out  device [tokens, q_heads, 128] contiguous.
+ *   q_out  device [tokens, q_heads, 128] contiguous, not overlapping q, k or v.
  * Refused on the device, with a bit of the error word (the tokens are not
  * appended and their q_out rows are NaN): a sequence whose length passes
  * table_width * page_size (CAPACITY), is less than n_b, or whose offsets are
@@ -145,12 +145,17 @@ palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_
  *          row of the table: their keys and values are read once for the
  *          whole batch (from row 0 of the table).  0: nothing is shared.  The
  *          result does not depend on it.
- *   out    device [tokens, q_heads, 128], contiguous, the cache's type; rows
- *          at and behind offsets[batch] are not touched.
+ *   out    device [tokens, q_heads, 128], contiguous, the cache's type, not
+ *          overlapping q; rows at and behind offsets[batch] are not touched.
  *   softmax_scale 0 selects 1/sqrt(128).
  * A row that sees no token (a length of 0, or less than n_b) gets zeros.
  * What the pages hold behind a sequence's length does not matter, NaN and
- * infinities included.  A sequence with more than max_new rows or offsets out
+ * infinities included; the values of its own tokens have to be finite (a
+ * token that a query does not see yet has the weight 0, and 0 * NaN is NaN).
+ * Weights are rounded to the cache's type once, where a KV head has more than
+ * 16 rows; sums, maxima and accumulators are fp32.  One to three kernel
+ * launches on `stream`, chosen by the sizes given here, not by the lengths.
+ * The results do not depend on the run.  A sequence with more than max_new rows or offsets out
  * of order sets PALU_DEVERR_SPAN and its rows are zeros; a length past the
  * table sets PALU_DEVERR_CAPACITY and is cut to it; a page id outside the
  * pool sets PALU_DEVERR_PAGE and page 0 is read for it. */

@@ -46,6 +46,10 @@ inline PagedView paged_view(const palu_paged_cache* c) {
 // PALU_OK, or why the descriptor cannot be used.
 palu_status paged_check(const palu_paged_cache* c);
 
+// Whether the contiguous 16-bit rows of an output share memory with a strided
+// operand of these extents (by their address ranges).
+bool rows_overlap(const void* out, int64_t out_rows, const void* in, const int64_t* strides, const int64_t* extents, int n);
+
 // Largest b in [0, batch) with offsets[b] <= row, searched by 16 lanes at
 // once (`lane` 0..15; `mask` their lanes of the warp): each step cuts the range
 // to a sixteenth, so the dependent loads are one for up to 16 sequences and

@@ -214,6 +214,13 @@ static palu_status rows_check(const char* name, const void* p, const int64_t* st
   return PALU_OK;
 }
 
+bool rows_overlap(const void* out, int64_t out_rows, const void* in, const int64_t* strides, const int64_t* extents, int n) {
+  int64_t span = kHeadDim;
+  for (int i = 0; i < n; ++i) span += (extents[i] - 1) * strides[i];
+  const char *o = static_cast<const char*>(out), *x = static_cast<const char*>(in);
+  return o < x + 2 * span && x < o + 2 * out_rows * kHeadDim;
+}
+
 palu_status paged_check(const palu_paged_cache* c) {
   if (!c) return fail(PALU_ERR_INVALID_ARG, "cache is NULL");
   if (c->magic != kPagedMagic) return fail(PALU_ERR_NOT_INITIALIZED, "paged cache is not initialised");
@@ -238,6 +245,11 @@ extern "C" palu_status palu_qk_norm_rope(const palu_qk_transform* transform, int
   if ((st = rows_check("q", q, q_strides, 3)) != PALU_OK || (st = rows_check("k", k, k_strides, 3)) != PALU_OK) return st;
   if (!q_out || !k_out || (((uintptr_t)q_out | (uintptr_t)k_out) & 15))
     return fail(PALU_ERR_INVALID_ARG, "q_out and k_out must be 16-byte aligned");
+  const int64_t qe[3] = {batch, tokens, q_heads}, ke[3] = {batch, tokens, kv_heads};
+  const int64_t q_rows = batch * tokens * q_heads, k_rows = batch * tokens * kv_heads;
+  if (rows_overlap(q_out, q_rows, q, q_strides, qe, 3) || rows_overlap(q_out, q_rows, k, k_strides, ke, 3) ||
+      rows_overlap(k_out, k_rows, q, q_strides, qe, 3) || rows_overlap(k_out, k_rows, k, k_strides, ke, 3))
+    return fail(PALU_ERR_INVALID_ARG, "an output overlaps an input");
   if (transform->cos_sin && (!positions || ((uintptr_t)positions & 7)))
     return fail(PALU_ERR_INVALID_ARG, "positions must be given, 8-byte aligned, with a table");
   QkParams p = {};
@@ -322,6 +334,10 @@ extern "C" palu_status palu_paged_append(const palu_paged_cache* cache, const pa
   if ((st = rows_check("k", k, k_strides, 2)) != PALU_OK || (st = rows_check("v", v, v_strides, 2)) != PALU_OK) return st;
   if ((uintptr_t)q_out & 15) return fail(PALU_ERR_INVALID_ARG, "q_out must be 16-byte aligned");
   if ((uintptr_t)positions & 7) return fail(PALU_ERR_INVALID_ARG, "positions must be 8-byte aligned");
+  const int64_t qe[2] = {tokens, q_heads}, ke[2] = {tokens, cache->kv_heads};
+  if (q && (rows_overlap(q_out, tokens * q_heads, q, q_strides, qe, 2) || rows_overlap(q_out, tokens * q_heads, k, k_strides, ke, 2) ||
+            rows_overlap(q_out, tokens * q_heads, v, v_strides, ke, 2)))
+    return fail(PALU_ERR_INVALID_ARG, "q_out overlaps an input");
   QkParams p = {};
   p.tr = *transform;
   if (!p.tr.cos_sin) p.tr.rope_dim = 0;  // no pairs

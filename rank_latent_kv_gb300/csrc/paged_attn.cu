@@ -699,6 +699,8 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   for (int i = 0; i < 2; ++i)
     if (q_strides[i] < 0 || q_strides[i] % 8)
       return fail(PALU_ERR_INVALID_ARG, "q's strides must be non-negative multiples of 8 elements");
+  const int64_t qe[2] = {tokens, q_heads};
+  if (rows_overlap(out, tokens * q_heads, q, q_strides, qe, 2)) return fail(PALU_ERR_INVALID_ARG, "out overlaps q");
   if (!(softmax_scale >= 0.f) || isinf(softmax_scale))
     return fail(PALU_ERR_INVALID_ARG, "softmax_scale must be finite and not negative");
   if (workspace_bytes < l.total) return fail(PALU_ERR_INVALID_ARG, "workspace too small");

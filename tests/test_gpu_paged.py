@@ -307,6 +307,44 @@ def test_rows_that_see_nothing_are_zero(P, dt, shared):
     attend_close(out, ref, mag, DT[dt])
 
 
+@pytest.mark.parametrize("Hq,Hk,new", [(4, 2, 1), (6, 1, 3)])
+def test_many_short_sequences(P, Hq, Hk, new):
+    """A thousand sequences, many without new tokens, some empty: more than a CTA's threads."""
+    rng = np.random.default_rng(new)
+    B = 1000
+    counts = [int(rng.integers(0, new + 1)) for _ in range(B)]
+    lengths = [max(int(rng.integers(0, 60)), n) for n in counts]
+    pools, dev, c = make_cache(P, torch.float16, lengths, 16, Hk, seed=8, width=4)
+    n = sum(counts)
+    q = torch.randn(n, Hq, D, generator=torch.Generator().manual_seed(7)).half()
+    out = c.attend(q.to(DEV), offsets_of(counts), new)
+    assert c.sync() == 0
+    ref, mag = ref_attend(q, pools, c.page_table.cpu(), lengths, counts, 16)
+    attend_close(out, ref, mag, torch.float16)
+    k, v = torch.randn(2, n, Hk, D, generator=torch.Generator().manual_seed(9)).half()
+    c.append(k.to(DEV), v.to(DEV), offsets_of(counts))
+    ids, row = c.page_table.cpu().long(), 0
+    for b, m in enumerate(counts):
+        for t in range(lengths[b] - m, lengths[b]):
+            pools[0][ids[b, t // 16], :, t % 16], pools[1][ids[b, t // 16], :, t % 16] = k[row], v[row]
+            row += 1
+    assert torch.equal(dev[0].cpu(), pools[0]) and torch.equal(dev[1].cpu(), pools[1])
+
+
+def test_no_new_tokens_at_all(P):
+    """Offsets of zero throughout: padded rows only, nothing is touched."""
+    for shared in (0, 2):
+        pools, dev, c = make_cache(P, torch.bfloat16, [40, 0, 33], 16, 2, width=3, shared=shared)
+        off = torch.zeros(4, dtype=torch.int32, device=DEV)
+        for n, mx in ((3, 1), (40, 40)):
+            q = torch.zeros(n, 8, D, dtype=torch.bfloat16, device=DEV)
+            out = torch.full((n, 8, D), 7.0, dtype=torch.bfloat16, device=DEV)
+            c.attend(q, off, mx, shared_pages=shared, out=out)
+            c.append(q[:, :2], q[:, 2:4], off)
+            assert (out == 7).all() and c.sync() == 0
+        assert torch.equal(dev[0].cpu(), pools[0])
+
+
 def test_large_scores_scale_and_flat_rows(P):
     lengths, new = [400, 250], [1, 12]
     pools, dev, c = make_cache(P, torch.float16, lengths, 32, 2, seed=9)
@@ -486,7 +524,8 @@ def test_python_refusals(P):
         lambda: c.attend(q, off.long(), 2), lambda: c.attend(q, off[:2], 2), lambda: c.attend(q, off, 0),
         lambda: c.attend(q, off, 2, shared_pages=4), lambda: c.attend(q, off, 2, shared_pages=-1),
         lambda: c.attend(q, off, 2, softmax_scale=-1.0), lambda: c.attend(q, off, 2, softmax_scale=float("nan")),
-        lambda: c.attend(q, off, 2, out=q[:2]), lambda: c.attend(q, off, 2, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV)),
+        lambda: c.attend(q, off, 2, out=q[:2]), lambda: c.attend(q, off, 2, out=q),
+        lambda: c.append(k, k, off, q=q, q_out=q), lambda: P.qk_norm_rope(q[None], k[None], None, q_out=q.view(1, 4, 3, D)), lambda: c.attend(q, off, 2, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV)),
         lambda: c.attend(torch.zeros(3, 4, 2 * D, dtype=torch.float16, device=DEV)[..., ::2], off, 2),
         lambda: c.attend(torch.zeros(3 * 4 * D + 4, dtype=torch.float16, device=DEV)[4:].view(3, 4, D), off, 2),
         lambda: c.append(k, k[:2], off), lambda: c.append(k[:, :1], k[:, :1], off), lambda: c.append(k, k, off, q=q[:2]),

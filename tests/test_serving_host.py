@@ -80,7 +80,7 @@ def transform(palu, **kw):
 
 
 def test_qk_norm_rope_refusals(palu):
-    def call(t=None, dtype=0, b=2, n=3, hq=4, hk=2, q=A, qs=(1536, 512, 128), k=A, ks=(768, 256, 128), pos=A, qo=A, ko=A):
+    def call(t=None, dtype=0, b=2, n=3, hq=4, hk=2, q=A, qs=(1536, 512, 128), k=A, ks=(768, 256, 128), pos=A, qo=2 * A, ko=3 * A):
         t = transform(palu) if t is None else t
         return palu.lib().palu_qk_norm_rope(ctypes.byref(t), dtype, b, n, hq, hk, q, I64x3(*qs), k, I64x3(*ks), pos, qo, ko, None,
                                             None)
@@ -88,7 +88,7 @@ def test_qk_norm_rope_refusals(palu):
                 dict(t=transform(palu, n_positions=0)), dict(t=transform(palu, eps=-1.0)), dict(t=transform(palu, eps=float("nan"))),
                 dict(t=transform(palu, q_weight=A + 2)), dict(t=transform(palu, cos_sin=A + 4)), dict(dtype=3), dict(b=0),
                 dict(n=0), dict(hq=0), dict(hk=0), dict(b=1 << 20, n=1 << 20), dict(q=0), dict(q=A + 2), dict(qs=(1536, 512, 4)),
-                dict(qs=(-8, 512, 128)), dict(k=0), dict(pos=0), dict(pos=A + 4), dict(qo=0), dict(ko=A + 8)):
+                dict(qs=(-8, 512, 128)), dict(k=0), dict(pos=0), dict(pos=A + 4), dict(qo=0), dict(ko=3 * A + 8), dict(qo=A), dict(ko=A + 256)):
         assert call(**bad) in (1, 2) and palu.palu_last_error(), bad
 
 
@@ -96,19 +96,19 @@ def test_append_and_attend_refusals(palu):
     _, c = init(palu)
     t = transform(palu)
 
-    def append(c=c, t=t, n=3, off=A, hq=4, q=A, qs=(512, 128), k=A, ks=(256, 128), v=A, vs=(256, 128), pos=None, qo=A):
+    def append(c=c, t=t, n=3, off=A, hq=4, q=A, qs=(512, 128), k=A, ks=(256, 128), v=A, vs=(256, 128), pos=None, qo=2 * A):
         return palu.lib().palu_paged_append(ctypes.byref(c), ctypes.byref(t), n, off, hq, q, I64x2(*qs), k, I64x2(*ks), v,
                                             I64x2(*vs), pos, qo, None)
     for bad in (dict(c=palu.palu_paged_cache()), dict(n=0), dict(n=1 << 31), dict(off=None), dict(off=A + 2), dict(hq=0),
                 dict(q=None), dict(qo=None), dict(q=A + 2), dict(qs=(512, 4)), dict(k=None), dict(ks=(-256, 128)), dict(v=None),
-                dict(v=A + 2), dict(pos=A + 4), dict(qo=A + 8), dict(t=transform(palu, rope_dim=40))):
+                dict(v=A + 2), dict(pos=A + 4), dict(qo=2 * A + 8), dict(qo=A), dict(k=2 * A), dict(t=transform(palu, rope_dim=40))):
         assert append(**bad) in (1, 2, 4), bad
 
-    def attend(c=c, n=3, off=A, new=1, hq=4, q=A, qs=(512, 128), shared=0, scale=0.0, out=A, ws=A, wb=1 << 30):
+    def attend(c=c, n=3, off=A, new=1, hq=4, q=A, qs=(512, 128), shared=0, scale=0.0, out=2 * A, ws=A, wb=1 << 30):
         return palu.lib().palu_paged_attn(ctypes.byref(c), n, off, new, hq, q, I64x2(*qs), shared, scale, out, ws, wb, None)
     for bad in (dict(c=palu.palu_paged_cache()), dict(n=0), dict(off=None), dict(off=A + 1), dict(new=0), dict(hq=3), dict(q=None),
                 dict(q=A + 8), dict(qs=(512, 4)), dict(qs=(-512, 128)), dict(shared=5), dict(shared=-1), dict(scale=-1.0),
-                dict(scale=float("inf")), dict(scale=float("nan")), dict(out=None), dict(out=A + 2), dict(ws=None), dict(wb=100)):
+                dict(scale=float("inf")), dict(scale=float("nan")), dict(out=None), dict(out=A), dict(out=A + 16), dict(out=2 * A + 2), dict(ws=None), dict(wb=100)):
         assert attend(**bad) in (1, 2, 4), bad
 
 
