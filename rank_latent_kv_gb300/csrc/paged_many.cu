@@ -45,7 +45,7 @@ constexpr int kRing = 5;
 // two apart.
 constexpr int kFull = 2 * kRing;
 constexpr int kHalf = 128;
-constexpr int kStageBytes = 32 * 36 * 4;  // a warp's 32 rows of 32 columns, padded against bank conflicts
+constexpr int kStageBytes = 32 * 36 * 4;  // 128 bytes of a warp's 32 rows, padded against bank conflicts
 
 struct ManySmem {
   uint64_t kv_full[kFull], kv_empty[kRing];
@@ -423,12 +423,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const bool both = m.rows > kHalf;
       // Q: a half's 128 rows, or each 64 of the one half's; rows behind the unit's are zeros
       {
+        UnitMeta u;  // in registers: the copies' asm would have each iteration read shared memory again
+        u.tok = m.tok, u.g0 = m.g0, u.kh = m.kh, u.rows = m.rows;
         const int r_base = both ? s * kHalf : 0, q_rows = both ? kHalf : kHalf / 2, q0 = both ? 0 : s * (kHalf / 2);
         const uint32_t q_tile = smem_addr(smem) + (both ? s : 0) * kTileBytes;
         for (int i = t; i < q_rows * 16; i += kHalf) {
           const int r = q0 + (i >> 4), ch = i & 15;
-          const bool there = r_base + r < m.rows;
-          const uint16_t* src = there ? row_query(p, m, r_base + r) + ch * 8 : p.q;
+          const bool there = r_base + r < u.rows;
+          const uint16_t* src = there ? row_query(p, u, r_base + r) + ch * 8 : p.q;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(panel_addr(q_tile, r, ch)), "l"(src),
                        "r"(there ? 16 : 0)
                        : "memory");
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (__any_sync(0xffffffffu, failed())) break;
       // A unit of up to 128 rows has an accumulator of even and one of odd tiles (if it had more than one), in the
       // same lanes of TMEM; the halves exchange their maxima and sums and each takes 64 columns of the joined rows.
-      // Of a larger unit each half has its own rows.  A warp turns 32 columns of its 32 rows around in shared memory
+      // Of a larger unit each half has its own rows.  A warp turns 128 bytes of its 32 rows around in shared memory
       // (Q is free), so that it stores whole lines.
       if (!seen) ref = -INFINITY;
       float2(*const ml)[kHalf] = reinterpret_cast<float2(*)[kHalf]>(smem + 8 * kStageBytes);  // behind the staging areas
@@ -586,37 +588,55 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       fb *= inv;
       float* const stage = reinterpret_cast<float*>(smem + warp * kStageBytes);
       const int r_warp = (both ? s * kHalf : 0) + 32 * (warp & 3);  // first of the warp's rows
-#pragma unroll 1
-      for (int c = both ? 0 : 64 * s; c < (both ? 128 : 64 * s + 64); c += 32) {
-        uint32_t o[32];
+      UnitMeta u;
+      u.tok = m.tok, u.g0 = m.g0, u.kh = m.kh, u.rows = m.rows;
+      const bool two = !both && m.n > 1;
+      auto columns = [&](int c, uint32_t* o) {  // 32 of O, joined and scaled
         float* v = reinterpret_cast<float*>(o);
         tc_ld32(o, o0_addr + c);
         tc_wait_ld(o);
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] *= fa;
-        if (!both && m.n > 1) {
+        if (two) {
           uint32_t y[32];
           tc_ld32(y, o0_addr + 128 + c);
           tc_wait_ld(y);
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = fmaf(__uint_as_float(y[k]), fb, v[k]);
         }
-        __syncwarp();
-        if (dest == kToOut) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(stage + lane * 20 + 4 * k) =
-                make_uint4(pack2<BF16>(v[8 * k], v[8 * k + 1]), pack2<BF16>(v[8 * k + 2], v[8 * k + 3]),
-                           pack2<BF16>(v[8 * k + 4], v[8 * k + 5]), pack2<BF16>(v[8 * k + 6], v[8 * k + 7]));
+      };
+      const int c0 = both ? 0 : 64 * s, c1 = both ? 128 : 64 * s + 64;
+      if (dest == kToOut) {
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 64) {
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 4 lanes a row
-            const int rr = 8 * k + (lane >> 2);
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 20 + 4 * (lane & 3));
-            if (r_warp + rr < m.rows)
-              *reinterpret_cast<uint4*>(p.out + row_index(p, m, r_warp + rr) * kHeadDim + c + 8 * (lane & 3)) = x;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            columns(c + 32 * h, o);
+            const float* v = reinterpret_cast<const float*>(o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(stage + lane * 36 + 16 * h + 4 * k) =
+                  make_uint4(pack2<BF16>(v[8 * k], v[8 * k + 1]), pack2<BF16>(v[8 * k + 2], v[8 * k + 3]),
+                             pack2<BF16>(v[8 * k + 4], v[8 * k + 5]), pack2<BF16>(v[8 * k + 6], v[8 * k + 7]));
           }
-        } else {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {  // 8 lanes a row
+            const int rr = 4 * k + (lane >> 3);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 36 + 4 * (lane & 7));
+            if (r_warp + rr < u.rows)
+              *reinterpret_cast<uint4*>(p.out + row_index(p, u, r_warp + rr) * kHeadDim + c + 8 * (lane & 7)) = x;
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          uint32_t o[32];
+          columns(c, o);
+          const float* v = reinterpret_cast<const float*>(o);
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             *reinterpret_cast<float4*>(stage + lane * 36 + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -625,8 +645,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           for (int k = 0; k < 8; ++k) {  // 8 lanes a row
             const int rr = 4 * k + (lane >> 3);
             const float4 x = *reinterpret_cast<const float4*>(stage + rr * 36 + 4 * (lane & 7));
-            if (r_warp + rr < m.rows) {
-              float* acc = dest == kToRow ? p.row_acc + (set + row_index(p, m, r_warp + rr)) * kHeadDim
+            if (r_warp + rr < u.rows) {
+              float* acc = dest == kToRow ? p.row_acc + (set + row_index(p, u, r_warp + rr)) * kHeadDim
                                           : p.part.acc + ((long long)dest * p.part.R + r_warp + rr) * kHeadDim;
               *reinterpret_cast<float4*>(acc + c + 4 * (lane & 7)) = x;
             }
