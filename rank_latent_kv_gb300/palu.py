@@ -521,22 +521,25 @@ def _need_is(t, name, shape, dtype, dev):
 
 def _rows(t, name, shape, dtype, dev):
     """A token-major operand of this shape: any strides with contiguous channels and 16-byte aligned rows.  Returns its
-    leading strides (0 for a dimension of one element: torch leaves that one open)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} must be a tensor")
+    leading strides, packed."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)} on cuda:{dev}")
     st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    if 1 in shape:
-        st = [s if n > 1 else 0 for s, n in zip(st, shape)]
-    align = t.data_ptr() >> 1
-    for s in st[:-1]:
-        align |= s
-    if align & 7:
-        raise ValueError(f"{name}'s rows must be 16-byte aligned (strides {t.stride()})")
-    return st
+    if len(st) == 3:
+        s0, s1, c = st
+        if c == 1 and not (t.data_ptr() >> 1 | s0 | s1) & 7:
+            return _pack2(s0, s1)
+    else:
+        s0, s1, s2, c = st
+        if c == 1 and not (t.data_ptr() >> 1 | s0 | s1 | s2) & 7:
+            return _pack3(s0, s1, s2)
+    # torch leaves the stride of a dimension of one element open
+    lead = [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
+    if c != 1 or t.data_ptr() % 16 or any(s % 8 for s in lead):
+        raise ValueError(f"{name} must have contiguous channels and 16-byte aligned rows (strides {st})")
+    return (_pack2 if len(lead) == 2 else _pack3)(*lead)
 
 
 def _shape_of(t, name, dims):
@@ -598,8 +601,7 @@ def qk_norm_rope(q, k, positions, cos_sin=None, q_weight=None, k_weight=None, ep
     else:
         _need_is(k_out, "k_out", (B, Hk, T, D), dt, dev)
     if B and T:
-        _check(lib().palu_qk_norm_rope(tr, _TYPES[dt], B, T, Hq, Hk, q.data_ptr(), _pack3(*qs[:3]), k.data_ptr(),
-                                       _pack3(*ks[:3]), pos, q_out.data_ptr(), k_out.data_ptr(),
+        _check(lib().palu_qk_norm_rope(tr, _TYPES[dt], B, T, Hq, Hk, q.data_ptr(), qs, k.data_ptr(), ks, pos, q_out.data_ptr(), k_out.data_ptr(),
                                        None if error is None else error.data_ptr(), _raw_stream(stream, dev)))
     return q_out, k_out
 
@@ -661,7 +663,7 @@ class PagedCache:
         hq = 0
         if q is not None:
             hq = _shape_of(q, "q", 3)[1]
-            qs = _pack2(*_rows(q, "q", (n, hq, D), dt, dev)[:2])
+            qs = _rows(q, "q", (n, hq, D), dt, dev)
             if q_out is None:
                 q_out = torch.empty((n, hq, D), dtype=dt, device=self.device)
             else:
@@ -670,8 +672,8 @@ class PagedCache:
         elif q_out is not None:
             raise ValueError("q_out is given without q")
         if n:
-            _check(lib().palu_paged_append(self._c, tr, n, offsets.data_ptr(), hq, qp, qs, k.data_ptr(), _pack2(*ks[:2]),
-                                           v.data_ptr(), _pack2(*vs[:2]), None if positions is None else positions.data_ptr(),
+            _check(lib().palu_paged_append(self._c, tr, n, offsets.data_ptr(), hq, qp, qs, k.data_ptr(), ks,
+                                           v.data_ptr(), vs, None if positions is None else positions.data_ptr(),
                                            out, _raw_stream(stream, dev)))
         return q_out
 
@@ -701,7 +703,7 @@ class PagedCache:
             workspace = self.attend_workspace(n, hq, max_new, shared_pages)
         elif not _is(workspace, workspace.shape, torch.uint8, dev):
             _refuse(workspace, "workspace", workspace.shape, torch.uint8, dev)
-        _check(lib().palu_paged_attn(self._c, n, offsets.data_ptr(), max_new, hq, q.data_ptr(), _pack2(*qs[:2]), shared_pages,
+        _check(lib().palu_paged_attn(self._c, n, offsets.data_ptr(), max_new, hq, q.data_ptr(), qs, shared_pages,
                                      softmax_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                      _raw_stream(stream, dev)))
         return out

@@ -359,6 +359,27 @@ def test_large_scores_scale_and_flat_rows(P):
         assert bool(((out.cpu().double() - ref).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_one_large_weight_among_many_small_ones(P, dt):
+    """A first token whose weight is 2^14 .. 2^21 times every other's, of which there are 20,000: their sum counts."""
+    S, new = 20000, 20
+    pools, dev, c = make_cache(P, DT[dt], [S], 64, 1, seed=12)
+    ids = c.page_table.cpu().long()
+    q = torch.full((new, 2, D), 0.25).to(DT[dt])
+    k = torch.zeros(S, D)
+    k[0] = 44.0                                            # score 128 * 0.25 * 44 / sqrt(128) = 124.5, the others' 110 .. 114.6
+    k[1:] = torch.linspace(38.9, 40.5, S - 1)[torch.randperm(S - 1, generator=torch.Generator().manual_seed(1))][:, None]
+    pools[0][ids[0, torch.arange(S) // 64], 0, torch.arange(S) % 64] = k.to(DT[dt])
+    dev[0].copy_(pools[0])
+    for n in (1, new):
+        out = c.attend(q[:n].to(DEV), offsets_of([n]), n)
+        ref, mag = ref_attend(q[:n], pools, ids, [S], [n], 64)
+        eps = torch.finfo(DT[dt]).eps
+        # scores of 124 with 128 products of size 11: fp32 sums are right to about 128 * 124 * 2^-24 = 2^-10 at worst
+        bar = (eps / 2 + 2.0 ** -9) * mag + eps / 2 * ref.abs()
+        assert bool(((out.cpu().double() - ref).abs() <= bar).all())
+
+
 def test_attend_refused_on_the_device(P):
     def fresh():
         return make_cache(P, torch.float16, [40, 33], 16, 2, seed=11, width=3)
