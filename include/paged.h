@@ -97,7 +97,8 @@ typedef struct {
  *            all given by their strides).
  *   page_table  device int32 [batch, table_width] and lengths device int64
  *            [batch]: the host program's, read by every call on its stream.
- *            A row's entries behind its length are never read.
+ *            A row's entries behind its length are never read (but for
+ *            those that an attention call names as shared).
  *   error    device uint32, zeroed by the caller. */
 palu_status palu_paged_cache_init(palu_paged_cache* cache, int32_t dtype, int32_t kv_heads, int32_t page_size,
                                   int64_t n_pages, void* k_pages, const int64_t k_strides[3], void* v_pages,
@@ -129,7 +130,9 @@ palu_status palu_paged_append(const palu_paged_cache* cache, const palu_qk_trans
                               const int64_t* positions, void* q_out, void* stream);
 
 /* Device workspace of palu_paged_attn (16-byte aligned; no initial contents
- * are needed, calls that share one must not overlap on the GPU). */
+ * are needed, calls that share one must not overlap on the GPU).  It also
+ * serves fewer tokens, a smaller max_new and any other number of shared pages
+ * (one sized for shared_pages 0 serves 0 only). */
 palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_t tokens, int32_t q_heads,
                                            int32_t max_new, int32_t shared_pages, size_t* bytes);
 
@@ -143,8 +146,9 @@ palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_
  *          palu_paged_append; each sequence has at most max_new rows.
  *   shared_pages  leading page-table entries that are the same pages in every
  *          row of the table: their keys and values are read once for the
- *          whole batch (from row 0 of the table).  0: nothing is shared.  The
- *          result does not depend on it.
+ *          whole batch, from row 0 of the table (whatever the length of
+ *          sequence 0).  0: nothing is shared.  The result does not depend on
+ *          it beyond rounding.
  *   out    device [tokens, q_heads, 128], contiguous, the cache's type, not
  *          overlapping q; rows at and behind offsets[batch] are not touched.
  *   softmax_scale 0 selects 1/sqrt(128).
@@ -155,10 +159,10 @@ palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_
  * Weights are rounded to the cache's type once, where a KV head has more than
  * 16 rows; sums, maxima and accumulators are fp32.  One to three kernel
  * launches on `stream`, chosen by the sizes given here, not by the lengths.
- * The results do not depend on the run.  A sequence with more than max_new rows or offsets out
- * of order sets PALU_DEVERR_SPAN and its rows are zeros; a length past the
- * table sets PALU_DEVERR_CAPACITY and is cut to it; a page id outside the
- * pool sets PALU_DEVERR_PAGE and page 0 is read for it. */
+ * Repeating a call repeats its result bit for bit.  A sequence with more than
+ * max_new rows or offsets out of order sets PALU_DEVERR_SPAN and its rows are
+ * zeros; a length past the table sets PALU_DEVERR_CAPACITY and is cut to it;
+ * a page id outside the pool sets PALU_DEVERR_PAGE and page 0 is read for it. */
 palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t tokens, const int32_t* offsets, int32_t max_new,
                             int32_t q_heads, const void* q, const int64_t q_strides[2], int32_t shared_pages,
                             float softmax_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);

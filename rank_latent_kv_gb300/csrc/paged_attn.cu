@@ -623,12 +623,12 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   const int64_t own_rows = std::min<int64_t>(max_new, tokens) * Gq, all_rows = tokens * Gq;
   l->shared = shared_pages > 0 && c->batch > 1;
   l->R_prefix = all_rows <= 8 ? 8 : all_rows <= 16 ? 16 : kManyRows;
-  l->R_own = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
+  const int R_rows = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
   // Few own keys behind a prefix of many rows: one launch for both (256 rows behind 311,296 shared tokens and 1 own token
   // a sequence: 65 us in two launches, 55 in one; 96 rows behind 8192 and 580 own: 46 and 50).
-  if (l->shared && l->R_prefix == kManyRows &&
-      (int64_t)(c->table_width - shared_pages) * c->page_size <= kOneLaunchKeys)
-    l->R_own = kManyRows;
+  const bool few_keys = l->shared && l->R_prefix == kManyRows &&
+                        (int64_t)(c->table_width - shared_pages) * c->page_size <= kOneLaunchKeys;
+  l->R_own = few_keys ? kManyRows : R_rows;
   l->one_launch = l->shared && l->R_own == kManyRows;  // then the prefix has many rows, too
   const size_t slots = 2 * (size_t)device_sm_count();
   size_t o = 0;
@@ -637,21 +637,29 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     o = align_up(o + bytes, 256);
     return at;
   };
+  auto take_parts = [&](int R, size_t* plan, size_t* begun, size_t* ml, size_t* acc) {
+    *plan = take(sizeof(long long) * (1 + (size_t)c->batch));
+    *begun = take(slots / 2 * sizeof(UnitMeta));
+    *ml = take(slots * R * sizeof(float2));
+    *acc = take(slots * R * kHeadDim * sizeof(float));
+  };
   const bool two = l->shared && !l->one_launch;
   const int grid = device_sm_count();
   l->grid_prefix = two && grid > 1 ? split_grid(c, all_rows, shared_pages, l->R_prefix, grid) : grid;
   l->grid_own = two && grid > 1 ? grid - l->grid_prefix : grid;
-  l->plan_p = two ? take(sizeof(long long) * (1 + (size_t)c->batch)) : 0;
-  l->begun_p = two ? take(slots / 2 * sizeof(UnitMeta)) : 0;
-  l->ml_p = two ? take(slots * l->R_prefix * sizeof(float2)) : 0;
-  l->acc_p = two ? take(slots * l->R_prefix * kHeadDim * sizeof(float)) : 0;
-  l->plan_o = take(sizeof(long long) * (1 + (size_t)c->batch));
-  l->begun_o = take(slots / 2 * sizeof(UnitMeta));
-  l->ml_o = take(slots * l->R_own * sizeof(float2));
-  l->acc_o = take(slots * l->R_own * kHeadDim * sizeof(float));
   l->row_ml = l->shared ? take(2 * (size_t)tokens * q_heads * sizeof(float2)) : 0;
   l->row_acc = l->shared ? take(2 * (size_t)tokens * q_heads * kHeadDim * sizeof(float)) : 0;
+  take_parts(l->R_own, &l->plan_o, &l->begun_o, &l->ml_o, &l->acc_o);
+  if (two) take_parts(l->R_prefix, &l->plan_p, &l->begun_p, &l->ml_p, &l->acc_p);
   l->total = o;
+  if (l->one_launch) {
+    // what two launches would take, so that a workspace also serves fewer new tokens or another number of shared pages
+    size_t unused;
+    o = l->plan_o;
+    take_parts(R_rows, &unused, &unused, &unused, &unused);
+    take_parts(l->R_prefix, &unused, &unused, &unused, &unused);
+    l->total = std::max(l->total, o);
+  }
   return PALU_OK;
 }
 

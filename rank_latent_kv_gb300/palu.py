@@ -678,7 +678,8 @@ class PagedCache:
         return q_out
 
     def attend_workspace(self, tokens, q_heads, max_new, shared_pages=0):
-        """A workspace for attend calls of up to these sizes (calls that share one must not overlap on the GPU)."""
+        """A workspace for attend calls of up to these sizes, with any number of shared pages unless this is 0 (calls that
+        share one must not overlap on the GPU)."""
         n = c_size_t()
         _check(lib().palu_paged_attn_workspace_size(self._c, max(tokens, 1), q_heads, max_new, shared_pages, ctypes.byref(n)))
         return _dev_bytes(n.value, self.device)

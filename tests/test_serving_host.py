@@ -72,6 +72,23 @@ def test_workspace_size(palu):
     assert palu.lib().palu_paged_attn_workspace_size(ctypes.byref(palu.palu_paged_cache()), 3, 4, 1, 0, ctypes.byref(n)) == 4
 
 
+@pytest.mark.parametrize("width", [4, 40])
+def test_a_workspace_serves_smaller_calls(palu, width):
+    _, c = init(palu, width=width, batch=30)
+    n = ctypes.c_size_t()
+
+    def size(tokens, new, shared):
+        assert palu.lib().palu_paged_attn_workspace_size(ctypes.byref(c), tokens, 14, new, shared, ctypes.byref(n)) == 0
+        return n.value
+    sizes = [(t, m) for t in (1, 2, 3, 30, 100, 300) for m in (1, 2, 3, 10, 100)]
+    for t, m in sizes:
+        shared = {size(t, m, s) for s in range(1, width + 1)}
+        assert len(shared) == 1 and size(t, m, 0) <= shared.pop()
+        for t1, m1 in sizes:
+            if t1 <= t and m1 <= m:
+                assert all(size(t1, m1, s) <= size(t, m, s) for s in (0, 1, width // 2, width))
+
+
 def transform(palu, **kw):
     t = palu.palu_qk_transform()
     for k, v in dict(dict(cos_sin=A, n_positions=100, rope_dim=64), **kw).items():
