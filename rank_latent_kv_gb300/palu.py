@@ -487,7 +487,7 @@ _pack_transform = struct.Struct("PPPqiifi").pack    # palu_qk_transform
 
 
 # These calls take a few microseconds on the GPU, so their checks are written for the case that all is well: one
-# expression a tensor, and the function that says what is wrong only where something is.
+# expression a tensor, and what is wrong is only worked out where something is.
 
 def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
@@ -503,70 +503,63 @@ def _here(t, name):
     return dev
 
 
-def _is(t, shape, dtype, dev):
-    """A contiguous tensor of this shape (a tuple) and type on this device."""
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
-
-
-def _refuse(t, name, shape, dtype, dev):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
+def _at(t, name, shape, dtype, dev):
+    """The address of a contiguous tensor of this shape (a tuple) and type on this device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
     raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)} on cuda:{dev}, contiguous")
-
-
-def _need_is(t, name, shape, dtype, dev):
-    if not _is(t, shape, dtype, dev):
-        _refuse(t, name, shape, dtype, dev)
 
 
 def _rows(t, name, shape, dtype, dev):
     """A token-major operand of this shape: any strides with contiguous channels and 16-byte aligned rows.  Returns its
-    leading strides, packed."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)} on cuda:{dev}")
-    st = t.stride()
-    if len(st) == 3:
-        s0, s1, c = st
-        if c == 1 and not (t.data_ptr() >> 1 | s0 | s1) & 7:
-            return _pack2(s0, s1)
-    else:
-        s0, s1, s2, c = st
-        if c == 1 and not (t.data_ptr() >> 1 | s0 | s1 | s2) & 7:
-            return _pack3(s0, s1, s2)
-    # torch leaves the stride of a dimension of one element open
-    lead = [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
-    if c != 1 or t.data_ptr() % 16 or any(s % 8 for s in lead):
-        raise ValueError(f"{name} must have contiguous channels and 16-byte aligned rows (strides {st})")
-    return (_pack2 if len(lead) == 2 else _pack3)(*lead)
+    address and its leading strides, packed."""
+    try:
+        st, at = t.stride(), t.data_ptr()
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            if len(st) == 3:
+                s0, s1, c = st
+                if c == 1 and not (at >> 1 | s0 | s1) & 7:
+                    return at, _pack2(s0, s1)
+            else:
+                s0, s1, s2, c = st
+                if c == 1 and not (at >> 1 | s0 | s1 | s2) & 7:
+                    return at, _pack3(s0, s1, s2)
+            # torch leaves the stride of a dimension of one element open
+            lead = [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
+            if c != 1 or at % 16 or any(s % 8 for s in lead):
+                raise ValueError(f"{name} must have contiguous channels and 16-byte aligned rows (strides {st})")
+            return at, (_pack2 if len(lead) == 2 else _pack3)(*lead)
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
+    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected {dtype} {tuple(shape)} on cuda:{dev}")
 
 
 def _shape_of(t, name, dims):
     """The shape of a tensor with this many dimensions, the last of them the head's channels."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    shape = t.shape
-    if len(shape) != dims or shape[-1] != D:
-        raise ValueError(f"{name} has shape {tuple(shape)}; expected {dims} dimensions, the last of {D}")
-    return shape
+    try:
+        shape = t.shape
+        if len(shape) == dims and shape[-1] == D:
+            return shape
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
+    raise ValueError(f"{name} has shape {tuple(shape)}; expected {dims} dimensions, the last of {D}")
 
 
 def _transform(dtype, dev, cos_sin, q_weight, k_weight, eps, interleaved):
     """palu_qk_transform as bytes."""
-    qw = kw = cs = n = rope = 0
-    if q_weight is not None:
-        _need_is(q_weight, "q_weight", (D,), dtype, dev)
-        qw = q_weight.data_ptr()
-    if k_weight is not None:
-        _need_is(k_weight, "k_weight", (D,), dtype, dev)
-        kw = k_weight.data_ptr()
+    n = rope = 0
+    qw = 0 if q_weight is None else _at(q_weight, "q_weight", (D,), dtype, dev)
+    kw = 0 if k_weight is None else _at(k_weight, "k_weight", (D,), dtype, dev)
+    cs = 0
     if cos_sin is not None:
-        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be a tensor [positions, rope_dim]")
-        n, rope = cos_sin.shape
-        _need_is(cos_sin, "cos_sin", (n, rope), _F32, dev)
-        cs = cos_sin.data_ptr()
+        try:
+            n, rope = cos_sin.shape
+        except (AttributeError, ValueError):
+            raise ValueError("cos_sin must be a tensor [positions, rope_dim]") from None
+        cs = _at(cos_sin, "cos_sin", (n, rope), _F32, dev)
     return _pack_transform(qw, kw, cs, n, rope, 1 if interleaved else 0, eps, 0)
 
 
@@ -582,27 +575,20 @@ def qk_norm_rope(q, k, positions, cos_sin=None, q_weight=None, k_weight=None, ep
     if dt not in _TYPES:
         raise ValueError(f"q has dtype {dt}; expected torch.float16 or torch.bfloat16")
     B, T, Hq, _ = shape = _shape_of(q, "q", 4)
-    qs = _rows(q, "q", shape, dt, dev)
+    qp, qs = _rows(q, "q", shape, dt, dev)
     Hk = _shape_of(k, "k", 4)[2]
-    ks = _rows(k, "k", (B, T, Hk, D), dt, dev)
+    kp, ks = _rows(k, "k", (B, T, Hk, D), dt, dev)
     tr = _transform(dt, dev, cos_sin, q_weight, k_weight, eps, interleaved)
-    pos = 0
-    if cos_sin is not None:
-        _need_is(positions, "positions", (B, T), _I64, dev)
-        pos = positions.data_ptr()
-    if error is not None:
-        _need_is(error, "error", (1,), _I32, dev)
+    pos = None if cos_sin is None else _at(positions, "positions", (B, T), _I64, dev)
+    err = None if error is None else _at(error, "error", (1,), _I32, dev)
     if q_out is None:
         q_out = torch.empty((B, Hq, T, D), dtype=dt, device=q.device)
-    else:
-        _need_is(q_out, "q_out", (B, Hq, T, D), dt, dev)
     if k_out is None:
         k_out = torch.empty((B, Hk, T, D), dtype=dt, device=q.device)
-    else:
-        _need_is(k_out, "k_out", (B, Hk, T, D), dt, dev)
+    qo, ko = _at(q_out, "q_out", (B, Hq, T, D), dt, dev), _at(k_out, "k_out", (B, Hk, T, D), dt, dev)
     if B and T:
-        _check(lib().palu_qk_norm_rope(tr, _TYPES[dt], B, T, Hq, Hk, q.data_ptr(), qs, k.data_ptr(), ks, pos, q_out.data_ptr(), k_out.data_ptr(),
-                                       None if error is None else error.data_ptr(), _raw_stream(stream, dev)))
+        _check(lib().palu_qk_norm_rope(tr, _TYPES[dt], B, T, Hq, Hk, qp, qs, kp, ks, pos, qo, ko, err,
+                                       _raw_stream(stream, dev)))
     return q_out, k_out
 
 
@@ -623,8 +609,8 @@ class PagedCache:
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be a tensor [batch, width]")
         self.batch, self.width = page_table.shape
-        _need_is(page_table, "page_table", (self.batch, self.width), _I32, dev)
-        _need_is(lengths, "lengths", (self.batch,), _I64, dev)
+        _at(page_table, "page_table", (self.batch, self.width), _I32, dev)
+        _at(lengths, "lengths", (self.batch,), _I64, dev)
         self.k_pages, self.v_pages, self.page_table, self.lengths = k_pages, v_pages, page_table, lengths
         self.error = torch.zeros(1, dtype=_I32, device=self.device)
 
@@ -652,29 +638,23 @@ class PagedCache:
         dev, dt = self._on_current(), self.dtype
         n = _shape_of(k, "k", 3)[0]
         shape = (n, self.kv_heads, D)
-        ks = _rows(k, "k", shape, dt, dev)
-        vs = _rows(v, "v", shape, dt, dev)
-        if not _is(offsets, self._offsets, _I32, dev):
-            _refuse(offsets, "offsets", self._offsets, _I32, dev)
+        kp, ks = _rows(k, "k", shape, dt, dev)
+        vp, vs = _rows(v, "v", shape, dt, dev)
+        op = _at(offsets, "offsets", self._offsets, _I32, dev)
         tr = _transform(dt, dev, cos_sin, q_weight, k_weight, eps, interleaved)
-        if positions is not None:
-            _need_is(positions, "positions", (n,), _I64, dev)
+        pos = None if positions is None else _at(positions, "positions", (n,), _I64, dev)
         qp = qs = out = None
         hq = 0
         if q is not None:
             hq = _shape_of(q, "q", 3)[1]
-            qs = _rows(q, "q", (n, hq, D), dt, dev)
+            qp, qs = _rows(q, "q", (n, hq, D), dt, dev)
             if q_out is None:
                 q_out = torch.empty((n, hq, D), dtype=dt, device=self.device)
-            else:
-                _need_is(q_out, "q_out", (n, hq, D), dt, dev)
-            qp, out = q.data_ptr(), q_out.data_ptr()
+            out = _at(q_out, "q_out", (n, hq, D), dt, dev)
         elif q_out is not None:
             raise ValueError("q_out is given without q")
         if n:
-            _check(lib().palu_paged_append(self._c, tr, n, offsets.data_ptr(), hq, qp, qs, k.data_ptr(), ks,
-                                           v.data_ptr(), vs, None if positions is None else positions.data_ptr(),
-                                           out, _raw_stream(stream, dev)))
+            _check(lib().palu_paged_append(self._c, tr, n, op, hq, qp, qs, kp, ks, vp, vs, pos, out, _raw_stream(stream, dev)))
         return q_out
 
     def attend_workspace(self, tokens, q_heads, max_new, shared_pages=0):
@@ -691,21 +671,18 @@ class PagedCache:
         [N, Hq, 128]; rows behind offsets[B] are left as they were."""
         dev = self._on_current()
         n, hq, _ = shape = _shape_of(q, "q", 3)
-        qs = _rows(q, "q", shape, self.dtype, dev)
-        if not _is(offsets, self._offsets, _I32, dev):
-            _refuse(offsets, "offsets", self._offsets, _I32, dev)
+        qp, qs = _rows(q, "q", shape, self.dtype, dev)
+        op = _at(offsets, "offsets", self._offsets, _I32, dev)
         if out is None:
             out = torch.empty(shape, dtype=self.dtype, device=self.device)
-        else:
-            _need_is(out, "out", shape, self.dtype, dev)
+        to = _at(out, "out", shape, self.dtype, dev)
         if n == 0:
             return out
         if workspace is None:
             workspace = self.attend_workspace(n, hq, max_new, shared_pages)
-        elif not _is(workspace, workspace.shape, torch.uint8, dev):
-            _refuse(workspace, "workspace", workspace.shape, torch.uint8, dev)
-        _check(lib().palu_paged_attn(self._c, n, offsets.data_ptr(), max_new, hq, q.data_ptr(), qs, shared_pages,
-                                     softmax_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        size = workspace.numel()
+        ws = _at(workspace, "workspace", (size,), torch.uint8, dev)
+        _check(lib().palu_paged_attn(self._c, n, op, max_new, hq, qp, qs, shared_pages, softmax_scale, to, ws, size,
                                      _raw_stream(stream, dev)))
         return out
 
@@ -716,6 +693,19 @@ class PagedCache:
         return e.value
 
 
+def _table(t, name, shape, dev):
+    """A table of probabilities, rows of contiguous fp32 values: its address and its leading strides, packed."""
+    try:
+        if t.dtype is _F32 and t.shape == shape and t.get_device() == dev:
+            s0, s1, c = t.stride()
+            if c == 1 or shape[2] <= 1:
+                return t.data_ptr(), _pack2(s0, s1)
+            raise ValueError(f"{name} must have contiguous rows")
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
+    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected torch.float32 {tuple(shape)} on cuda:{dev}")
+
+
 def draft_verify(target, draft, drafts, accept_u, sample_u, n_drafts=None, lengths=None, tokens=None, n_kept=None,
                  new_lengths=None, stream=None):
     """Verify drafted tokens (include/draft.h): target fp32 [B, k+1, V], draft fp32 [B, k, V] or None, drafts int64
@@ -723,54 +713,32 @@ def draft_verify(target, draft, drafts, accept_u, sample_u, n_drafts=None, lengt
     with all drafts counted.  Returns (tokens int64 [B, k+1]: the kept drafts, one drawn token, -1; n_kept int32 [B];
     new_lengths int64 [B], or None without lengths)."""
     dev = _here(target, "target")
-    if not isinstance(drafts, torch.Tensor) or drafts.dim() != 2:
-        raise ValueError("drafts must be a tensor [batch, k]")
-    B, k = shape = drafts.shape
+    try:
+        B, k = shape = drafts.shape
+    except (AttributeError, ValueError):
+        raise ValueError("drafts must be a tensor [batch, k]") from None
     rows = (B,)
-    _need_is(drafts, "drafts", shape, _I64, dev)
-
-    def table(t, name, n):  # rows of contiguous fp32 values
-        if t.dtype is not _F32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != n or t.get_device() != dev:
-            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; expected torch.float32 {(B, n, '*')} on cuda:{dev}")
-        st = t.stride()
-        if st[2] != 1 and t.shape[2] > 1:
-            raise ValueError(f"{name} must have contiguous rows")
-        return _pack2(st[0], st[1])
-    ts, V = table(target, "target", k + 1), target.shape[2]
-    dp = ds = None
-    if draft is not None:
-        if not isinstance(draft, torch.Tensor):
-            raise ValueError("draft must be a tensor or None")
-        ds, dp = table(draft, "draft", k), draft.data_ptr()
-        if draft.shape[2] != V:
-            raise ValueError(f"draft has {draft.shape[2]} values a row and target {V}")
-    _need_is(accept_u, "accept_u", shape, _F32, dev)
-    _need_is(sample_u, "sample_u", rows, _F32, dev)
-    np_ = lp = nlp = None
-    if n_drafts is not None:
-        _need_is(n_drafts, "n_drafts", rows, _I32, dev)
-        np_ = n_drafts.data_ptr()
-    if tokens is None:
-        tokens = torch.empty((B, k + 1), dtype=_I64, device=target.device)
-    else:
-        _need_is(tokens, "tokens", (B, k + 1), _I64, dev)
-    if n_kept is None:
-        n_kept = torch.empty(rows, dtype=_I32, device=target.device)
-    else:
-        _need_is(n_kept, "n_kept", rows, _I32, dev)
+    xp = _at(drafts, "drafts", shape, _I64, dev)
+    V = target.shape[-1]
+    tp, ts = _table(target, "target", (B, k + 1, V), dev)
+    dp, ds = (None, None) if draft is None else _table(draft, "draft", (B, k, V), dev)
+    ap, up = _at(accept_u, "accept_u", shape, _F32, dev), _at(sample_u, "sample_u", rows, _F32, dev)
+    np_ = None if n_drafts is None else _at(n_drafts, "n_drafts", rows, _I32, dev)
+    lp = nlp = None
     if lengths is not None:
-        _need_is(lengths, "lengths", rows, _I64, dev)
+        lp = _at(lengths, "lengths", rows, _I64, dev)
         if new_lengths is None:
-            new_lengths = torch.empty(rows, dtype=_I64, device=target.device)
-        else:
-            _need_is(new_lengths, "new_lengths", rows, _I64, dev)
-        lp, nlp = lengths.data_ptr(), new_lengths.data_ptr()
+            new_lengths = torch.empty_like(lengths)
+        nlp = _at(new_lengths, "new_lengths", rows, _I64, dev)
     elif new_lengths is not None:
         raise ValueError("new_lengths is given without lengths")
+    if tokens is None:
+        tokens = torch.empty((B, k + 1), dtype=_I64, device=target.device)
+    if n_kept is None:
+        n_kept = torch.empty(rows, dtype=_I32, device=target.device)
+    yp, np2 = _at(tokens, "tokens", (B, k + 1), _I64, dev), _at(n_kept, "n_kept", rows, _I32, dev)
     if B:
-        _check(lib().palu_draft_verify(B, k, V, target.data_ptr(), ts, dp, ds, drafts.data_ptr(), np_, accept_u.data_ptr(),
-                                       sample_u.data_ptr(), lp, tokens.data_ptr(), n_kept.data_ptr(), nlp,
-                                       _raw_stream(stream, dev)))
+        _check(lib().palu_draft_verify(B, k, V, tp, ts, dp, ds, xp, np_, ap, up, lp, yp, np2, nlp, _raw_stream(stream, dev)))
     return tokens, n_kept, new_lengths
 
 
