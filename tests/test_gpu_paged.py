@@ -516,6 +516,57 @@ def test_captured_graph_follows_lengths_and_pages(P):
         attend_close(out[:n], ref, mag, torch.float16)
 
 
+@pytest.mark.parametrize("shared,new", [(0, 2), (3, 1), (3, 6)])
+def test_copies_and_fills_between_the_calls(P, shared, new):
+    """Inputs copied and outputs filled right before the calls and results read right behind them, eagerly and in a
+    captured graph: the launches begin early, but never before the work ahead of them has ended."""
+    page, Hq, Hk, B = 32, 8, 2, 40
+    lengths = [page * shared + 40 + 7 * i for i in range(B)]
+    pools, dev, c = make_cache(P, torch.bfloat16, lengths, page, Hk, seed=33, shared=shared, width=shared + 11)
+    g = torch.Generator().manual_seed(10)
+    n = B * new
+    src = torch.randn(4, n, Hq + 2 * Hk, D, generator=g).bfloat16().to(DEV)
+    x, off = torch.empty_like(src[0]), offsets_of([new] * B)
+    cs = _table(1000, 128).to(DEV)
+    ws = c.attend_workspace(n, Hq, new, shared)
+    q, out, res = (torch.zeros(n, Hq, D, dtype=torch.bfloat16, device=DEV) for _ in range(3))
+    pick = torch.zeros(1, dtype=torch.int64, device=DEV)
+    base = torch.tensor(lengths, device=DEV)
+    grow = torch.zeros(1, dtype=torch.int64, device=DEV)
+
+    def step():
+        x.copy_(src[pick][0])                     # a kernel
+        c.lengths.copy_(base)                     # a copy
+        c.lengths.add_(grow)
+        q.zero_()                                 # a fill
+        c.append(x[:, Hq:Hq + Hk], x[:, Hq + Hk:], off, q=x[:, :Hq], cos_sin=cs, q_out=q)
+        out.zero_()
+        c.attend(q, off, new, shared_pages=shared, workspace=ws, out=out)
+        res.copy_(out)
+        c.attend(q, off, new, shared_pages=shared, workspace=ws, out=out)
+
+    def check(i):
+        pick.fill_(i)
+        grow.fill_(i)
+        run()
+        a, b = res.clone(), out.clone()
+        assert torch.equal(a, b) and c.sync() == 0
+        host, at = [t.cpu() for t in dev], [v + i for v in lengths]
+        rows = torch.cat([torch.arange(b * new, (b + 1) * new) for b in (0, 17, B - 1)])
+        ref, mag = ref_attend(q[rows].cpu(), host, c.page_table.cpu()[[0, 17, B - 1]], [at[0], at[17], at[B - 1]], [new] * 3, page)
+        attend_close(a[rows], ref, mag, torch.bfloat16)
+    run = step
+    for i in range(4):
+        check(i)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    run = graph.replay
+    for i in (2, 0, 3, 1):
+        check(i)
+
+
 def test_two_streams_with_workspaces_of_their_own(P):
     pools, dev, c = make_cache(P, torch.bfloat16, [2000, 1500], 64, 4, seed=31, shared=10)
     q = torch.randn(2, 10, 16, D, generator=torch.Generator().manual_seed(9)).bfloat16()
