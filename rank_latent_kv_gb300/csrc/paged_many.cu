@@ -20,8 +20,8 @@
 //   one 128 x 128 x 16; measured 3,950 clocks a tile pair.)
 //   A tile pair takes about 3,100 clocks: the products alone 2,048, in which
 //   they read 192 KB of shared memory and the copies write 64, at 128 bytes a
-//   clock as long again.  1,024 tokens of 8 heads over 53,248 keys: 171 us,
-//   1290 TFLOP/s.
+//   clock as long again.  1,024 tokens of 8 heads over 53,248 keys: 163 us,
+//   1361 TFLOP/s.
 //   Shared memory: Q0 Q1 (32 KB each), a ring of five 32 KB tiles that holds
 //   K and V of successive key tiles in turn.
 //   Warps 0-3, 4-7: the halves' softmax; warp 8: loads; warps 9, 10: the
@@ -466,40 +466,32 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         wait_or_fail(&sh.s_full[s], sc & 1, &sh.failed, err);
         __syncwarp();
         tc_fence_after();
-        // The scores of the first 64 keys stay in registers; those of the others pass through twice, for the maximum and
-        // for the weights (a thread with all 128 spills).
-        uint32_t x[64], y[32], w[32];
+        // The scores pass twice, 64 at a time, for the maximum and for the weights (a thread with all 128 spills).  Both
+        // loops are kept rolled: a launch has to fetch its code, and the softmax has time to spare.
+        uint32_t x[64];
+        float* const f = reinterpret_cast<float*>(x);
         const int seen_here = lim - tile_key;
         const bool cut = __any_sync(0xffffffffu, seen_here < kKeyTile);
-        auto masked = [&](uint32_t* r, int c, int n) {
-          float* f = reinterpret_cast<float*>(r);
+        auto load = [&](int u) {
+          tc_ld32(x, s_addr + 64 * u);
+          tc_ld32(x + 32, s_addr + 64 * u + 32);
+          tc_wait_ld(x);
+          tc_wait_ld(x + 32);
+          if (cut) {
+            const int n = seen_here - 64 * u;
 #pragma unroll
-          for (int i = 0; i < n; ++i) f[i] = c + i < seen_here ? f[i] : -INFINITY;
+            for (int i = 0; i < 64; ++i) f[i] = i < n ? f[i] : -INFINITY;
+          }
         };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto max_of = [&](const uint32_t* r, int n) {
-          const float* f = reinterpret_cast<const float*>(r);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          load(u);
 #pragma unroll
-          for (int i = 0; i < n; i += 8)
+          for (int i = 0; i < 64; i += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
-        };
-        tc_ld32(x, s_addr);
-        tc_ld32(x + 32, s_addr + 32);
-        tc_wait_ld(x);
-        tc_wait_ld(x + 32);
-        tc_ld32(y, s_addr + 64);
-        tc_ld32(w, s_addr + 96);
-        if (cut) masked(x, 0, 64);
-        max_of(x, 64);
-        tc_wait_ld(y);
-        tc_wait_ld(w);
-        if (cut) {
-          masked(y, 64, 32);
-          masked(w, 96, 32);
         }
-        max_of(y, 32);
-        max_of(w, 32);
         const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * p.scale_log2;
         // raise the maximum?  O of this half is complete up to the tile before: its product was issued before these scores
         float alpha = 1.f;
@@ -522,36 +514,26 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
         }
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        auto weights = [&](uint32_t* r, int n, uint32_t* out) {
-          float* f = reinterpret_cast<float*>(r);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          load(u);
+          uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < n / 2; ++i) {
+          for (int i = 0; i < 32; ++i) {
             float a = f[2 * i], b = f[2 * i + 1];
             fma2(a, b, p.scale_log2, -ref);
             a = ex2f_(a);
             b = ex2f_(b);
             add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], a, b);
-            out[i] = pack2<BF16>(a, b);
+            w[i] = pack2<BF16>(a, b);
           }
-        };
-        auto publish = [&](int u) {
+          tc_st32(s_addr + 32 * u, w);
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.p_full[s][u]);
-        };
-        weights(x, 64, w);
-        tc_st32(s_addr, w);
-        publish(0);
-        tc_ld32(x, s_addr + 64);
-        tc_ld32(x + 32, s_addr + 96);
-        tc_wait_ld(x);
-        tc_wait_ld(x + 32);
-        if (cut) masked(x, 64, 64);
-        weights(x, 64, w);
-        tc_st32(s_addr + 32, w);
+        }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        publish(1);
       }
       // ---- the unit's result
       wait_or_fail(&sh.unit_done, unit & 1, &sh.failed, err);
