@@ -493,6 +493,15 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor of the memory of the call's stream: of another's it could be handed out again, or still be in use there,
+    while this call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _here(t, name):
     """The tensor's device index, which has to be the current one: the library launches there."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -582,9 +591,9 @@ def qk_norm_rope(q, k, positions, cos_sin=None, q_weight=None, k_weight=None, ep
     pos = None if cos_sin is None else _at(positions, "positions", (B, T), _I64, dev)
     err = None if error is None else _at(error, "error", (1,), _I32, dev)
     if q_out is None:
-        q_out = torch.empty((B, Hq, T, D), dtype=dt, device=q.device)
+        q_out = _empty((B, Hq, T, D), dt, q.device, stream)
     if k_out is None:
-        k_out = torch.empty((B, Hk, T, D), dtype=dt, device=q.device)
+        k_out = _empty((B, Hk, T, D), dt, q.device, stream)
     qo, ko = _at(q_out, "q_out", (B, Hq, T, D), dt, dev), _at(k_out, "k_out", (B, Hk, T, D), dt, dev)
     if B and T:
         _check(lib().palu_qk_norm_rope(tr, _TYPES[dt], B, T, Hq, Hk, qp, qs, kp, ks, pos, qo, ko, err,
@@ -649,7 +658,7 @@ class PagedCache:
             hq = _shape_of(q, "q", 3)[1]
             qp, qs = _rows(q, "q", (n, hq, D), dt, dev)
             if q_out is None:
-                q_out = torch.empty((n, hq, D), dtype=dt, device=self.device)
+                q_out = _empty((n, hq, D), dt, self.device, stream)
             out = _at(q_out, "q_out", (n, hq, D), dt, dev)
         elif q_out is not None:
             raise ValueError("q_out is given without q")
@@ -657,12 +666,12 @@ class PagedCache:
             _check(lib().palu_paged_append(self._c, tr, n, op, hq, qp, qs, kp, ks, vp, vs, pos, out, _raw_stream(stream, dev)))
         return q_out
 
-    def attend_workspace(self, tokens, q_heads, max_new, shared_pages=0):
+    def attend_workspace(self, tokens, q_heads, max_new, shared_pages=0, stream=None):
         """A workspace for attend calls of up to these sizes, with any number of shared pages unless this is 0 (calls that
         share one must not overlap on the GPU)."""
         n = c_size_t()
         _check(lib().palu_paged_attn_workspace_size(self._c, max(tokens, 1), q_heads, max_new, shared_pages, ctypes.byref(n)))
-        return _dev_bytes(n.value, self.device)
+        return _empty(max(n.value, 256), torch.uint8, self.device, stream)
 
     def attend(self, q, offsets, max_new, shared_pages=0, softmax_scale=0.0, workspace=None, out=None, stream=None):
         """Attention of the new tokens (already appended) over the cache: row r of q [N, Hq, 128], sequence b's token
@@ -674,12 +683,12 @@ class PagedCache:
         qp, qs = _rows(q, "q", shape, self.dtype, dev)
         op = _at(offsets, "offsets", self._offsets, _I32, dev)
         if out is None:
-            out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            out = _empty(shape, self.dtype, self.device, stream)
         to = _at(out, "out", shape, self.dtype, dev)
         if n == 0:
             return out
         if workspace is None:
-            workspace = self.attend_workspace(n, hq, max_new, shared_pages)
+            workspace = self.attend_workspace(n, hq, max_new, shared_pages, stream)
         size = workspace.numel()
         ws = _at(workspace, "workspace", (size,), torch.uint8, dev)
         _check(lib().palu_paged_attn(self._c, n, op, max_new, hq, qp, qs, shared_pages, softmax_scale, to, ws, size,
@@ -728,14 +737,14 @@ def draft_verify(target, draft, drafts, accept_u, sample_u, n_drafts=None, lengt
     if lengths is not None:
         lp = _at(lengths, "lengths", rows, _I64, dev)
         if new_lengths is None:
-            new_lengths = torch.empty_like(lengths)
+            new_lengths = _empty(rows, _I64, target.device, stream)
         nlp = _at(new_lengths, "new_lengths", rows, _I64, dev)
     elif new_lengths is not None:
         raise ValueError("new_lengths is given without lengths")
     if tokens is None:
-        tokens = torch.empty((B, k + 1), dtype=_I64, device=target.device)
+        tokens = _empty((B, k + 1), _I64, target.device, stream)
     if n_kept is None:
-        n_kept = torch.empty(rows, dtype=_I32, device=target.device)
+        n_kept = _empty(rows, _I32, target.device, stream)
     yp, np2 = _at(tokens, "tokens", (B, k + 1), _I64, dev), _at(n_kept, "n_kept", rows, _I32, dev)
     if B:
         _check(lib().palu_draft_verify(B, k, V, tp, ts, dp, ds, xp, np_, ap, up, lp, yp, np2, nlp, _raw_stream(stream, dev)))

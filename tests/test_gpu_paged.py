@@ -585,6 +585,42 @@ def test_two_streams_with_workspaces_of_their_own(P):
         attend_close(out[i], *ref[i], torch.bfloat16)
 
 
+def _stream_of(t):
+    """The stream whose memory a tensor is, by the allocator's record."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_results_and_workspaces_are_memory_of_the_calls_stream(P):
+    """With `stream`, what a call allocates is that stream's memory: filled again at once on the current stream, memory of
+    the current one would change under the running call."""
+    lengths = [9000 + 100 * i for i in range(8)]
+    pools, dev, c = make_cache(P, torch.bfloat16, lengths, 64, 4, seed=35, shared=10)
+    g = torch.Generator().manual_seed(12)
+    q, k, v = (torch.randn(16, h, D, generator=g).bfloat16().to(DEV) for h in (16, 4, 4))
+    off, cs = offsets_of([2] * 8), _table(10000, 128).to(DEV)
+    pos = torch.zeros(1, 16, dtype=torch.int64, device=DEV)
+    ref_q = c.append(k, v, off, q=q, cos_sin=cs)
+    ref = c.attend(ref_q, off, 2, shared_pages=10)
+    t, x = torch.rand(3, 4, 500, device=DEV), torch.zeros(3, 3, dtype=torch.int64, device=DEV)
+    u, w, n = torch.rand(3, 3, device=DEV), torch.rand(3, device=DEV), torch.full((3,), 9, device=DEV)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    size = c.attend_workspace(16, 16, 2, 10).numel()
+    for _ in range(10):
+        a = c.append(k, v, off, q=q, cos_sin=cs, stream=s)
+        b = c.attend(a, off, 2, shared_pages=10, stream=s)
+        junk = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for _ in range(3)]
+        del junk
+        results = [a, b, *P.qk_norm_rope(q[None], k[None], pos, cs, stream=s), *P.draft_verify(t, None, x, u, w, lengths=n, stream=s),
+                   c.attend_workspace(16, 16, 2, 10, stream=s)]
+        torch.cuda.synchronize()
+        assert [_stream_of(r) for r in results] == [s.cuda_stream] * len(results)
+        assert torch.equal(a, ref_q) and torch.equal(b, ref)
+    assert c.sync() == 0
+
+
 def test_python_refusals(P):
     pools, dev, c = make_cache(P, torch.float16, [40, 33], 16, 2, seed=11, width=3)
     q, k = torch.zeros(3, 4, D, dtype=torch.float16, device=DEV), torch.zeros(3, 2, D, dtype=torch.float16, device=DEV)
