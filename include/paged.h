@@ -110,7 +110,7 @@ palu_status palu_paged_cache_init(palu_paged_cache* cache, int32_t dtype, int32_
  * its tokens lengths[b] - n_b .. lengths[b] - 1.  Keys (and queries) go
  * through the transform; values are copied.  Repeating a call writes the same
  * values to the same places.
- *   offsets  device int32 [batch + 1], non-decreasing; rows at and behind
+ *   offsets  device int32 [batch + 1], from 0 on, non-decreasing; rows at and behind
  *          offsets[batch] (a batch padded for a captured graph) are not
  *          touched.  n_b may be 0.
  *   q      device [tokens, q_heads, 128], strides token and head, or NULL
@@ -161,7 +161,7 @@ palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_
  * launches on `stream`, chosen by the sizes given here, not by the lengths.
  * Repeating a call repeats its result bit for bit.  A sequence with more than
  * max_new rows or offsets out of order sets PALU_DEVERR_SPAN and its rows are
- * zeros; a length past the table sets PALU_DEVERR_CAPACITY and is cut to it;
+ * zeros, as are rows before offsets[0] where that is not 0; a length past the table sets PALU_DEVERR_CAPACITY and is cut to it;
  * a page id outside the pool sets PALU_DEVERR_PAGE and page 0 is read for it. */
 palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t tokens, const int32_t* offsets, int32_t max_new,
                             int32_t q_heads, const void* q, const int64_t q_strides[2], int32_t shared_pages,

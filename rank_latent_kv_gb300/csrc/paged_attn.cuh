@@ -122,7 +122,7 @@ __device__ __forceinline__ SeqSpan seq_span(const AttnParams& p, int b, unsigned
   SeqSpan s;
   s.tok0 = o0;
   s.n = (o0 >= 0 && o1 >= o0 && o1 <= p.N && (long long)o1 - o0 <= p.max_new) ? o1 - o0 : 0;
-  if (s.n == 0 && o1 != o0) *bad |= PALU_DEVERR_SPAN;
+  if ((s.n == 0 && o1 != o0) || (b == 0 && o0 != 0)) *bad |= PALU_DEVERR_SPAN;
   if (len > cap) *bad |= PALU_DEVERR_CAPACITY;
   s.len = (int)(len < 0 ? 0 : len > cap ? cap : len);
   return s;
@@ -218,11 +218,13 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
       if (s.n && row_limit(s, 0) < p.S0) sc->cut_prefix = 1;
       if (!p.do_own) continue;
       mine += seq_ticks<R>(s, p.Gq, p.S0, Hkv);
-      // without a prefix nothing joins parts of every row: rows that see nothing are zeroed here
-      if (p.S0 == 0 && b % (int)gridDim.x == (int)blockIdx.x) {
-        const int o0 = max(__ldg(p.offsets + b), 0), o1 = min(__ldg(p.offsets + b + 1), p.N);
-        const int z1 = s.n ? min(o1, o0 + max(s.n - s.len, 0)) : o1;
-        for (long long i = (long long)o0 * p.Hq * (kHeadDim / 8); i < (long long)z1 * p.Hq * (kHeadDim / 8); ++i)
+      // without a prefix nothing joins parts of every row: rows that see nothing, or that are before the first
+      // sequence, are zeroed here, all CTAs sharing them
+      if (p.S0 == 0) {
+        const int o0 = __ldg(p.offsets + b), o1 = min(__ldg(p.offsets + b + 1), p.N);
+        const int z0 = b ? max(o0, 0) : 0, z1 = s.n ? min(o1, o0 + max(s.n - s.len, 0)) : o1;
+        for (long long i = (long long)z0 * p.Hq * (kHeadDim / 8) + blockIdx.x; i < (long long)z1 * p.Hq * (kHeadDim / 8);
+             i += gridDim.x)
           reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0u, 0u, 0u, 0u);
       }
     }

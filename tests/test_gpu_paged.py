@@ -412,6 +412,42 @@ def test_attend_refused_on_the_device(P):
         assert word(c) == P.PALU_DEVERR_CAPACITY
 
 
+@pytest.mark.parametrize("shared", [0, 1])
+def test_rows_before_the_first_sequence_and_bad_spans(P, shared):
+    """Offsets that begin behind 0, or that a sequence has too many rows of: the error word and zeros, with a shared prefix
+    or without, and the other sequences served."""
+    q = torch.randn(9, 4, D, generator=torch.Generator().manual_seed(3)).half()
+    for first, new, max_new, bad in ((2, [1, 2, 1], 2, []), (7, [1, 0, 1], 40, []), (0, [1, 7, 1], 6, [1]), (0, [6, 1, 2], 2, [0]),
+                                     (3, [0, 0, 0], 2, [])):
+        lengths = [40, 33, 25]
+        pools, dev, c = make_cache(P, torch.float16, lengths, 16, 2, seed=11, width=3, shared=shared)
+        out = torch.full((9, 4, D), 7.0, dtype=torch.float16, device=DEV)
+        off = offsets_of(new) + first
+        end = first + sum(new)
+        c.attend(q.to(DEV), off, max_new, shared_pages=shared, out=out)
+        with pytest.raises(P.PaluError) as e:
+            c.sync()
+        assert f"word {P.PALU_DEVERR_SPAN}:" in str(e.value)
+        assert (out[end:] == 7).all() and (out[:first] == 0).all()
+        ref, mag = ref_attend(q[first:end], pools, c.page_table.cpu(), lengths, new, 16)
+        row = 0
+        for b, n in enumerate(new):
+            if b in bad:
+                assert (out[first + row:first + row + n] == 0).all()
+            elif n:
+                attend_close(out[first + row:first + row + n], ref[row:row + n], mag[row:row + n], torch.float16)
+            row += n
+
+
+@pytest.mark.parametrize("n", [1, 3000])
+def test_all_rows_of_a_large_call_see_nothing(P, n):
+    pools, dev, c = make_cache(P, torch.bfloat16, [0, 0], 16, 2, seed=3, width=5)
+    q = torch.randn(2 * n, 64, D, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    out = torch.full((2 * n + 1, 64, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    c.attend(q, offsets_of([n, n]), n, out=out[:-1])
+    assert c.sync() == 0 and (out[:-1] == 0).all() and (out[-1] == 7).all()
+
+
 def test_shared_prefix_does_not_change_the_result(P):
     lengths, new, page, shared = [1000, 900, 1100], [4, 4, 4], 64, 13
     pools, dev, c = make_cache(P, torch.bfloat16, lengths, page, 4, seed=21, shared=shared)
