@@ -44,6 +44,7 @@ extern "C" {
  *            lengths - (n - a) (may be the same array).
  *   tokens   device int64 [batch, k+1]: the kept drafts, the drawn token,
  *            then -1.  The drawn token is -1 where no weight is positive.
+ *            Must not overlap an input.
  *   n_kept   device int32 [batch]: a.
  * k in 1 .. 256.  One kernel launch, no workspace. */
 palu_status palu_draft_verify(int64_t batch, int32_t k, int64_t vocab, const float* target,

@@ -67,7 +67,8 @@ typedef struct {
  *   positions  device int64 [batch, tokens] (read only where there is a
  *          table; may be NULL without one).
  *   q_out  device [batch, q_heads, tokens, 128], k_out the same with
- *          kv_heads; contiguous, 16-byte aligned, not overlapping the inputs.
+ *          kv_heads; contiguous, 16-byte aligned, overlapping neither the
+ *          inputs nor each other.
  *   error  device uint32 (may be NULL): PALU_DEVERR_POSITION is set when a
  *          position lies outside the table; that token's rows become NaN.
  * One kernel launch. */
@@ -115,7 +116,8 @@ palu_status palu_paged_cache_init(palu_paged_cache* cache, int32_t dtype, int32_
  *          touched.  n_b may be 0.
  *   q      device [tokens, q_heads, 128], strides token and head, or NULL
  *          (then q_out is NULL and q_heads 0); k and v device
- *          [tokens, kv_heads, 128]; alignment as in palu_qk_norm_rope.
+ *          [tokens, kv_heads, 128]; alignment as in palu_qk_norm_rope.  None
+ *          of them may lie in the rows of the pages that the call writes.
  *   positions  device int64 [tokens], the positions of the rotation; NULL:
  *          each token's place in its sequence.
  *   q_out  device [tokens, q_heads, 128] contiguous, not overlapping q, k or v.

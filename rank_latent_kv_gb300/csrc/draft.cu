@@ -276,7 +276,14 @@ extern "C" palu_status palu_draft_verify(int64_t batch, int32_t k, int64_t vocab
     return fail(PALU_ERR_INVALID_ARG, "NULL pointer");
   if (draft && !draft_strides) return fail(PALU_ERR_INVALID_ARG, "draft_strides is NULL");
   if (!lengths != !new_lengths) return fail(PALU_ERR_INVALID_ARG, "lengths and new_lengths come together");
-  if (tokens == drafts) return fail(PALU_ERR_INVALID_ARG, "tokens must not be the drafts' array");
+  // a sequence's tokens must not overwrite another's drafts or lengths
+  auto overlap = [&](const void* in, int64_t bytes) {
+    const char *o = reinterpret_cast<const char*>(tokens), *x = static_cast<const char*>(in);
+    return in && o < x + bytes && x < o + batch * (k + 1) * (int64_t)sizeof(int64_t);
+  };
+  if (overlap(drafts, batch * k * 8) || overlap(n_drafts, batch * 4) || overlap(accept_u, batch * k * 4) ||
+      overlap(sample_u, batch * 4) || overlap(lengths, batch * 8))
+    return fail(PALU_ERR_INVALID_ARG, "tokens must not overlap an input");
   if (target_strides[0] < 0 || target_strides[1] < 0 || (draft && (draft_strides[0] < 0 || draft_strides[1] < 0)))
     return fail(PALU_ERR_INVALID_ARG, "strides must not be negative");
   if (((uintptr_t)target | (uintptr_t)draft | (uintptr_t)accept_u | (uintptr_t)sample_u | (uintptr_t)n_kept |

@@ -246,10 +246,11 @@ extern "C" palu_status palu_qk_norm_rope(const palu_qk_transform* transform, int
   if (!q_out || !k_out || (((uintptr_t)q_out | (uintptr_t)k_out) & 15))
     return fail(PALU_ERR_INVALID_ARG, "q_out and k_out must be 16-byte aligned");
   const int64_t qe[3] = {batch, tokens, q_heads}, ke[3] = {batch, tokens, kv_heads};
-  const int64_t q_rows = batch * tokens * q_heads, k_rows = batch * tokens * kv_heads;
+  const int64_t q_rows = batch * tokens * q_heads, k_rows = batch * tokens * kv_heads, row_stride = kHeadDim;
   if (rows_overlap(q_out, q_rows, q, q_strides, qe, 3) || rows_overlap(q_out, q_rows, k, k_strides, ke, 3) ||
-      rows_overlap(k_out, k_rows, q, q_strides, qe, 3) || rows_overlap(k_out, k_rows, k, k_strides, ke, 3))
-    return fail(PALU_ERR_INVALID_ARG, "an output overlaps an input");
+      rows_overlap(k_out, k_rows, q, q_strides, qe, 3) || rows_overlap(k_out, k_rows, k, k_strides, ke, 3) ||
+      rows_overlap(q_out, q_rows, k_out, &row_stride, &k_rows, 1))
+    return fail(PALU_ERR_INVALID_ARG, "an output overlaps an input or the other output");
   if (transform->cos_sin && (!positions || ((uintptr_t)positions & 7)))
     return fail(PALU_ERR_INVALID_ARG, "positions must be given, 8-byte aligned, with a table");
   QkParams p = {};

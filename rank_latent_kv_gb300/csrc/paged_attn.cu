@@ -12,7 +12,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "paged_attn.cuh"
 #include "splitk_attend.cuh"

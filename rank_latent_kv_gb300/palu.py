@@ -728,7 +728,7 @@ def draft_verify(target, draft, drafts, accept_u, sample_u, n_drafts=None, lengt
         raise ValueError("drafts must be a tensor [batch, k]") from None
     rows = (B,)
     xp = _at(drafts, "drafts", shape, _I64, dev)
-    V = target.shape[-1]
+    V = target.shape[-1] if target.dim() else 0
     tp, ts = _table(target, "target", (B, k + 1, V), dev)
     dp, ds = (None, None) if draft is None else _table(draft, "draft", (B, k, V), dev)
     ap, up = _at(accept_u, "accept_u", shape, _F32, dev), _at(sample_u, "sample_u", rows, _F32, dev)

@@ -136,3 +136,21 @@ def test_draft_verify_refusals(palu):
                 dict(ts=(-1, 50)), dict(ds=(150, -1)), dict(x=None), dict(x=A + 4), dict(au=None), dict(su=None), dict(tok=None),
                 dict(tok=A), dict(kept=None), dict(le=A), dict(nl=A), dict(n=A + 1)):
         assert call(**bad) in (1, 2) and palu.palu_last_error(), bad
+
+
+def test_outputs_that_overlap_are_refused(palu):
+    t = transform(palu)
+    n = 2 * 3 * 2 * 128 * 2                      # bytes of k_out
+
+    def rope(qo, ko):
+        return palu.lib().palu_qk_norm_rope(ctypes.byref(t), 0, 2, 3, 4, 2, A, I64x3(1536, 512, 128), A, I64x3(768, 256, 128), A, qo,
+                                            ko, None, None)
+    for qo, ko in ((2 * A, 2 * A), (2 * A, 2 * A + n), (2 * A + n - 256, 2 * A)):
+        assert rope(qo, ko) == 1 and b"overlap" in palu.lib().palu_last_error()
+
+    # tokens [2, 4] (64 bytes) against drafts [2, 3] (48), n_drafts (8), accept_u (24), sample_u (8), lengths (16)
+    def verify(tok, x=2 * A, n=3 * A, au=4 * A, su=5 * A, le=6 * A):
+        return palu.lib().palu_draft_verify(2, 3, 50, A, I64x2(200, 50), A, I64x2(150, 50), x, n, au, su, le, tok, A, A, None)
+    for at, size in ((2 * A, 48), (3 * A, 8), (4 * A, 24), (5 * A, 8), (6 * A, 16)):
+        for tok in (at, at + size - 8, at - 56):
+            assert verify(tok) == 1 and b"overlap" in palu.lib().palu_last_error(), (at, tok)
