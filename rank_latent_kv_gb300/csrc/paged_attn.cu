@@ -435,6 +435,19 @@ struct JoinRowsParams {
   PartSet prefix, own;
 };
 
+// Ticks of a sequence's own units before row tile `rts`, added up by a whole warp: a long chunk has hundreds of row
+// tiles, and every row's join asks.
+template <int R>
+__device__ __forceinline__ long long seq_ticks_warp(const SeqSpan& s, int rts, int Gq, int S0, int kv_heads) {
+  long long t = 0;
+  for (int rt = threadIdx.x & 31; rt < rts; rt += 32) t += unit_ticks<R>(R, own_tiles(s, rt * R, R, Gq, S0));
+  if (rts) {
+#pragma unroll
+    for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+  }
+  return t * kv_heads;
+}
+
 template <int R>
 __device__ __forceinline__ void own_place(const JoinRowsParams& p, const SeqSpan& s, int b, int kh, int lr, long long* f,
                                           int* n, int* t) {
@@ -442,7 +455,7 @@ __device__ __forceinline__ void own_place(const JoinRowsParams& p, const SeqSpan
   const int rt = lr / R, rows = min(R, s.n * a.Gq - rt * R);
   *n = own_tiles(s, rt * R, rows, a.Gq, a.S0);
   *t = LineCost<R>::tile(rows);
-  *f = __ldcg(p.own.plan + 1 + b) + seq_ticks<R>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R>(rows, *n) +
+  *f = __ldcg(p.own.plan + 1 + b) + seq_ticks_warp<R>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R>(rows, *n) +
        LineCost<R>::unit(rows);
 }
 template <int R>
@@ -608,6 +621,31 @@ static int split_grid(const palu_paged_cache* c, int64_t all_rows, int32_t share
   return best;
 }
 
+// Whether reading the shared pages once pays.  It saves the tiles that the sequences would each read (a row tile each at
+// least) beyond those of the whole batch's row tiles; it costs a second launch and, for every row, a record of each part
+// that is written, read and joined.  28 heads of 4 KV heads, 512 own keys, bf16, read once and by each sequence: 16
+// sequences of 1 token behind 1024 keys 19.1 and 14.3 us, behind 4096 23.3 and 33.0; 256 sequences of 5 behind 256 129 and
+// 95 us, behind 4096 185 and 442; 16 of 1024 new tokens behind 8192 1901 and 1506 us.  In clocks, summed over the SMs:
+constexpr double kShareTile = 2900., kShareRow = 350., kShareLaunch = 13300.;
+
+// The most new tokens a call for which it can (the tiles saved are at most one a sequence, KV head and tile of the table).
+static int64_t most_shared_tokens(const palu_paged_cache* c, int32_t q_heads) {
+  const double tiles = prefix_tiles_of(c->table_width * c->page_size);
+  const double n = (kShareTile * c->kv_heads * tiles * c->batch - kShareLaunch * device_sm_count()) / (kShareRow * q_heads);
+  return std::max<int64_t>(1, (int64_t)n);
+}
+static bool share_pays(const palu_paged_cache* c, int64_t tokens, int32_t q_heads, int32_t max_new, int32_t shared_pages) {
+  if (shared_pages == 0 || c->batch == 1 || tokens > most_shared_tokens(c, q_heads)) return false;
+  const int Gq = q_heads / c->kv_heads;
+  auto row_tiles = [&](double new_tokens) { return ceil(new_tokens * Gq / kManyRows); };
+  // the counts are the device's: as many sequences as can be with the most new tokens, one token for the others
+  const double many = std::min<int64_t>(max_new, tokens), B = std::min<int64_t>(c->batch, tokens);
+  const double full = many > 1 ? std::min(B, (tokens - B) / (many - 1)) : 0;
+  const double saved = full * row_tiles(many) + (B - full) * row_tiles(1) - row_tiles((double)tokens);
+  return kShareTile * c->kv_heads * prefix_tiles_of(shared_pages * c->page_size) * saved >
+         kShareRow * (double)tokens * q_heads + kShareLaunch * device_sm_count();
+}
+
 static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_t q_heads, int32_t max_new,
                                int32_t shared_pages, AttnLayout* l) {
   palu_status st = paged_check(c);
@@ -620,7 +658,7 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   if (shared_pages < 0 || shared_pages > c->table_width)
     return fail(PALU_ERR_INVALID_ARG, "shared_pages must be in [0, table_width]");
   const int64_t own_rows = std::min<int64_t>(max_new, tokens) * Gq, all_rows = tokens * Gq;
-  l->shared = shared_pages > 0 && c->batch > 1;
+  l->shared = share_pays(c, tokens, q_heads, max_new, shared_pages);
   l->R_prefix = all_rows <= 8 ? 8 : all_rows <= 16 ? 16 : kManyRows;
   const int R_rows = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
   // Few own keys behind a prefix of many rows: one launch for both (256 rows behind 311,296 shared tokens and 1 own token
@@ -646,18 +684,22 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   const int grid = device_sm_count();
   l->grid_prefix = two && grid > 1 ? split_grid(c, all_rows, shared_pages, l->R_prefix, grid) : grid;
   l->grid_own = two && grid > 1 ? grid - l->grid_prefix : grid;
-  l->row_ml = l->shared ? take(2 * (size_t)tokens * q_heads * sizeof(float2)) : 0;
-  l->row_acc = l->shared ? take(2 * (size_t)tokens * q_heads * kHeadDim * sizeof(float)) : 0;
+  // With shared pages the size is the same whether or not they are read once here: it also serves fewer tokens, and
+  // any other number of them.
+  const bool may_share = shared_pages > 0 && c->batch > 1;
+  const size_t records = may_share ? 2 * (size_t)std::min(tokens, most_shared_tokens(c, q_heads)) * q_heads : 0;
+  l->row_ml = take(records * sizeof(float2));
+  l->row_acc = take(records * kHeadDim * sizeof(float));
+  const size_t parts = o;
   take_parts(l->R_own, &l->plan_o, &l->begun_o, &l->ml_o, &l->acc_o);
   if (two) take_parts(l->R_prefix, &l->plan_p, &l->begun_p, &l->ml_p, &l->acc_p);
   l->total = o;
-  if (l->one_launch) {
-    // what two launches would take, so that a workspace also serves fewer new tokens or another number of shared pages
+  if (may_share) {
     size_t unused;
-    o = l->plan_o;
+    o = parts;
     take_parts(R_rows, &unused, &unused, &unused, &unused);
     take_parts(l->R_prefix, &unused, &unused, &unused, &unused);
-    l->total = std::max(l->total, o);
+    l->total = o;
   }
   return PALU_OK;
 }

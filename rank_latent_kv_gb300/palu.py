@@ -676,7 +676,7 @@ class PagedCache:
     def attend(self, q, offsets, max_new, shared_pages=0, softmax_scale=0.0, workspace=None, out=None, stream=None):
         """Attention of the new tokens (already appended) over the cache: row r of q [N, Hq, 128], sequence b's token
         at place t, attends to tokens 0 .. t of its sequence.  max_new: the most rows a sequence has.  shared_pages:
-        leading page-table entries that are the same in every row; they are read once for the batch.  Returns out
+        leading page-table entries that are the same in every row; where that is faster they are read once for the batch.  Returns out
         [N, Hq, 128]; rows behind offsets[B] are left as they were."""
         dev = self._on_current()
         n, hq, _ = shape = _shape_of(q, "q", 3)

@@ -483,6 +483,68 @@ def test_long_units_on_all_sms(P, page, Hk, new):
         assert bool(((out[0][:, i].float() - one).abs() <= bar).all())
 
 
+SHARED = [  # page, new, lengths, Hq, Hk, shared pages: sizes at which the shared pages are read once
+    (16, [1] * 8, [257 + 40 * i for i in range(8)], 64, 64, 16), (64, [1] * 8, [257, 300, 256, 700, 0, 1, 255, 600], 64, 64, 4),
+    (16, [1] * 8, [288 + 37 * i for i in range(8)], 128, 64, 17), (128, [1] * 30, [257 + 60 * i for i in range(30)], 64, 32, 2),
+    (32, [2, 0, 1, 2, 2, 1, 0, 2], [700, 300, 290, 258, 257, 256, 20, 500], 64, 64, 8),
+    (16, [1, 5, 3, 5, 0, 5, 2, 4], [560, 516, 900, 512, 300, 570, 257, 515], 128, 64, 32),
+    (64, [20, 20, 1, 7, 20, 3, 0, 20], [700, 532, 600, 515, 300, 513, 10, 560], 96, 96, 8),
+    (32, [9, 1, 1, 9, 1, 2, 1, 1], [700, 641, 640, 649, 100, 660, 680, 661], 128, 32, 20),
+    (32, [1] * 6, [400, 256, 257, 290, 10, 500], 96, 96, 8),
+    (128, [3] * 30, [257 + 2 * i for i in range(30)], 48, 48, 2),
+]
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("page,new,lengths,Hq,Hk,shared", SHARED)
+def test_shared_pages_are_read_once(P, dt, page, new, lengths, Hq, Hk, shared):
+    """The other sequences' leading table entries name a page of NaN in the second call: only row 0's are read."""
+    d = DT[dt]
+    pools, dev, c = make_cache(P, d, lengths, page, Hk, seed=page + sum(lengths), shared=shared, spare=2)
+    n = sum(new)
+    q = torch.randn(n + 2, Hq, D, generator=torch.Generator().manual_seed(n)).to(d)
+    ref, mag = ref_attend(q[:n], pools, c.page_table.cpu(), lengths, new, page)
+    ws = c.attend_workspace(n + 2, Hq, max(new), shared)
+    out = [torch.full((n + 2, Hq, D), 7.0, dtype=d, device=DEV) for _ in range(3)]
+    c.attend(q.to(DEV), offsets_of(new), max(new), shared_pages=shared, workspace=ws, out=out[0])
+    c.attend(q.to(DEV), offsets_of(new), max(new), workspace=ws, out=out[1])
+    free = sorted(set(range(dev[0].shape[0])) - set(c.page_table.flatten().tolist()))[0]
+    for t in dev:
+        t[free] = float("nan")
+    c.page_table[1:, :shared] = free
+    c.attend(q.to(DEV), offsets_of(new), max(new), shared_pages=shared, workspace=ws, out=out[2])
+    assert c.sync() == 0
+    for o in out:
+        assert (o[n:] == 7).all()
+        attend_close(o[:n], ref, mag, d)
+    assert torch.equal(out[0], out[2])
+
+
+@pytest.mark.parametrize("new,shared", [([600, 1, 300, 0], 3), ([1500, 1500, 2, 1], 20)])
+def test_long_chunks_with_a_shared_prefix(P, new, shared):
+    """Chunks of many row tiles with shared pages named, against the same call without: spot rows against 64 bits."""
+    page, Hq, Hk = 64, 28, 4
+    lengths = [page * shared + n + 5 for n in new]
+    pools, dev, c = make_cache(P, torch.bfloat16, lengths, page, Hk, seed=41, shared=shared)
+    n = sum(new)
+    q = torch.randn(n, Hq, D, generator=torch.Generator().manual_seed(2)).bfloat16()
+    off = offsets_of(new)
+    a = c.attend(q.to(DEV), off, max(new), shared_pages=shared)
+    b = c.attend(q.to(DEV), off, max(new))
+    assert c.sync() == 0
+    eps = torch.finfo(torch.bfloat16).eps
+    row = 0
+    for i, m in enumerate(new):
+        for t in sorted({0, m // 3, m - 1}) if m else ():
+            ref, mag = ref_attend(q[row + t:row + t + 1], pools, c.page_table.cpu()[i:i + 1], [lengths[i] - (m - 1 - t)], [1], page)
+            for o in (a, b):
+                attend_close(o[row + t:row + t + 1], ref, mag, torch.bfloat16)
+        row += m
+    # all rows: both lie within the bar of the exact value, whose size is bounded by the largest value
+    top = max(float(x.abs().max()) for x in pools[1:])
+    assert float((a.float() - b.float()).abs().max()) <= 2 * (eps + 2.0 ** -12) * top
+
+
 def test_calls_repeat_bit_for_bit(P):
     pools, dev, c = make_cache(P, torch.float16, [3000, 17, 900], 32, 4, seed=22, shared=0)
     q = torch.randn(15, 12, D, generator=torch.Generator().manual_seed(5)).half().to(DEV)

@@ -154,3 +154,23 @@ def test_outputs_that_overlap_are_refused(palu):
     for at, size in ((2 * A, 48), (3 * A, 8), (4 * A, 24), (5 * A, 8), (6 * A, 16)):
         for tok in (at, at + size - 8, at - 56):
             assert verify(tok) == 1 and b"overlap" in palu.lib().palu_last_error(), (at, tok)
+
+
+def test_a_workspace_serves_calls_that_share_and_calls_that_do_not(palu):
+    """Whether shared pages are read once depends on the sizes: the size of a workspace must not fall where it changes."""
+    _, c = init(palu, hk=64, ks=(1 << 18, 2048, 128), vs=(1 << 18, 2048, 128), width=200, batch=30)
+    n = ctypes.c_size_t()
+
+    def size(tokens, new, shared):
+        assert palu.lib().palu_paged_attn_workspace_size(ctypes.byref(c), tokens, 128, new, shared, ctypes.byref(n)) == 0
+        return n.value
+    for new in (1, 3, 9, 200, 100000):
+        for shared in (0, 1, 8, 9, 100, 200):
+            sizes = [size(t, new, shared) for t in (1, 2, 29, 30, 31, 60, 90, 270, 300, 900, 1000, 2000, 5000, 6000, 10000, 100000)]
+            assert sizes == sorted(sizes)
+    for t in (30, 300, 5000, 100000):
+        for shared in (0, 1, 8, 9, 100, 200):
+            sizes = [size(t, new, shared) for new in (1, 2, 3, 8, 9, 10, 200, 100000)]
+            assert sizes == sorted(sizes)
+        assert len({size(t, 9, s) for s in (1, 7, 8, 9, 40, 200)}) == 1
+    assert size(100000, 9, 8) < 100000 * 128 * 520         # no record of every row where they are never shared
