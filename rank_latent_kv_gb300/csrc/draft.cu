@@ -50,6 +50,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Arrivals without an order of memory: enough to know that every CTA of the cluster has begun.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -107,6 +110,7 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(32 * WAR
   __shared__ int found, win;        // drawn token; its segment
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
+  cluster_arrive_relaxed();
   const long long b = blockIdx.x / kDraftCluster;
   const int n = d.n_drafts ? min(max(d.n_drafts[b], 0), d.k) : d.k;
   if (tid == 0) {
@@ -170,6 +174,9 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(32 * WAR
 #pragma unroll
     for (int x = 16; x; x >>= 1)
       sum = pair_add(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, x), __shfl_xor_sync(0xffffffffu, sum.y, x)));
+    // a CTA's shared memory may be written from outside only once the CTA has begun: a small vocabulary leaves segments
+    // empty, and their warps are here at once
+    if (pass == 0) cluster_wait();
     if (lane < kDraftCluster) store_remote(&sums[pass][seg0], lane, sum);
     cluster_sync();
     // the first warp of every CTA finds the segment of the drawn token
