@@ -462,7 +462,7 @@ template <int R>
 __device__ __forceinline__ void prefix_place(const JoinRowsParams& p, int kh, int lr, long long* f, int* n, int* t) {
   const AttnParams& a = p.a;
   const int all_rows = a.N * a.Gq, rts = (all_rows + R - 1) / R, rt = lr / R;
-  *n = prefix_tiles_of(a.S0);
+  *n = prefix_tiles_of((int)__ldcg(p.prefix.plan + 1 + a.c.batch));
   const int rows = min(R, all_rows - rt * R);
   *t = LineCost<R>::tile(rows);
   *f = kh * prefix_ticks<R>(all_rows, rts, *n) + prefix_ticks<R>(all_rows, rt, *n) + LineCost<R>::unit(rows);
@@ -675,7 +675,7 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     return at;
   };
   auto take_parts = [&](int R, size_t* plan, size_t* begun, size_t* ml, size_t* acc) {
-    *plan = take(sizeof(long long) * (1 + (size_t)c->batch));
+    *plan = take(sizeof(long long) * (2 + (size_t)c->batch));
     *begun = take(slots / 2 * sizeof(UnitMeta));
     *ml = take(slots * R * sizeof(float2));
     *acc = take(slots * R * kHeadDim * sizeof(float));

@@ -9,7 +9,9 @@
 // A row is one (new token, query head).  The rows that attend to the same
 // keys through the same KV head form units of up to R rows, R the row tile of
 // the kernel that takes them:
-//   prefix units (KV head, row tile): all rows of the batch, keys [0, S0);
+//   prefix units (KV head, row tile): all rows of the batch, keys [0, S0), or
+//     up to the longest length where no sequence has all of them: behind it
+//     pages may hold anything, and 0 * NaN is NaN;
 //   own units (sequence, row tile, KV head): keys [S0, the last row's place].
 // Units in this order make one line, measured in ticks: a unit takes a fixed
 // number for its beginning and end, then some for each of its 128-key tiles
@@ -52,7 +54,7 @@ struct UnitMeta {
 struct PartSet {
   float2* ml;       // [2 grid][R] (m, l)
   float* acc;       // [2 grid][R][128]
-  long long* plan;  // [0]: W; [1 + b]: where sequence b's own units begin
+  long long* plan;  // [0]: W; [1 + b]: where sequence b's own units begin; [1 + B]: the prefix units' last key
   UnitMeta* begun;  // [grid]: the unit that CTA c begins and a later one ends (rows 0: none)
   int grid, R;
 };
@@ -180,7 +182,7 @@ __device__ __forceinline__ long long prefix_ticks(int all_rows, int rts, int til
   return t;
 }
 
-__host__ __device__ inline int prefix_tiles_of(int S0) { return (S0 + kKeyTile - 1) / kKeyTile; }
+__host__ __device__ inline int prefix_tiles_of(int keys) { return (keys + kKeyTile - 1) / kKeyTile; }
 
 // Where a finished unit goes.
 enum { kToOut = -1, kToRow = -2 };
@@ -190,7 +192,9 @@ enum { kToOut = -1, kToRow = -2 };
 struct PlanScratch {
   long long warp_sum[16];
   long long w0, w1, W, base;
+  int warp_longest[16];
   int b;
+  int prefix_end;  // prefix units' keys: [0, prefix_end)
   int cut_prefix;  // a sequence does not see the whole prefix with all of its new tokens
 };
 
@@ -201,12 +205,11 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
   auto meet = [] { asm volatile("bar.sync 3, %0;" ::"n"(THREADS) : "memory"); };
   const int B = p.c.batch, Hkv = p.c.kv_heads;
   const int all_rows = p.N * p.Gq;
-  const long long prefix =
-      p.do_prefix ? Hkv * prefix_ticks<R>(all_rows, (all_rows + R - 1) / R, prefix_tiles_of(p.S0)) : 0;
   const int per = (B + nthr - 1) / nthr;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   unsigned bad = 0;
   long long mine = 0;
+  int longest = 0;  // of the sequences that have rows
   if (tid == 0) {
     sc->b = -1;
     sc->cut_prefix = 0;
@@ -216,6 +219,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
     for (int b = b0; b < b1; ++b) {
       const SeqSpan s = seq_span(p, b, &bad);
       if (s.n && row_limit(s, 0) < p.S0) sc->cut_prefix = 1;
+      if (s.n) longest = max(longest, s.len);
       if (!p.do_own) continue;
       mine += seq_ticks<R>(s, p.Gq, p.S0, Hkv);
       // without a prefix nothing joins parts of every row: rows that see nothing, or that are before the first
@@ -234,14 +238,24 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
     const long long y = __shfl_up_sync(0xffffffffu, incl, x);
     if (lane >= x) incl += y;
   }
-  if (lane == 31) sc->warp_sum[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    sc->warp_sum[warp] = incl;
+    sc->warp_longest[warp] = longest;
+  }
   meet();
-  long long before = prefix, total = prefix;
+  long long before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < nwarp; ++w) {
     if (w < warp) before += sc->warp_sum[w];
     total += sc->warp_sum[w];
+    longest = max(longest, sc->warp_longest[w]);
   }
+  const int prefix_end = min(p.S0, longest);
+  const long long prefix =
+      p.do_prefix ? Hkv * prefix_ticks<R>(all_rows, (all_rows + R - 1) / R, prefix_tiles_of(prefix_end)) : 0;
+  before += prefix;
+  total += prefix;
   before += incl - mine;
   // a stretch is never shorter than a tile, so that every CTA between a unit's first and last holds a part of it
   const long long W = max((total + gridDim.x - 1) / gridDim.x, (long long)LineCost<R>::kMaxTile);
@@ -268,7 +282,11 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
     sc->w0 = w0;
     sc->w1 = w1;
     sc->W = W;
-    if (blockIdx.x == 0) p.part.plan[0] = W;
+    sc->prefix_end = prefix_end;
+    if (blockIdx.x == 0) {
+      p.part.plan[0] = W;
+      p.part.plan[1 + B] = prefix_end;
+    }
     p.part.begun[blockIdx.x].rows = 0;
   }
   meet();
@@ -306,7 +324,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
   };
   long long base = 0;
   if (p.do_prefix) {
-    const int all_rows = p.N * p.Gq, rts = (all_rows + R - 1) / R, tiles = prefix_tiles_of(p.S0);
+    const int all_rows = p.N * p.Gq, rts = (all_rows + R - 1) / R, tiles = prefix_tiles_of(sc->prefix_end);
     const long long head = prefix_ticks<R>(all_rows, rts, tiles), full = unit_ticks<R>(R, tiles);
     m.pos = m.seq = 0;
     m.prefix = 1;
@@ -320,7 +338,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
           m.rows = min(R, all_rows - rt * R);
           m.tok = rt * R / p.Gq;
           m.g0 = rt * R - m.tok * p.Gq;
-          if (!run_unit(u0, tiles, 0, p.S0)) return;
+          if (!run_unit(u0, tiles, 0, sc->prefix_end)) return;
         }
     }
   }

@@ -1,0 +1,60 @@
+"""Attention behind a shared prefix, at sizes for which the shared pages are read
+once.  That they were is part of each test: in a second call the other
+sequences' leading table entries name a page of NaN, which only a call that
+reads row 0's pages leaves out of its result.  Bars as in test_gpu_paged.py."""
+import pytest
+import torch
+
+from test_gpu_paged import D, DEV, DT, attend_close, make_cache, offsets_of, ref_attend
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def P():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from rank_latent_kv_gb300 import palu
+    palu.lib()
+    return palu
+
+
+def hide_shared(c, dev, shared):
+    """Rows 1.. of the table name a page of NaN for the shared pages; returns the table as it was."""
+    was = c.page_table.clone()
+    free = sorted(set(range(dev[0].shape[0])) - set(was.flatten().tolist()))[0]
+    for t in dev:
+        t[free] = NAN
+    c.page_table[1:, :shared] = free
+    return was
+
+
+BEHIND = [  # page, new, lengths, Hq, Hk, shared pages, table width: no sequence as long as the named prefix
+    (16, [1] * 8, [100 + 17 * i for i in range(8)], 64, 64, 16, 16),          # up to 8 rows, two launches' sizes or one
+    (16, [1] * 8, [1 + 16 * i for i in range(8)], 64, 64, 32, 100),           # whole tiles that nobody sees
+    (64, [2, 0, 1, 2, 2, 1, 0, 2], [190, 300, 0, 129, 128, 127, 1, 191], 64, 64, 8, 30),  # 10 rows; the longest has none
+    (128, [1] * 30, [1 + 8 * i for i in range(30)], 64, 32, 2, 2),            # many rows, one launch
+    (32, [1] * 30, [200 + i for i in range(30)], 64, 32, 8, 60),              # many rows, own keys on few
+    (64, [20, 20, 1, 7, 20, 3, 0, 20], [300, 132, 200, 115, 300, 13, 10, 60], 96, 96, 8, 12),  # many rows throughout
+]
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("page,new,lengths,Hq,Hk,shared,width", BEHIND)
+def test_what_lies_behind_all_lengths_does_not_matter(P, dt, page, new, lengths, Hq, Hk, shared, width):
+    """Every sequence ends inside the named prefix (a fixed number of pages in a captured graph, after a rollback); NaN
+    behind the longest that has new rows."""
+    d = DT[dt]
+    seen = [l if m else 0 for l, m in zip(lengths, new)]
+    pools, dev, c = make_cache(P, d, seen, page, Hk, seed=page + sum(lengths), shared=shared, width=width, fill=NAN)
+    c.lengths.copy_(torch.tensor(lengths))
+    n = sum(new)
+    q = torch.randn(n, Hq, D, generator=torch.Generator().manual_seed(n)).to(d)
+    ref, mag = ref_attend(q, pools, c.page_table.cpu(), lengths, new, page)
+    a = c.attend(q.to(DEV), offsets_of(new), max(new), shared_pages=shared)
+    assert c.sync() == 0
+    attend_close(a, ref, mag, d)
+    hide_shared(c, dev, shared)
+    b = c.attend(q.to(DEV), offsets_of(new), max(new), shared_pages=shared)
+    assert c.sync() == 0 and torch.equal(a, b)
