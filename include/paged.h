@@ -149,8 +149,9 @@ palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_
  *   shared_pages  leading page-table entries that are the same pages in every
  *          row of the table.  Where that is faster (by the sizes given here)
  *          their keys and values are read once for the whole batch, from row
- *          0 of the table, whatever the length of sequence 0.  0: nothing is
- *          shared.  The result does not depend on it beyond rounding.
+ *          0 of the table, whatever the length of sequence 0, as far as the
+ *          longest sequence with new rows goes.  0: nothing is shared.  The
+ *          result does not depend on it beyond rounding.
  *   out    device [tokens, q_heads, 128], contiguous, the cache's type, not
  *          overlapping q; rows at and behind offsets[batch] are not touched.
  *   softmax_scale 0 selects 1/sqrt(128).
