@@ -160,7 +160,8 @@ palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_
  * infinities included; the values of its own tokens have to be finite (a
  * token that a query does not see yet has the weight 0, and 0 * NaN is NaN).
  * Weights are rounded to the cache's type once, where a KV head has more than
- * 16 rows; sums, maxima and accumulators are fp32.  One to three kernel
+ * 16 rows (in fp16 those under 2^-20 of a row's largest lose bits, and those
+ * under 2^-31 count only in the sum); sums, maxima and accumulators are fp32.  One to three kernel
  * launches on `stream`, chosen by the sizes given here, not by the lengths.
  * Repeating a call repeats its result bit for bit.  A sequence with more than
  * max_new rows or offsets out of order sets PALU_DEVERR_SPAN and its rows are

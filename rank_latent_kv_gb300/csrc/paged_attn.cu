@@ -8,7 +8,10 @@
 // one copy a page and 64-channel panel, and eight warps that take 16 tokens
 // of each tile: scores as K q^T with the tokens as the m side and the rows as
 // the n side of m16n8k16, so no product is spent on padding 3 or 7 rows to
-// 16; a running maximum a warp, merged once a unit.
+// 16; a running maximum a warp, merged once a unit.  In fp16 the weights'
+// reference lies 2^14 below the maximum: a warp may have 100,000 tokens whose
+// weights next to a first token's 1 would be below the smallest fp16 number,
+// and together count (304 sequences of 1,200,000: 36 times the bar of rounding).
 #include <math.h>
 
 #include <algorithm>
@@ -22,6 +25,8 @@ constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * (kFewWarps + 1);
 constexpr int kFewStages = 3;
 constexpr int kMergeStride = kHeadDim + 2;
+template <bool BF16>
+constexpr float kFewLift = BF16 ? 0.f : 14.f;  // log2: the largest weight; 2^14 < 65504
 
 // One tile, as the loading warp hands it to the others.
 struct TileMeta {
@@ -203,8 +208,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
               const float mn = fmaxf(m_run[nt][e], bm);
-              const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen so far: every weight is 0
-              const float al = ex2f_(m_run[nt][e] - ref);
+              const float top = mn == -INFINITY ? 0.f : mn;  // nothing seen so far: every weight is 0
+              const float al = ex2f_(m_run[nt][e] - top), ref = top - kFewLift<BF16>;
               m_run[nt][e] = mn;
               pr[e] = ex2f_(s[e] - ref);
               pr[e + 2] = ex2f_(s[e + 2] - ref);
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                                        : (long long)m.dest * p.part.R + r;
                 float2* ml = (m.dest == kToRow ? p.row_ml : p.part.ml) + rec;
                 float* ac = (m.dest == kToRow ? p.row_acc : p.part.acc) + rec * kHeadDim;
-                if (lane == 0) *ml = make_float2(M, L);
+                if (lane == 0) *ml = make_float2(M - kFewLift<BF16>, L);  // what the sums are relative to
                 *reinterpret_cast<float4*>(ac + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
               }
             }
