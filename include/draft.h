@@ -27,8 +27,11 @@ extern "C" {
  *   one more token is drawn from the weights w(t) = max(p_a(t) - q_a(t), 0)
  *   if a < n (from p_a where these are all zero), and from p_n if a = n:
  *   the lowest t with w(0) + .. + w(t) > sample_u[b] * (w(0) + .. + w(V-1)).
- * The products and sums are carried to at least 45 bits, so a token depends
- * neither on the order of summation nor on the launch.  Weights that are NaN
+ * The test of a draft is exact.  A running sum and u times the total are
+ * together right to (278 + 12 ceil(V / 16384)) 2^-48 of the total (2^-39 for a
+ * vocabulary of 152,065): a draw nearer than that to a border between two
+ * tokens may give either, and the other one in a batch of another size (a call
+ * that is repeated repeats its answer).  Weights that are NaN
  * count as 0; probabilities must be finite and need not be normalised.  A
  * draft outside 0 .. V-1 is never kept.
  *   target   device fp32, row (b, i) at target + b * target_strides[0] +

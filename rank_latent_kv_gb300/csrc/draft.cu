@@ -12,8 +12,18 @@
 // five fp64 instructions a value would take about 80 us for 64 rows of 152,065,
 // against 12 us of reading.  So everything is an unevaluated pair of floats:
 // a difference is its rounded value and the exact remainder, a sum carries its
-// rounding errors along (about 17 fp32 instructions a value), right to about
-// 2^-45 of the sum.
+// rounding errors along (about 18 fp32 instructions a value).
+//
+// How far a sum may be off, with u = 2^-24.  Eight values: seven remainders of
+// at most u times the sum each are added up in one float, 49 u^2 at worst.  Two
+// pairs: 3 u^2 of the result (16 u^2 of the eight values, whose remainder is not
+// yet small).  A lane adds up nb groups of eight, then lanes, segments and CTAs
+// follow in at most 18 sums of pairs: (66 + 3 nb + 54) u^2 with nb = V / 16384 at
+// most.  The running sum of the drawn token adds the rescan of its segment, 36 +
+// 6 nb, and what it is compared with is the total scaled, 2 more: together
+// (278 + 12 nb) 2^-48 of the total, 2^-39 for 152,065 tokens.  (One remainder
+// carried through a lane's whole stretch grew with its length instead: 2^-45 at
+// 75 values a lane, but 2^-28 at 20,000.)
 #include <algorithm>
 
 #include "draft.h"
@@ -139,7 +149,7 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(32 * WAR
   const long long t0 = (long long)seg0 * d.seg, t1 = min(t0 + d.seg, (long long)d.V);
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    float s = 0.f, e = 0.f;
+    float2 run = make_float2(0.f, 0.f);
     // eight values of each row a lane at a time, the next eight on their way meanwhile; behind the segment's end lanes
     // read its last value, with weight 0
     const int len = (int)(t1 - t0), skip_at = skip >= t0 && skip < t1 ? (int)(skip - t0) : -1;
@@ -151,13 +161,19 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(32 * WAR
       for (int i = 0; i < 8; ++i) q[i] = qseg ? __ldcs(qseg + min(t + 32 * i, len - 1)) : 0.f;
     };
     auto add = [&](int t, const float (&p)[8], const float (&q)[8]) {
+      float2 eight;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float hi, lo, r;
         draft_weight(t + 32 * i == skip_at || t + 32 * i >= len ? 0.f : p[i], q[i], hi, lo);
-        two_sum(s, hi, s, r);
-        e = __fadd_rn(e, __fadd_rn(r, lo));
+        if (i == 0) {
+          eight = make_float2(hi, lo);
+        } else {
+          two_sum(eight.x, hi, eight.x, r);
+          eight.y = __fadd_rn(eight.y, __fadd_rn(r, lo));
+        }
       }
+      run = pair_add(run, eight);
     };
     if (len > 0) {
       float p0[8], q0[8], p1[8], q1[8];
@@ -170,21 +186,20 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(32 * WAR
         add(t + 8 * 32, p1, q1);
       }
     }
-    float2 sum = pair_add(make_float2(s, 0.f), make_float2(e, 0.f));
 #pragma unroll
     for (int x = 16; x; x >>= 1)
-      sum = pair_add(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, x), __shfl_xor_sync(0xffffffffu, sum.y, x)));
+      run = pair_add(run, make_float2(__shfl_xor_sync(0xffffffffu, run.x, x), __shfl_xor_sync(0xffffffffu, run.y, x)));
     // a CTA's shared memory may be written from outside only once the CTA has begun: a small vocabulary leaves segments
     // empty, and their warps are here at once
     if (pass == 0) cluster_wait();
-    if (lane < kDraftCluster) store_remote(&sums[pass][seg0], lane, sum);
+    if (lane < kDraftCluster) store_remote(&sums[pass][seg0], lane, run);
     cluster_sync();
     // the first warp of every CTA finds the segment of the drawn token
     if (warp == 0) {
-      float2 v[PER_LANE], run = make_float2(0.f, 0.f);
+      float2 v[PER_LANE], mine_sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < PER_LANE; ++i) run = pair_add(run, v[i] = sums[pass][lane * PER_LANE + i]);
-      const float2 incl = warp_scan(run, lane), total = shfl(incl, 31), want = pair_scale(total, d.sample_u[b]);
+      for (int i = 0; i < PER_LANE; ++i) mine_sum = pair_add(mine_sum, v[i] = sums[pass][lane * PER_LANE + i]);
+      const float2 incl = warp_scan(mine_sum, lane), total = shfl(incl, 31), want = pair_scale(total, d.sample_u[b]);
       float2 c = before_lane(incl, lane), mine_before = c;
       int mine = SEGS;
 #pragma unroll

@@ -37,3 +37,26 @@ def test_short_rows_of_many_sequences(P, B, V):
     torch.cuda.synchronize()
     for out, kept in outs:
         assert np.array_equal(kept.cpu().numpy(), rk) and np.array_equal(out.cpu().numpy(), rt)
+
+
+@pytest.mark.parametrize("B", [18, 64])
+def test_long_rows_keep_the_stated_bound(P, B):
+    """A row of 41 million weights that are whole numbers, so that the definition is exact in integers: every drawn token's
+    border lies within (278 + 12 ceil(V / 16384)) 2^-48 of the total (include/draft.h).  Its first half is flat: equal
+    values round alike, so that what is lost adds up; the powers of two behind it lose nothing."""
+    V, k = 41_000_003, 1
+    g = torch.Generator(device=DEV).manual_seed(B)
+    w = torch.full((V,), 1 << 23, device=DEV)
+    w[:V // 2] = 12345679
+    ui = torch.randint(0, 1 << 24, (B,), generator=g, device=DEV)
+    t = (w.double() * 2.0 ** -24).float()[None, None].expand(B, k + 1, V)
+    z = torch.zeros(B, k, dtype=torch.int64, device=DEV)
+    out, kept, _ = P.draft_verify(t, None, z, torch.zeros(B, k, device=DEV), (ui.double() * 2.0 ** -24).float(),
+                                  n_drafts=torch.zeros(B, dtype=torch.int32, device=DEV))
+    cum = w.cumsum(0).cpu()
+    total = int(cum[-1])
+    tol = total * (278 + 12 * -(-V // 16384)) / 2 ** 48
+    assert (kept == 0).all()
+    for token, u in zip(out[:, 0].tolist(), ui.tolist()):
+        want = total * u / 2 ** 24                        # 73 bits, rounded to 53: far below tol
+        assert (int(cum[token - 1]) if token else 0) - tol <= want < int(cum[token]) + tol, (token, u)
