@@ -47,8 +47,9 @@ extern "C" {
  *            lengths - (n - a) (may be the same array).
  *   tokens   device int64 [batch, k+1]: the kept drafts, the drawn token,
  *            then -1.  The drawn token is -1 where no weight is positive.
- *            Must not overlap an input.
- *   n_kept   device int32 [batch]: a.
+ *   n_kept   device int32 [batch]: a (may be the array n_drafts).
+ * Outputs must overlap neither an input nor each other, but for the two that
+ * may be the same array.
  * k in 1 .. 256.  One kernel launch, no workspace. */
 palu_status palu_draft_verify(int64_t batch, int32_t k, int64_t vocab, const float* target,
                               const int64_t target_strides[2], const float* draft, const int64_t draft_strides[2],

@@ -281,6 +281,25 @@ __global__ void __cluster_dims__(kDraftCluster, 1, 1) __launch_bounds__(32 * WAR
   }
 }
 
+// Memory of an argument (at NULL: none).
+struct Range {
+  const void* at;
+  int64_t bytes;
+};
+static bool overlap(const Range& a, const Range& b) {
+  const char *x = static_cast<const char*>(a.at), *y = static_cast<const char*>(b.at);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// Bytes from a table's first value to behind its last; false where that is more than 2^62.
+static bool table_bytes(int64_t batch, int64_t rows, int64_t vocab, const int64_t* strides, int64_t* bytes) {
+  int64_t a, b, n;
+  if (__builtin_mul_overflow(batch - 1, strides[0], &a) || __builtin_mul_overflow(rows - 1, strides[1], &b) ||
+      __builtin_add_overflow(a, b, &n) || __builtin_add_overflow(n, vocab, &n) || n > (1LL << 60))
+    return false;
+  *bytes = 4 * n;
+  return true;
+}
+
 }  // namespace palu
 
 using namespace palu;
@@ -298,16 +317,25 @@ extern "C" palu_status palu_draft_verify(int64_t batch, int32_t k, int64_t vocab
     return fail(PALU_ERR_INVALID_ARG, "NULL pointer");
   if (draft && !draft_strides) return fail(PALU_ERR_INVALID_ARG, "draft_strides is NULL");
   if (!lengths != !new_lengths) return fail(PALU_ERR_INVALID_ARG, "lengths and new_lengths come together");
-  // a sequence's tokens must not overwrite another's drafts or lengths
-  auto overlap = [&](const void* in, int64_t bytes) {
-    const char *o = reinterpret_cast<const char*>(tokens), *x = static_cast<const char*>(in);
-    return in && o < x + bytes && x < o + batch * (k + 1) * (int64_t)sizeof(int64_t);
-  };
-  if (overlap(drafts, batch * k * 8) || overlap(n_drafts, batch * 4) || overlap(accept_u, batch * k * 4) ||
-      overlap(sample_u, batch * 4) || overlap(lengths, batch * 8))
-    return fail(PALU_ERR_INVALID_ARG, "tokens must not overlap an input");
   if (target_strides[0] < 0 || target_strides[1] < 0 || (draft && (draft_strides[0] < 0 || draft_strides[1] < 0)))
     return fail(PALU_ERR_INVALID_ARG, "strides must not be negative");
+  int64_t target_bytes, draft_bytes = 0;
+  if (!table_bytes(batch, k + 1, vocab, target_strides, &target_bytes) ||
+      (draft && !table_bytes(batch, k, vocab, draft_strides, &draft_bytes)))
+    return fail(PALU_ERR_INVALID_ARG, "strides span more than the address space");
+  // a sequence's answer must not overwrite what another has yet to read or has written
+  const Range outs[3] = {{tokens, batch * (k + 1) * 8}, {n_kept, batch * 4}, {new_lengths, batch * 8}};
+  const Range ins[7] = {{target, target_bytes}, {draft, draft_bytes}, {drafts, batch * k * 8}, {n_drafts, batch * 4},
+                        {accept_u, batch * k * 4}, {sample_u, batch * 4}, {lengths, batch * 8}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& in : ins) {
+      // each sequence's element is read before its own is written
+      const bool same = outs[i].at == in.at && ((i == 2 && in.at == lengths) || (i == 1 && in.at == n_drafts));
+      if (overlap(outs[i], in) && !same) return fail(PALU_ERR_INVALID_ARG, "an output overlaps an input");
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return fail(PALU_ERR_INVALID_ARG, "outputs overlap each other");
+  }
   if (((uintptr_t)target | (uintptr_t)draft | (uintptr_t)accept_u | (uintptr_t)sample_u | (uintptr_t)n_kept |
        (uintptr_t)n_drafts) & 3 ||
       ((uintptr_t)drafts | (uintptr_t)tokens | (uintptr_t)lengths | (uintptr_t)new_lengths) & 7)

@@ -60,3 +60,24 @@ def test_long_rows_keep_the_stated_bound(P, B):
     for token, u in zip(out[:, 0].tolist(), ui.tolist()):
         want = total * u / 2 ** 24                        # 73 bits, rounded to 53: far below tol
         assert (int(cum[token - 1]) if token else 0) - tol <= want < int(cum[token]) + tol, (token, u)
+
+
+def test_counts_and_lengths_in_place(P):
+    """n_kept may be n_drafts, new_lengths may be lengths; a view shifted by one sequence is refused."""
+    B, k, V = 200, 3, 301
+    t, d, x, au, su = inputs(B, k, V, 5)
+    n = np.arange(B, dtype=np.int32) % (k + 1)
+    rt, rk = reference(t, d, x, au, su, n)
+    dev = lambda a: torch.from_numpy(a).to(DEV)
+    t, d, x, au, su = map(dev, (t, d, x, au, su))
+    for _ in range(5):
+        count, length = torch.zeros(B + 1, dtype=torch.int32, device=DEV), torch.full((B + 1,), 100, device=DEV)
+        count[:B] = dev(n)
+        toks, kept, new = P.draft_verify(t, d, x, au, su, n_drafts=count[:B], lengths=length[:B], n_kept=count[:B],
+                                         new_lengths=length[:B])
+        assert np.array_equal(toks.cpu().numpy(), rt) and np.array_equal(kept.cpu().numpy(), rk)
+        assert np.array_equal(new.cpu().numpy(), 100 - (n - rk))
+    with pytest.raises(P.PaluError, match="overlap"):
+        P.draft_verify(t, d, x, au, su, n_drafts=count[:B], n_kept=count[1:])
+    with pytest.raises(P.PaluError, match="overlap"):
+        P.draft_verify(t, d, x, au, su, lengths=length[:B], new_lengths=length[1:])
