@@ -194,7 +194,7 @@ struct PlanScratch {
   long long w0, w1, W, base;
   int warp_longest[16];
   int b;
-  int prefix_end;  // prefix units' keys: [0, prefix_end)
+  int prefix_end;  // prefix units' keys: [0, prefix_end), where the launch has prefix units
   int cut_prefix;  // a sequence does not see the whole prefix with all of its new tokens
 };
 
@@ -238,24 +238,24 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
     const long long y = __shfl_up_sync(0xffffffffu, incl, x);
     if (lane >= x) incl += y;
   }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) {
-    sc->warp_sum[warp] = incl;
-    sc->warp_longest[warp] = longest;
-  }
+  if (p.do_prefix) sc->warp_longest[warp] = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) sc->warp_sum[warp] = incl;
   meet();
   long long before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < nwarp; ++w) {
     if (w < warp) before += sc->warp_sum[w];
     total += sc->warp_sum[w];
-    longest = max(longest, sc->warp_longest[w]);
   }
-  const int prefix_end = min(p.S0, longest);
-  const long long prefix =
-      p.do_prefix ? Hkv * prefix_ticks<R>(all_rows, (all_rows + R - 1) / R, prefix_tiles_of(prefix_end)) : 0;
-  before += prefix;
-  total += prefix;
+  long long prefix = 0;
+  if (p.do_prefix) {
+#pragma unroll
+    for (int w = 0; w < nwarp; ++w) longest = max(longest, sc->warp_longest[w]);
+    longest = min(longest, p.S0);
+    prefix = Hkv * prefix_ticks<R>(all_rows, (all_rows + R - 1) / R, prefix_tiles_of(longest));
+    before += prefix;
+    total += prefix;
+  }
   before += incl - mine;
   // a stretch is never shorter than a tile, so that every CTA between a unit's first and last holds a part of it
   const long long W = max((total + gridDim.x - 1) / gridDim.x, (long long)LineCost<R>::kMaxTile);
@@ -282,10 +282,10 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
     sc->w0 = w0;
     sc->w1 = w1;
     sc->W = W;
-    sc->prefix_end = prefix_end;
+    sc->prefix_end = longest;
     if (blockIdx.x == 0) {
       p.part.plan[0] = W;
-      p.part.plan[1 + B] = prefix_end;
+      if (p.do_prefix) p.part.plan[1 + B] = longest;
     }
     p.part.begun[blockIdx.x].rows = 0;
   }
