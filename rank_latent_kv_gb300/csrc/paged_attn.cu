@@ -1,17 +1,4 @@
-// Attention over the paged cache for few rows a KV head (single-token decode,
-// a few drafted tokens), the joining of partial results, and the host side.
-//
-// paged_few_kernel is bound by reading the cache: 512 bytes a token and KV
-// head feed 4 * 128 * rows flops, far below the card's ratio for up to 16
-// rows.  So everything serves the loads: one persistent CTA an SM, a loading
-// warp that keeps three 64 KB tiles (128 keys and values) in flight by TMA,
-// one copy a page and 64-channel panel, and eight warps that take 16 tokens
-// of each tile: scores as K q^T with the tokens as the m side and the rows as
-// the n side of m16n8k16, so no product is spent on padding 3 or 7 rows to
-// 16; a running maximum a warp, merged once a unit.  In fp16 the weights'
-// reference lies 2^14 below the maximum: a warp may have 100,000 tokens whose
-// weights next to a first token's 1 would be below the smallest fp16 number,
-// and together count (304 sequences of 1,200,000: 36 times the bar of rounding).
+// The paged attention's host side, and the joining of partial results.
 #include <math.h>
 
 #include <algorithm>
@@ -20,290 +7,6 @@
 #include "splitk_attend.cuh"
 
 namespace palu {
-
-constexpr int kFewWarps = 8;
-constexpr int kFewThreads = 32 * (kFewWarps + 1);
-constexpr int kFewStages = 3;
-constexpr int kMergeStride = kHeadDim + 2;
-template <bool BF16>
-constexpr float kFewLift = BF16 ? 0.f : 14.f;  // log2: the largest weight; 2^14 < 65504
-
-// One tile, as the loading warp hands it to the others.
-struct TileMeta {
-  UnitMeta u;
-  int key0;         // place of the first key
-  int valid;        // keys of the tile that exist (1 .. 128)
-  int first, last;  // of the stretch
-};
-struct FewSmem {
-  uint64_t full[kFewStages], empty[kFewStages], join;
-  TileMeta meta[kFewStages];
-  PlanScratch plan;
-  int failed;  // a wait ran out: the remaining ones are not begun
-};
-// tiles (1024-byte aligned), the warps' merge area (8 rows at a time), the rest
-constexpr int kFewMergeBytes = kFewWarps * 8 * kMergeStride * 4;
-constexpr int kFewSmemBytes = 1024 + kFewStages * 2 * kTileBytes + kFewMergeBytes + (int)sizeof(FewSmem);
-static_assert(kFewSmemBytes <= 232448, "shared memory of paged_few_kernel");
-
-template <bool BF16>
-__device__ __forceinline__ void mma_16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  if (BF16)
-    mma_bf16(d, a0, a1, a2, a3, b0, b1);
-  else
-    mma_f16(d, a0, a1, a2, a3, b0, b1);
-}
-
-// NT: n8 tiles of rows (8 or 16 rows a unit).
-template <bool BF16, int NT>
-__global__ void __launch_bounds__(kFewThreads, 1)
-    paged_few_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* merge = reinterpret_cast<float*>(smem + kFewStages * 2 * kTileBytes);
-  FewSmem& sh = *reinterpret_cast<FewSmem*>(smem + kFewStages * 2 * kTileBytes + kFewMergeBytes);
-  constexpr int R = 8 * NT;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  grid_dep_launch();
-  if (tid == 0) {
-    for (int i = 0; i < kFewStages; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], kFewWarps);
-      sh.meta[i] = TileMeta{};
-    }
-    mbar_init(&sh.join, kFewWarps);
-    sh.failed = 0;
-    fence_mbar_init();
-  }
-  plan_start<R, kFewThreads>(p, &sh.plan, tid);  // all threads meet in it
-  if (sh.plan.w1 > sh.plan.w0) {
-    if (warp == kFewWarps) {
-      // ---- the loading warp
-      unsigned bad = 0;
-      int it = 0;
-      // room for the next tile: all lanes go on or stop together
-      auto room = [&] {
-        if (it >= kFewStages)
-          wait_or_fail(&sh.empty[it % kFewStages], ((it / kFewStages) - 1) & 1, &sh.failed, p.c.error);
-        return !__any_sync(0xffffffffu, *(volatile int*)&sh.failed);
-      };
-      plan_walk<R>(p, &sh.plan, [&](const UnitMeta& u) -> bool {
-        if (lane < u.rows) {  // the unit's queries, to L2 while the tiles before it are worked on
-          const uint16_t* q = row_query(p, u, lane);
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
-        }
-        for (int k = 0; k < u.n; ++k, ++it) {
-          const int st = it % kFewStages, key0 = u.key0 + k * kKeyTile, valid = min(kKeyTile, u.key_end - key0);
-          const int pages = (valid + p.c.page - 1) >> p.c.page_shift;
-          const int page = lane < pages ? page_of(p, u.seq, key0 + lane * p.c.page, &bad) : 0;
-          if (!room()) return false;
-          if (lane == 0) {
-            sh.meta[st] = TileMeta{u, key0, valid, k == 0, k == u.n - 1};
-            mbar_arrive_expect_tx(&sh.full[st], pages * p.c.page * kHeadDim * 4);
-          }
-          __syncwarp();
-          if (lane < pages) {
-            const uint32_t kt = smem_addr(smem + st * 2 * kTileBytes) + lane * p.c.page * 128;
-            tma_page(kt, &kmap, &sh.full[st], 0, u.kh, page);
-            tma_page(kt + kPanelBytes, &kmap, &sh.full[st], 64, u.kh, page);
-            tma_page(kt + kTileBytes, &vmap, &sh.full[st], 0, u.kh, page);
-            tma_page(kt + kTileBytes + kPanelBytes, &vmap, &sh.full[st], 64, u.kh, page);
-          }
-        }
-        return true;
-      });
-      const bool ended = room();
-      if (ended && lane == 0) {  // a tile of no keys ends the line
-        sh.meta[it % kFewStages].valid = 0;
-        mbar_arrive(&sh.full[it % kFewStages]);
-      }
-      if (bad) atomicOr(p.c.error, bad);
-      // no copy is in flight when the block ends, also where the others gave up (the stage that the end took had
-      // been emptied)
-      for (int k = max(it - kFewStages + (ended ? 1 : 0), 0); k < it; ++k)
-        if (!mbar_wait_bounded(&sh.full[k % kFewStages], (k / kFewStages) & 1)) break;
-    } else {
-      // ---- 16 tokens of each tile a warp
-      const int g = lane >> 2, c = lane & 3, mat = lane >> 3, rr = lane & 7, r0 = 16 * warp;
-      float m_run[NT][2], l_run[NT][2], acc[NT][8][4];
-      uint32_t qb[NT][8][2];
-      int lim[NT][2];
-      UnitMeta m = {};
-      uint32_t joins = 0;
-      // the eight warps meet (bounded, unlike a named barrier)
-      auto join = [&] {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.join);
-        wait_or_fail(&sh.join, joins & 1, &sh.failed, p.c.error);
-        ++joins;
-        __syncwarp();
-      };
-      for (int it = 0;; ++it) {
-        const int st = it % kFewStages;
-        wait_or_fail(&sh.full[st], (it / kFewStages) & 1, &sh.failed, p.c.error);
-        if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) break;
-        const TileMeta& tm = sh.meta[st];
-        const int valid = tm.valid, key0 = tm.key0, last = tm.last;
-        if (valid == 0) break;
-        if (tm.first) {
-          m = tm.u;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int rg = nt * 8 + g;
-            const uint16_t* qh = row_query(p, m, rg);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              qb[nt][ks][0] = rg < m.rows ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
-              qb[nt][ks][1] = rg < m.rows ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 8 + 2 * c) : 0u;
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = nt * 8 + 2 * c + e;
-              lim[nt][e] = r < m.rows ? unit_row_limit(p, sh.plan, m, r) : 0;
-              m_run[nt][e] = -INFINITY;
-              l_run[nt][e] = 0.f;
-            }
-#pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
-          }
-        }
-        const uint32_t kt = smem_addr(smem + st * 2 * kTileBytes), vt = kt + kTileBytes;
-        if (r0 < valid) {
-          if (valid < r0 + 16) {
-            // whatever lies behind the last key must not reach the products: 0 * NaN is NaN
-            const int z0 = valid - r0;
-            for (int i = lane; i < (16 - z0) * 16; i += 32) {
-              const uint32_t a = panel_addr(vt, r0 + z0 + (i >> 4), i & 15);
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          float sc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4(a0, a1, a2, a3, panel_addr(kt, r0 + rr + ((mat & 1) << 3), 2 * ks + (mat >> 1)));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16<BF16>(sc[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
-          }
-          const int t = key0 + r0 + g;
-          uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float* s = sc[nt];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[e] = t + 8 * (e >> 1) < lim[nt][e & 1] ? s[e] * p.scale_log2 : -INFINITY;
-            float pr[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float bm = fmaxf(s[e], s[e + 2]);
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
-              const float mn = fmaxf(m_run[nt][e], bm);
-              const float top = mn == -INFINITY ? 0.f : mn;  // nothing seen so far: every weight is 0
-              const float al = ex2f_(m_run[nt][e] - top), ref = top - kFewLift<BF16>;
-              m_run[nt][e] = mn;
-              pr[e] = ex2f_(s[e] - ref);
-              pr[e + 2] = ex2f_(s[e + 2] - ref);
-              l_run[nt][e] = l_run[nt][e] * al + (pr[e] + pr[e + 2]);
-#pragma unroll
-              for (int mt = 0; mt < 8; ++mt) {
-                acc[nt][mt][e] *= al;
-                acc[nt][mt][e + 2] *= al;
-              }
-            }
-            // The weights enter as a rounded value and its remainder: two
-            // products instead of one cost nothing here, and the output is
-            // then as exact as its own rounding lets it be.
-            const uint32_t h0 = pack2<BF16>(pr[0], pr[1]), h1 = pack2<BF16>(pr[2], pr[3]);
-            const float2 f0 = unpack2<BF16>(h0), f1 = unpack2<BF16>(h1);
-            ph[nt][0] = movmatrix_t(h0);
-            ph[nt][1] = movmatrix_t(h1);
-            pl[nt][0] = movmatrix_t(pack2<BF16>(pr[0] - f0.x, pr[1] - f0.y));
-            pl[nt][1] = movmatrix_t(pack2<BF16>(pr[2] - f1.x, pr[3] - f1.y));
-          }
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4_t(a0, a1, a2, a3, panel_addr(vt, r0 + rr + ((mat >> 1) << 3), 2 * mt + (mat & 1)));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_16<BF16>(acc[nt][mt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-              mma_16<BF16>(acc[nt][mt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[st]);
-        if (last) {
-          // join the warps' states, 8 rows at a time, and write the unit's result
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            join();
-            float* mw = merge + warp * 8 * kMergeStride;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float l = l_run[nt][e];
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-              if (g == 0) {
-                mw[(2 * c + e) * kMergeStride + kHeadDim] = m_run[nt][e];
-                mw[(2 * c + e) * kMergeStride + kHeadDim + 1] = l;
-              }
-            }
-#pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mw[(2 * c + (e & 1)) * kMergeStride + 16 * mt + g + 8 * (e >> 1)] = acc[nt][mt][e];
-            join();
-            // a warp a row, four channels a lane
-            const int r = nt * 8 + warp;
-            if (r < m.rows) {
-              const float* mr = merge + warp * kMergeStride;
-              float M = -INFINITY;
-#pragma unroll
-              for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, mr[w * 8 * kMergeStride + kHeadDim]);
-              const float ref = M == -INFINITY ? 0.f : M;
-              float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int w = 0; w < kFewWarps; ++w) {
-                const float* x = mr + w * 8 * kMergeStride;
-                const float f = ex2f_(x[kHeadDim] - ref);
-                L += x[kHeadDim + 1] * f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] += x[4 * lane + i] * f;
-              }
-              const long long at = row_index(p, m, r);
-              if (m.dest == kToOut) {
-                const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
-                uint2 v = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
-                *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) = v;
-              } else {
-                const long long rec = m.dest == kToRow ? (m.prefix ? 0 : (long long)p.N * p.Hq) + at
-                                                       : (long long)m.dest * p.part.R + r;
-                float2* ml = (m.dest == kToRow ? p.row_ml : p.part.ml) + rec;
-                float* ac = (m.dest == kToRow ? p.row_acc : p.part.acc) + rec * kHeadDim;
-                if (lane == 0) *ml = make_float2(M - kFewLift<BF16>, L);  // what the sums are relative to
-                *reinterpret_cast<float4*>(ac + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
-              }
-            }
-          }
-        }
-      }
-    }
-  }
-  // a launch before this one (the prefix on another kernel) has ended too when this one has
-  grid_dep_wait();
-}
 
 // ---- joining.  Eight warps a CTA: all on one row, every eighth part each, where
 // rows are few and may have up to a part an SM (a single long sequence); else
@@ -435,11 +138,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const
 }
 
 // With a prefix: every row has a part or more of it, and of its own keys.
-struct JoinRowsParams {
-  AttnParams a;
-  PartSet prefix, own;
-};
-
 // Ticks of a sequence's own units before row tile `rts`, added up by a whole warp: a long chunk has hundreds of row
 // tiles, and every row's join asks.
 template <int R>
@@ -454,29 +152,26 @@ __device__ __forceinline__ long long seq_ticks_warp(const SeqSpan& s, int rts, i
 }
 
 template <int R>
-__device__ __forceinline__ void own_place(const JoinRowsParams& p, const SeqSpan& s, int b, int kh, int lr, long long* f,
+__device__ __forceinline__ void own_place(const AttnParams& a, const SeqSpan& s, int b, int kh, int lr, long long* f,
                                           int* n, int* t) {
-  const AttnParams& a = p.a;
   const int rt = lr / R, rows = min(R, s.n * a.Gq - rt * R);
   *n = own_tiles(s, rt * R, rows, a.Gq, a.S0);
   *t = LineCost<R>::tile(rows);
-  *f = __ldcg(p.own.plan + 1 + b) + seq_ticks_warp<R>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R>(rows, *n) +
+  *f = __ldcg(a.part.plan + 1 + b) + seq_ticks_warp<R>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R>(rows, *n) +
        LineCost<R>::unit(rows);
 }
 template <int R>
-__device__ __forceinline__ void prefix_place(const JoinRowsParams& p, int kh, int lr, long long* f, int* n, int* t) {
-  const AttnParams& a = p.a;
+__device__ __forceinline__ void prefix_place(const AttnParams& a, int kh, int lr, long long* f, int* n, int* t) {
   const int all_rows = a.N * a.Gq, rts = (all_rows + R - 1) / R, rt = lr / R;
-  *n = prefix_tiles_of((int)__ldcg(p.prefix.plan + 1 + a.c.batch));
+  *n = prefix_tiles_of((int)__ldcg(a.prefix.plan + 1 + a.c.batch));
   const int rows = min(R, all_rows - rt * R);
   *t = LineCost<R>::tile(rows);
   *f = kh * prefix_ticks<R>(all_rows, rts, *n) + prefix_ticks<R>(all_rows, rt, *n) + LineCost<R>::unit(rows);
 }
 
 template <bool BF16, int STEP>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const JoinRowsParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const AttnParams a) {
   __shared__ JoinScratch sc;
-  const AttnParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row_first = (long long)blockIdx.x * STEP, rows_all = (long long)a.N * a.Hq;
   // Where a row's parts lie: CTAs first .. first + n - 1 of the launch that had its unit, or one record of the row.
@@ -520,20 +215,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     long long f;
     int n, t;
     const int lr = i * a.Gq + gi, gr = tok * a.Gq + gi;
-    if (p.own.R == 8) own_place<8>(p, s, b, kh, lr, &f, &n, &t);
-    else if (p.own.R == 16) own_place<16>(p, s, b, kh, lr, &f, &n, &t);
-    else own_place<kManyRows>(p, s, b, kh, lr, &f, &n, &t);
-    w.own = parts(p.own, f, n, t, lr % p.own.R);
-    if (p.prefix.R == 8) prefix_place<8>(p, kh, gr, &f, &n, &t);
-    else if (p.prefix.R == 16) prefix_place<16>(p, kh, gr, &f, &n, &t);
-    else prefix_place<kManyRows>(p, kh, gr, &f, &n, &t);
-    w.pre = parts(p.prefix, f, n, t, gr % p.prefix.R);
+    if (a.part.R == 8) own_place<8>(a, s, b, kh, lr, &f, &n, &t);
+    else if (a.part.R == 16) own_place<16>(a, s, b, kh, lr, &f, &n, &t);
+    else own_place<kManyRows>(a, s, b, kh, lr, &f, &n, &t);
+    w.own = parts(a.part, f, n, t, lr % a.part.R);
+    if (a.prefix.R == 8) prefix_place<8>(a, kh, gr, &f, &n, &t);
+    else if (a.prefix.R == 16) prefix_place<16>(a, kh, gr, &f, &n, &t);
+    else prefix_place<kManyRows>(a, kh, gr, &f, &n, &t);
+    w.pre = parts(a.prefix, f, n, t, gr % a.prefix.R);
   };
   Row w = find(row_first + (STEP > 1 ? warp : 0));
   grid_dep_wait();
   auto part = [&](int k, const float2*& ml, const float*& acc) {
     const bool pre = k < w.pre.n;
-    const PartSet& ps = pre ? p.prefix : p.own;
+    const PartSet& ps = pre ? a.prefix : a.part;
     const Parts& q = pre ? w.pre : w.own;
     const int c = pre ? k : k - w.pre.n;
     const bool whole = q.n == 1;
@@ -588,43 +283,14 @@ static palu_status page_map(CUtensorMap* map, const palu_paged_cache* c, const v
   return PALU_OK;
 }
 
-constexpr int kOneLaunchKeys = 256;  // own keys a sequence up to which one launch takes them with a prefix of many rows
-
 // Sizes that the host can know: which kernel takes the shared and which the
 // own keys, and the workspace's parts.
 struct AttnLayout {
-  int grid_prefix, grid_own;
   bool shared;       // the prefix is a part of its own
-  bool one_launch;   // both parts on the kernel for many rows
+  bool both;         // its rows are many and the own units' few: a line of each
   int R_prefix, R_own;
   size_t plan_p, begun_p, ml_p, acc_p, plan_o, begun_o, ml_o, acc_o, row_ml, row_acc, total;
 };
-
-// SMs for the prefix where it and the own keys are two launches: they run side
-// by side, each on SMs of its own, because a launch's beginning and end (about
-// 25,000 and 10,000 clocks: its code has to be fetched) leave the memory idle.
-// The own lengths are not known here: half of what the page table allows.
-static int split_grid(const palu_paged_cache* c, int64_t all_rows, int32_t shared_pages, int R_prefix, int grid) {
-  const int64_t t0 = prefix_tiles_of(shared_pages * c->page_size);
-  const int64_t own = ((int64_t)(c->table_width - shared_pages) * c->page_size / 2 + kKeyTile - 1) / kKeyTile;
-  const int64_t full = all_rows / R_prefix, rest = all_rows % R_prefix;
-  double a;  // clocks of one SM
-  if (R_prefix == kManyRows)
-    a = c->kv_heads * (full * (20000. + 3100. * t0) + (rest > kManyRows / 2 ? 20000. + 3100. * t0 : rest ? 12500. + 2900. * t0 : 0.));
-  else
-    a = c->kv_heads * (5700. + 2900. * t0);
-  const double b = (double)c->batch * c->kv_heads * (5700. + 2900. * own);
-  int best = grid / 2;
-  double least = INFINITY;
-  for (int g = 1; g < grid; ++g) {
-    const double t = std::max(25000. + a / g, 10000. + b / (grid - g));
-    if (t < least) {
-      least = t;
-      best = g;
-    }
-  }
-  return best;
-}
 
 // Whether reading the shared pages once pays.  It saves the tiles that the sequences would each read (a row tile each at
 // least) beyond those of the whole batch's row tiles; it costs a second launch and, for every row, a record of each part
@@ -666,12 +332,9 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   l->shared = share_pays(c, tokens, q_heads, max_new, shared_pages);
   l->R_prefix = all_rows <= 8 ? 8 : all_rows <= 16 ? 16 : kManyRows;
   const int R_rows = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
-  // Few own keys behind a prefix of many rows: one launch for both (256 rows behind 311,296 shared tokens and 1 own token
-  // a sequence: 65 us in two launches, 55 in one; 96 rows behind 8192 and 580 own: 46 and 50).
-  const bool few_keys = l->shared && l->R_prefix == kManyRows &&
-                        (int64_t)(c->table_width - shared_pages) * c->page_size <= kOneLaunchKeys;
-  l->R_own = few_keys ? kManyRows : R_rows;
-  l->one_launch = l->shared && l->R_own == kManyRows;  // then the prefix has many rows, too
+  // Otherwise one line: up to 16 rows in all go to the prefix's row tiles, and so do own units of more than 16.
+  l->both = l->shared && l->R_prefix == kManyRows && R_rows < kManyRows && device_sm_count() > 1;
+  l->R_own = l->shared && !l->both ? l->R_prefix : R_rows;
   const size_t slots = 2 * (size_t)device_sm_count();
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -685,10 +348,6 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     *ml = take(slots * R * sizeof(float2));
     *acc = take(slots * R * kHeadDim * sizeof(float));
   };
-  const bool two = l->shared && !l->one_launch;
-  const int grid = device_sm_count();
-  l->grid_prefix = two && grid > 1 ? split_grid(c, all_rows, shared_pages, l->R_prefix, grid) : grid;
-  l->grid_own = two && grid > 1 ? grid - l->grid_prefix : grid;
   // With shared pages the size is the same whether or not they are read once here: it also serves fewer tokens, and
   // any other number of them.
   const bool may_share = shared_pages > 0 && c->batch > 1;
@@ -697,7 +356,7 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   l->row_acc = take(records * kHeadDim * sizeof(float));
   const size_t parts = o;
   take_parts(l->R_own, &l->plan_o, &l->begun_o, &l->ml_o, &l->acc_o);
-  if (two) take_parts(l->R_prefix, &l->plan_p, &l->begun_p, &l->ml_p, &l->acc_p);
+  if (l->both) take_parts(l->R_prefix, &l->plan_p, &l->begun_p, &l->ml_p, &l->acc_p);
   l->total = o;
   if (may_share) {
     size_t unused;
@@ -707,23 +366,6 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
     l->total = o;
   }
   return PALU_OK;
-}
-
-template <bool BF16>
-static palu_status launch_few(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool dependent,
-                              cudaStream_t s) {
-  return p.part.R == 8 ? launch(paged_few_kernel<BF16, 1>, p.part.grid, kFewThreads, kFewSmemBytes, dependent, s,
-                                "paged_few_kernel launch", p, km, vm)
-                       : launch(paged_few_kernel<BF16, 2>, p.part.grid, kFewThreads, kFewSmemBytes, dependent, s,
-                                "paged_few_kernel launch", p, km, vm);
-}
-
-// The launch of one part, on the kernel for its number of rows.  `dependent`:
-// it may begin while the launch before it (the prefix) still runs.
-static palu_status launch_part(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, bool dependent,
-                               cudaStream_t s) {
-  if (p.part.R == kManyRows) return launch_many(p, km, vm, bf16, s);
-  return bf16 ? launch_few<true>(p, km, vm, dependent, s) : launch_few<false>(p, km, vm, dependent, s);
 }
 
 }  // namespace palu
@@ -778,46 +420,37 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   p.gq_mul = (65536 + p.Gq - 1) / p.Gq;
   p.S0 = l.shared ? shared_pages * cache->page_size : 0;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
-  const PartSet own = {reinterpret_cast<float2*>(ws + l.ml_o), reinterpret_cast<float*>(ws + l.acc_o),
-                       reinterpret_cast<long long*>(ws + l.plan_o), reinterpret_cast<UnitMeta*>(ws + l.begun_o), l.grid_own,
-                       l.R_own};
-  const PartSet prefix = l.one_launch ? own
-                                      : PartSet{reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
-                                                reinterpret_cast<long long*>(ws + l.plan_p), reinterpret_cast<UnitMeta*>(ws + l.begun_p),
-                                                l.grid_prefix, l.R_prefix};
+  p.part = {reinterpret_cast<float2*>(ws + l.ml_o), reinterpret_cast<float*>(ws + l.acc_o),
+            reinterpret_cast<long long*>(ws + l.plan_o), reinterpret_cast<UnitMeta*>(ws + l.begun_o), l.R_own};
+  p.prefix = p.part;
+  if (l.both)
+    p.prefix = {reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
+                reinterpret_cast<long long*>(ws + l.plan_p), reinterpret_cast<UnitMeta*>(ws + l.begun_p), l.R_prefix};
   const bool bf16 = cache->dtype == PALU_TYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (l.shared && !l.one_launch) {
-    p.part = prefix;
-    p.do_prefix = 1;
-    if ((st = launch_part(p, km, vm, bf16, false, s)) != PALU_OK) return st;
-  }
-  p.part = own;
-  p.do_prefix = l.one_launch;
-  p.do_own = 1;
-  if ((st = launch_part(p, km, vm, bf16, l.shared && !l.one_launch, s)) != PALU_OK) return st;
+  auto* const attend = l.both ? launch_both : l.R_own == kManyRows ? launch_many : launch_few;
+  if ((st = attend(p, km, vm, bf16, s)) != PALU_OK) return st;
   if (!l.shared) {
     if (l.R_own < kManyRows) {
-      const dim3 jgrid(l.grid_own, l.R_own);
+      const dim3 jgrid(device_sm_count(), l.R_own);
       return bf16 ? launch(paged_join_units_kernel<true, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p)
                   : launch(paged_join_units_kernel<false, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p);
     }
-    const dim3 jgrid(l.grid_own, l.R_own / kJoinWarps);
+    const dim3 jgrid(device_sm_count(), l.R_own / kJoinWarps);
     return bf16 ? launch(paged_join_units_kernel<true, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
                          "paged_join_units_kernel launch", p)
                 : launch(paged_join_units_kernel<false, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
                          "paged_join_units_kernel launch", p);
   }
-  const JoinRowsParams jp = {p, prefix, own};
   const long long rows = (long long)p.N * p.Hq;
   if (rows <= kJoinRows)
     return bf16 ? launch(paged_join_rows_kernel<true, 1>, dim3((unsigned)rows), 32 * kJoinWarps, 0, true, s,
-                         "paged_join_rows_kernel launch", jp)
+                         "paged_join_rows_kernel launch", p)
                 : launch(paged_join_rows_kernel<false, 1>, dim3((unsigned)rows), 32 * kJoinWarps, 0, true, s,
-                         "paged_join_rows_kernel launch", jp);
+                         "paged_join_rows_kernel launch", p);
   const dim3 jgrid((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
   return bf16 ? launch(paged_join_rows_kernel<true, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
-                       "paged_join_rows_kernel launch", jp)
+                       "paged_join_rows_kernel launch", p)
               : launch(paged_join_rows_kernel<false, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
-                       "paged_join_rows_kernel launch", jp);
+                       "paged_join_rows_kernel launch", p);
 }

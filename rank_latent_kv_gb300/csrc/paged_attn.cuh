@@ -16,7 +16,9 @@
 // Units in this order make one line, measured in ticks: a unit takes a fixed
 // number for its beginning and end, then some for each of its 128-key tiles
 // (LineCost).  CTA c of a persistent grid takes the tiles that begin in
-// [c W, (c+1) W), so every SM has the same work whatever the lengths.  A CTA's
+// [c W, (c+1) W), so every SM has the same work whatever the lengths.  Where
+// the prefix has many rows and the own units few, each has a line and CTAs of
+// its own, divided by the two lines' lengths (split_ctas).  A CTA's
 // stretch begins with at most one unit that an earlier CTA began and ends with
 // at most one that a later CTA ends: two partial results a CTA at most.  Units
 // inside are complete: they go straight to the output, or, where the prefix
@@ -50,13 +52,13 @@ struct UnitMeta {
   int parts;    // CTAs that hold a part of the unit, where this is its first one
 };
 
-// Partial results of one kernel launch: 2 slots a CTA, each R rows.
+// Partial results of a line: 2 slots a CTA, each R rows.
 struct PartSet {
   float2* ml;       // [2 grid][R] (m, l)
   float* acc;       // [2 grid][R][128]
   long long* plan;  // [0]: W; [1 + b]: where sequence b's own units begin; [1 + B]: the prefix units' last key
-  UnitMeta* begun;  // [grid]: the unit that CTA c begins and a later one ends (rows 0: none)
-  int grid, R;
+  UnitMeta* begun;  // [SMs]: the unit that CTA c begins and a later one ends (rows 0: none)
+  int R;
 };
 
 struct AttnParams {
@@ -67,23 +69,24 @@ struct AttnParams {
   uint16_t* out;
   float2* row_ml;   // [2][N Hq]: complete prefix units, complete own units (where there is a prefix)
   float* row_acc;   // [2][N Hq][128]
-  PartSet part;
+  PartSet part;     // the line, or the own units'
+  PartSet prefix;   // the prefix units', where they have one
   int N, max_new, Hq, Gq;
   int gq_mul;       // ceil(2^16 / Gq)
   int S0;           // shared tokens
-  int do_prefix, do_own;
   float scale_log2;
 };
 
-// What a unit costs, in ticks, in the kernel with row tiles of R: to begin and
-// end it, and a 128-key tile of it.
+// What a unit costs, in ticks of kClocks, in the kernel with row tiles of R: to
+// begin and end it, and a 128-key tile of it.
 template <int R>
 struct LineCost {
   static __device__ int unit(int rows) { return 2; }  // 5,700 clocks
   static __device__ int tile(int rows) { return 1; }  // 2,900
   static constexpr int kMaxTile = 1;
+  static constexpr float kClocks = 2900.f;
 };
-// In units of 200 clocks, measured: 1520 units of 256 rows and 4 tiles take
+// Measured: 1520 units of 256 rows and 4 tiles take
 // 34,000 clocks each, of 40 rows and 1 or 4 tiles 15,000 and 22,600; in long
 // units a tile of 256 rows takes 3,100 and one of up to 128 rows 2,900 (the
 // time of its 64 KB at memory speed).
@@ -93,6 +96,7 @@ struct LineCost<kManyRows> {
   static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 100 : 60; }
   static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 16 : 14; }
   static constexpr int kMaxTile = 16;
+  static constexpr float kClocks = 200.f;
 };
 
 // Row r (of a unit) -> token and query head, r < 256: g0 + r < 320 and Gq <= 64,
@@ -187,20 +191,41 @@ __host__ __device__ inline int prefix_tiles_of(int keys) { return (keys + kKeyTi
 // Where a finished unit goes.
 enum { kToOut = -1, kToRow = -2 };
 
-// The CTA's stretch of the line, found by THREADS of its threads, tid 0 ..
+// The CTA's stretch of its line, found by THREADS of its threads, tid 0 ..
 // THREADS - 1, which meet at named barrier 3.
 struct PlanScratch {
   long long warp_sum[16];
   long long w0, w1, W, base;
   int warp_longest[16];
+  int cta;         // where there are two lines: its number among the CTAs of its line,
+  int has_prefix;  // and whether that is the prefix units'
   int b;
-  int prefix_end;  // prefix units' keys: [0, prefix_end), where the launch has prefix units
+  int prefix_end;  // prefix units' keys: [0, prefix_end)
   int cut_prefix;  // a sequence does not see the whole prefix with all of its new tokens
 };
 
-template <int R, int THREADS>
+// CTAs of `grid` for the prefix where it has many rows and the own units few: a
+// line of each, of `a` clocks of prefix and `b` of own units, so that both end
+// together.  The device divides, because only it knows the lengths: a table is
+// as wide as the longest sequence that a program admits (32 sequences of 777
+// own tokens behind 8192, 24 heads of 8: 39 us in tables for 777 and for 131,072
+// tokens; with half of the table's width as a guess 42 and 786, and 120 without
+// sharing).  A prefix tile takes longer where own units keep the memory busy:
+// measured over all divisions of 13 calls, from a / b = 1 / 50 to 2, its clocks
+// count 0.8 + 2.3 (b / (a + b))^2 times (within 4 % of the best division, 1 % on
+// average; plain shares by a and b up to 54 % off).  Every CTA finds the same
+// number; each kind has one at least.
+__device__ __forceinline__ int split_ctas(float a, float b, int grid) {
+  const float x = __fdividef(b, a + b), k = (0.8f + 2.3f * x * x) * a;
+  return a > 0.f ? min(max((int)(grid * __fdividef(k, k + b) + 0.5f), 1), grid - 1) : 1;
+}
+
+// R: row tiles of the own units; RP: of the prefix units.  RP != R: a line of
+// each.
+template <int R, int RP, int THREADS>
 __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc, int tid) {
   constexpr int nthr = THREADS, nwarp = THREADS / 32;
+  constexpr bool SPLIT = R != RP;
   const int warp = tid >> 5, lane = tid & 31;
   auto meet = [] { asm volatile("bar.sync 3, %0;" ::"n"(THREADS) : "memory"); };
   const int B = p.c.batch, Hkv = p.c.kv_heads;
@@ -215,59 +240,68 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
     sc->cut_prefix = 0;
   }
   meet();
-  if (p.do_own || p.do_prefix)
-    for (int b = b0; b < b1; ++b) {
-      const SeqSpan s = seq_span(p, b, &bad);
-      if (s.n && row_limit(s, 0) < p.S0) sc->cut_prefix = 1;
-      if (s.n) longest = max(longest, s.len);
-      if (!p.do_own) continue;
-      mine += seq_ticks<R>(s, p.Gq, p.S0, Hkv);
-      // without a prefix nothing joins parts of every row: rows that see nothing, or that are before the first
-      // sequence, are zeroed here, all CTAs sharing them
-      if (p.S0 == 0) {
-        const int o0 = __ldg(p.offsets + b), o1 = min(__ldg(p.offsets + b + 1), p.N);
-        const int z0 = b ? max(o0, 0) : 0, z1 = s.n ? min(o1, o0 + max(s.n - s.len, 0)) : o1;
-        for (long long i = (long long)z0 * p.Hq * (kHeadDim / 8) + blockIdx.x; i < (long long)z1 * p.Hq * (kHeadDim / 8);
-             i += gridDim.x)
-          reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
+  for (int b = b0; b < b1; ++b) {
+    const SeqSpan s = seq_span(p, b, &bad);
+    if (s.n && row_limit(s, 0) < p.S0) sc->cut_prefix = 1;
+    if (s.n) longest = max(longest, s.len);
+    mine += seq_ticks<R>(s, p.Gq, p.S0, Hkv);
+    // without a prefix nothing joins parts of every row: rows that see nothing, or that are before the first
+    // sequence, are zeroed here, all CTAs sharing them
+    if (p.S0 == 0) {
+      const int o0 = __ldg(p.offsets + b), o1 = min(__ldg(p.offsets + b + 1), p.N);
+      const int z0 = b ? max(o0, 0) : 0, z1 = s.n ? min(o1, o0 + max(s.n - s.len, 0)) : o1;
+      for (long long i = (long long)z0 * p.Hq * (kHeadDim / 8) + blockIdx.x; i < (long long)z1 * p.Hq * (kHeadDim / 8);
+           i += gridDim.x)
+        reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
+  }
   long long incl = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, x);
     if (lane >= x) incl += y;
   }
-  if (p.do_prefix) sc->warp_longest[warp] = __reduce_max_sync(0xffffffffu, longest);
+  if (p.S0) sc->warp_longest[warp] = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 31) sc->warp_sum[warp] = incl;
   meet();
-  long long before = 0, total = 0;
+  long long before = 0, own = 0, prefix = 0;
 #pragma unroll
   for (int w = 0; w < nwarp; ++w) {
     if (w < warp) before += sc->warp_sum[w];
-    total += sc->warp_sum[w];
+    own += sc->warp_sum[w];
   }
-  long long prefix = 0;
-  if (p.do_prefix) {
+  before += incl - mine;
+  if (p.S0) {
 #pragma unroll
     for (int w = 0; w < nwarp; ++w) longest = max(longest, sc->warp_longest[w]);
     longest = min(longest, p.S0);
-    prefix = Hkv * prefix_ticks<R>(all_rows, (all_rows + R - 1) / R, prefix_tiles_of(longest));
-    before += prefix;
-    total += prefix;
+    prefix = Hkv * prefix_ticks<RP>(all_rows, (all_rows + RP - 1) / RP, prefix_tiles_of(longest));
   }
-  before += incl - mine;
+  int cta = blockIdx.x, grid = gridDim.x;
+  bool has_prefix = p.S0 > 0, has_own = true;
+  if (SPLIT) {
+    const int g = split_ctas((float)prefix * LineCost<RP>::kClocks, (float)own * LineCost<R>::kClocks, grid);
+    has_prefix = cta < g;
+    has_own = !has_prefix;
+    grid = has_prefix ? g : grid - g;
+    cta -= has_prefix ? 0 : g;
+  }
+  const PartSet& part = SPLIT && has_prefix ? p.prefix : p.part;
+  if (!has_prefix) prefix = 0;
+  before += prefix;
+  const long long total = prefix + (has_own ? own : 0);
   // a stretch is never shorter than a tile, so that every CTA between a unit's first and last holds a part of it
-  const long long W = max((total + gridDim.x - 1) / gridDim.x, (long long)LineCost<R>::kMaxTile);
-  const long long w0 = (long long)blockIdx.x * W, w1 = min(w0 + W, total);
-  if (p.do_own) {
+  const long long tile = SPLIT && has_prefix ? LineCost<RP>::kMaxTile : LineCost<R>::kMaxTile;
+  const long long W = max((total + grid - 1) / grid, tile);
+  const long long w0 = cta * W, w1 = min(w0 + W, total);
+  if (has_own) {
     // the thread whose sequences hold the CTA's first own tick walks them; CTA 0 writes the plan down
     const long long at = max(w0, prefix);
     const bool here = at < w1 && at >= before && at < before + mine;
-    if (here || blockIdx.x == 0) {
+    if (here || cta == 0) {
       long long base = before;
       for (int b = b0; b < b1; ++b) {
-        if (blockIdx.x == 0) p.part.plan[1 + b] = base;
+        if (cta == 0) part.plan[1 + b] = base;
         const long long t = per == 1 ? mine : seq_ticks<R>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
         if (here && at >= base && at < base + t) {
           sc->b = b;
@@ -276,29 +310,35 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
         base += t;
       }
     }
-    if (blockIdx.x == 0 && bad) atomicOr(p.c.error, bad);
+    if (cta == 0 && bad) atomicOr(p.c.error, bad);
   }
   if (tid == 0) {
     sc->w0 = w0;
     sc->w1 = w1;
     sc->W = W;
-    sc->prefix_end = longest;
-    if (blockIdx.x == 0) {
-      p.part.plan[0] = W;
-      if (p.do_prefix) p.part.plan[1 + B] = longest;
+    if (SPLIT) {
+      sc->cta = cta;
+      sc->has_prefix = has_prefix;
     }
-    p.part.begun[blockIdx.x].rows = 0;
+    if (p.S0) sc->prefix_end = longest;
+    if (cta == 0) {
+      part.plan[0] = W;
+      if (has_prefix) part.plan[1 + B] = longest;
+    }
+    part.begun[cta].rows = 0;
   }
   meet();
 }
 
 // Calls unit(meta) for each unit of which the CTA's stretch of the line has
 // tiles, in order, until it returns false: run by one warp, all its lanes.
-template <int R, class F>
-__device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch* sc, F&& unit) {
+// SPLIT: the line is one of two, of the prefix or of the own units.
+template <int R, bool SPLIT, class F>
+__device__ __forceinline__ void plan_walk(const AttnParams& p, const PartSet& part, const PlanScratch* sc, F&& unit) {
   const int Hkv = p.c.kv_heads;
   const long long w0 = sc->w0, w1 = sc->w1;
-  const int cta = blockIdx.x;
+  const int cta = SPLIT ? sc->cta : blockIdx.x;
+  const bool has_prefix = SPLIT ? sc->has_prefix : p.S0 > 0;
   UnitMeta m = {};
   // the tiles of a unit [u0, u0 + ticks) that begin in [w0, w1)
   auto run_unit = [&](long long u0, int n, int key_base, int key_end) -> bool {
@@ -318,12 +358,12 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
     m.n = k1 - k0;
     if (m.dest == 2 * cta + 1) {
       m.parts = div_small(f + (long long)(n - 1) * t, sc->W) - cta + 1;
-      if ((threadIdx.x & 31) == 0) p.part.begun[cta] = m;
+      if ((threadIdx.x & 31) == 0) part.begun[cta] = m;
     }
     return unit(m);
   };
   long long base = 0;
-  if (p.do_prefix) {
+  if (has_prefix) {
     const int all_rows = p.N * p.Gq, rts = (all_rows + R - 1) / R, tiles = prefix_tiles_of(sc->prefix_end);
     const long long head = prefix_ticks<R>(all_rows, rts, tiles), full = unit_ticks<R>(R, tiles);
     m.pos = m.seq = 0;
@@ -342,7 +382,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PlanScratch
         }
     }
   }
-  if (!p.do_own || sc->b < 0) return;
+  if ((SPLIT && has_prefix) || sc->b < 0) return;
   base = sc->base;
   unsigned bad = 0;
   for (int b = sc->b; b < p.c.batch; ++b) {
@@ -445,7 +485,10 @@ palu_status launch(K kernel, dim3 grid, int threads, int smem, bool dependent, c
   return cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), what);
 }
 
-// The kernel for many rows (paged_many.cu).
+// The kernels: few rows (paged_few.cu), many rows (paged_many.cu), and a prefix of many rows with own units of few
+// (paged_both.cu).
+palu_status launch_few(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 palu_status launch_many(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
+palu_status launch_both(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 
 }  // namespace palu
