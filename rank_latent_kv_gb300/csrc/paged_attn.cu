@@ -293,10 +293,10 @@ struct AttnLayout {
 };
 
 // Whether reading the shared pages once pays.  It saves the tiles that the sequences would each read (a row tile each at
-// least) beyond those of the whole batch's row tiles; it costs a second launch and, for every row, a record of each part
-// that is written, read and joined.  28 heads of 4 KV heads, 512 own keys, bf16, read once and by each sequence: 16
-// sequences of 1 token behind 1024 keys 19.1 and 14.3 us, behind 4096 23.3 and 33.0; 256 sequences of 5 behind 256 129 and
-// 95 us, behind 4096 185 and 442; 16 of 1024 new tokens behind 8192 1901 and 1506 us.  In clocks, summed over the SMs:
+// least) beyond those of the whole batch's row tiles; it costs a longer beginning and, for every row, a record of each
+// part that is written, read and joined.  28 heads of 4 KV heads, 512 own keys, bf16, read once and by each sequence: 16
+// sequences of 1 token behind 1024 keys 16.5 and 14.5 us, behind 4096 20.1 and 23.9; 256 sequences of 5 behind 256 128 and
+// 96 us, behind 4096 182 and 353; 16 of 1024 new tokens behind 8192 1972 and 1456.  In clocks, summed over the SMs:
 constexpr double kShareTile = 2900., kShareRow = 350., kShareLaunch = 13300.;
 
 // The most new tokens a call for which it can (the tiles saved are at most one a sequence, KV head and tile of the table).
