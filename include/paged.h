@@ -161,13 +161,15 @@ palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_
  * token that a query does not see yet has the weight 0, and 0 * NaN is NaN).
  * Weights are rounded to the cache's type once, where a KV head has more than
  * 16 rows (in fp16 those under 2^-20 of a row's largest lose bits, and those
- * under 2^-31 count only in the sum); sums, maxima and accumulators are fp32.  Two kernel
- * launches on `stream`, chosen by the sizes given here, not by the lengths; how
- * the SMs are divided follows from the lengths, not from the table's width.
- * Repeating a call repeats its result bit for bit.  A sequence with more than
- * max_new rows or offsets out of order sets PALU_DEVERR_SPAN and its rows are
- * zeros, as are rows before offsets[0] where that is not 0; a length past the table sets PALU_DEVERR_CAPACITY and is cut to it;
- * a page id outside the pool sets PALU_DEVERR_PAGE and page 0 is read for it. */
+ * under 2^-31 count only in the sum); sums, maxima and accumulators are fp32.
+ * Two kernel launches on `stream`, chosen by the sizes given here, not by the
+ * lengths; how the SMs are divided follows from the lengths, not from the
+ * table's width.  Repeating a call repeats its result bit for bit.
+ * A sequence with more than max_new rows or offsets out of order sets
+ * PALU_DEVERR_SPAN and its rows are zeros, as are rows before offsets[0] where
+ * that is not 0; a length past the table sets PALU_DEVERR_CAPACITY and is cut
+ * to it; a page id outside the pool sets PALU_DEVERR_PAGE and page 0 is read
+ * for it. */
 palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t tokens, const int32_t* offsets, int32_t max_new,
                             int32_t q_heads, const void* q, const int64_t q_strides[2], int32_t shared_pages,
                             float softmax_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);

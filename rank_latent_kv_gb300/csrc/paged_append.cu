@@ -8,8 +8,9 @@
 // output is head-major.  A lane holds both members of four pairs (two 8-byte
 // pieces of a row: with 16 contiguous bytes a lane the half-split pairs came by
 // shuffle, and instructions, not memory, were the bound: 67 us for 16,384
-// tokens of 24 + 8 heads instead of 55, 5.0 TB/s), all four rows in flight at once; the token's angles
-// and the norm's weights stay in registers for the run.  The sum of squares is
+// tokens of 24 + 8 heads instead of 54, 5.1 TB/s, on the device; 56 to 57 as a
+// call), all four rows in flight at once; the token's angles and the norm's
+// weights stay in registers for the run.  The sum of squares is
 // a 4-step butterfly over the 16 lanes.  fp32 throughout, one rounding at the
 // store.
 #include <math.h>

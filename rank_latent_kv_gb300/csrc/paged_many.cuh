@@ -20,8 +20,8 @@
 //   one 128 x 128 x 16; measured 3,950 clocks a tile pair.)
 //   A tile pair takes about 3,100 clocks: the products alone 2,048, in which
 //   they read 192 KB of shared memory and the copies write 64, at 128 bytes a
-//   clock as long again.  1,024 tokens of 8 heads over 53,248 keys: 163 us,
-//   1361 TFLOP/s.
+//   clock as long again.  1,024 tokens of 8 heads over 53,248 keys: 160 us,
+//   1383 TFLOP/s.
 //   Shared memory: Q0 Q1 (32 KB each), a ring of five 32 KB tiles that holds
 //   K and V of successive key tiles in turn.
 //   Warps 0-3, 4-7: the halves' softmax; warp 8: loads; warps 9, 10: the
