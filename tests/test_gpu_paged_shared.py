@@ -334,3 +334,35 @@ def test_steps_behind_a_shared_prompt(P, dt, Hq, Hk, page, shared):
         rt, rk = verify_reference(t, p, tokens, au, su, drafts.numpy())
         assert (toks.cpu().numpy() == rt).all() and (kept.cpu().numpy() == rk).all()
         assert c.lengths.tolist() == [l - int(a) + int(b) for l, a, b in zip(lengths, drafts, rk)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_no_new_tokens_behind_a_shared_prefix(P, kind):
+    """A padded batch without any new token: nothing is read that matters, nothing is written."""
+    page, new, Hq, Hk, shared, own = KINDS[kind]
+    pools, dev, c = make_cache(P, torch.bfloat16, kind_lengths(kind, 1), page, Hk, seed=8, shared=shared, width=shared + own)
+    n = sum(new)
+    q = torch.full((n, Hq, D), NAN, dtype=torch.bfloat16, device=DEV)
+    out = torch.full((n, Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    c.attend(q, torch.zeros(len(new) + 1, dtype=torch.int32, device=DEV), max(new), shared_pages=shared, out=out)
+    assert c.sync() == 0 and (out == 7).all()
+
+
+@pytest.mark.parametrize("B,new,Hq,Hk,shared", [(1500, 1, 8, 2, 16), (900, 3, 6, 2, 40), (700, 5, 16, 2, 64)])
+def test_more_sequences_than_a_cta_has_threads(P, B, new, Hq, Hk, shared):
+    """Many short sequences behind a prefix: some without rows, some that end inside it, most with few own tokens."""
+    page, d = 16, torch.float16
+    g = torch.Generator().manual_seed(B)
+    counts = torch.randint(0, new + 1, (B,), generator=g).tolist()
+    counts[5], counts[B - 1] = new, new
+    lengths = [page * shared + int(torch.randint(m, 80, (1,), generator=g)) for m in counts]
+    for b in range(0, B, 50):
+        lengths[b] = int(torch.randint(0, page * shared + 1, (1,), generator=g))
+    pools, dev, c = make_cache(P, d, lengths, page, Hk, seed=10, shared=shared, width=shared + 5)
+    table0 = c.page_table.clone()
+    hide_shared(c, dev, shared)
+    n = sum(counts)
+    q = torch.randn(n, Hq, D, generator=g).to(d)
+    out = c.attend(q.to(DEV), offsets_of(counts), new, shared_pages=shared)
+    assert c.sync() == 0
+    attend_close(out, *ref_by_sequence(q, pools, table0, lengths, counts, page), d)
