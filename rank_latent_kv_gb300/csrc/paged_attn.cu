@@ -3,6 +3,7 @@
 
 #include <algorithm>
 
+#include "paged4.cuh"
 #include "paged_attn.cuh"
 #include "splitk_attend.cuh"
 
@@ -140,10 +141,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_units_kernel(const
 // With a prefix: every row has a part or more of it, and of its own keys.
 // Ticks of a sequence's own units before row tile `rts`, added up by a whole warp: a long chunk has hundreds of row
 // tiles, and every row's join asks.
-template <int R>
+template <int R, bool FOUR>
 __device__ __forceinline__ long long seq_ticks_warp(const SeqSpan& s, int rts, int Gq, int S0, int kv_heads) {
   long long t = 0;
-  for (int rt = threadIdx.x & 31; rt < rts; rt += 32) t += unit_ticks<R>(R, own_tiles(s, rt * R, R, Gq, S0));
+  for (int rt = threadIdx.x & 31; rt < rts; rt += 32) t += unit_ticks<R, FOUR>(R, own_tiles(s, rt * R, R, Gq, S0));
   if (rts) {
 #pragma unroll
     for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
@@ -151,25 +152,25 @@ __device__ __forceinline__ long long seq_ticks_warp(const SeqSpan& s, int rts, i
   return t * kv_heads;
 }
 
-template <int R>
+template <int R, bool FOUR>
 __device__ __forceinline__ void own_place(const AttnParams& a, const SeqSpan& s, int b, int kh, int lr, long long* f,
                                           int* n, int* t) {
   const int rt = lr / R, rows = min(R, s.n * a.Gq - rt * R);
   *n = own_tiles(s, rt * R, rows, a.Gq, a.S0);
-  *t = LineCost<R>::tile(rows);
-  *f = __ldcg(a.part.plan + 1 + b) + seq_ticks_warp<R>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R>(rows, *n) +
-       LineCost<R>::unit(rows);
+  *t = LineCost<R, FOUR>::tile(rows);
+  *f = __ldcg(a.part.plan + 1 + b) + seq_ticks_warp<R, FOUR>(s, rt, a.Gq, a.S0, a.c.kv_heads) + kh * unit_ticks<R, FOUR>(rows, *n) +
+       LineCost<R, FOUR>::unit(rows);
 }
-template <int R>
+template <int R, bool FOUR>
 __device__ __forceinline__ void prefix_place(const AttnParams& a, int kh, int lr, long long* f, int* n, int* t) {
   const int all_rows = a.N * a.Gq, rts = (all_rows + R - 1) / R, rt = lr / R;
   *n = prefix_tiles_of((int)__ldcg(a.prefix.plan + 1 + a.c.batch));
   const int rows = min(R, all_rows - rt * R);
-  *t = LineCost<R>::tile(rows);
-  *f = kh * prefix_ticks<R>(all_rows, rts, *n) + prefix_ticks<R>(all_rows, rt, *n) + LineCost<R>::unit(rows);
+  *t = LineCost<R, FOUR>::tile(rows);
+  *f = kh * prefix_ticks<R, FOUR>(all_rows, rts, *n) + prefix_ticks<R, FOUR>(all_rows, rt, *n) + LineCost<R, FOUR>::unit(rows);
 }
 
-template <bool BF16, int STEP>
+template <bool BF16, int STEP, bool FOUR>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const AttnParams a) {
   __shared__ JoinScratch sc;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -215,13 +216,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_rows_kernel(const 
     long long f;
     int n, t;
     const int lr = i * a.Gq + gi, gr = tok * a.Gq + gi;
-    if (a.part.R == 8) own_place<8>(a, s, b, kh, lr, &f, &n, &t);
-    else if (a.part.R == 16) own_place<16>(a, s, b, kh, lr, &f, &n, &t);
-    else own_place<kManyRows>(a, s, b, kh, lr, &f, &n, &t);
+    if (a.part.R == 8) own_place<8, FOUR>(a, s, b, kh, lr, &f, &n, &t);
+    else if (a.part.R == 16) own_place<16, FOUR>(a, s, b, kh, lr, &f, &n, &t);
+    else own_place<kManyRows, FOUR>(a, s, b, kh, lr, &f, &n, &t);
     w.own = parts(a.part, f, n, t, lr % a.part.R);
-    if (a.prefix.R == 8) prefix_place<8>(a, kh, gr, &f, &n, &t);
-    else if (a.prefix.R == 16) prefix_place<16>(a, kh, gr, &f, &n, &t);
-    else prefix_place<kManyRows>(a, kh, gr, &f, &n, &t);
+    if (a.prefix.R == 8) prefix_place<8, FOUR>(a, kh, gr, &f, &n, &t);
+    else if (a.prefix.R == 16) prefix_place<16, FOUR>(a, kh, gr, &f, &n, &t);
+    else prefix_place<kManyRows, FOUR>(a, kh, gr, &f, &n, &t);
     w.pre = parts(a.prefix, f, n, t, gr % a.prefix.R);
   };
   Row w = find(row_first + (STEP > 1 ? warp : 0));
@@ -300,13 +301,13 @@ struct AttnLayout {
 constexpr double kShareTile = 2900., kShareRow = 350., kShareLaunch = 13300.;
 
 // The most new tokens a call for which it can (the tiles saved are at most one a sequence, KV head and tile of the table).
-static int64_t most_shared_tokens(const palu_paged_cache* c, int32_t q_heads) {
+static int64_t most_shared_tokens(const palu_paged_cache* c, bool four, int32_t q_heads) {
   const double tiles = prefix_tiles_of(c->table_width * c->page_size);
   const double n = (kShareTile * c->kv_heads * tiles * c->batch - kShareLaunch * device_sm_count()) / (kShareRow * q_heads);
   return std::max<int64_t>(1, (int64_t)n);
 }
-static bool share_pays(const palu_paged_cache* c, int64_t tokens, int32_t q_heads, int32_t max_new, int32_t shared_pages) {
-  if (shared_pages == 0 || c->batch == 1 || tokens > most_shared_tokens(c, q_heads)) return false;
+static bool share_pays(const palu_paged_cache* c, bool four, int64_t tokens, int32_t q_heads, int32_t max_new, int32_t shared_pages) {
+  if (shared_pages == 0 || c->batch == 1 || tokens > most_shared_tokens(c, four, q_heads)) return false;
   const int Gq = q_heads / c->kv_heads;
   auto row_tiles = [&](double new_tokens) { return ceil(new_tokens * Gq / kManyRows); };
   // the counts are the device's: as many sequences as can be with the most new tokens, one token for the others
@@ -317,7 +318,7 @@ static bool share_pays(const palu_paged_cache* c, int64_t tokens, int32_t q_head
          kShareRow * (double)tokens * q_heads + kShareLaunch * device_sm_count();
 }
 
-static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_t q_heads, int32_t max_new,
+static palu_status attn_layout(const palu_paged_cache* c, bool four, int64_t tokens, int32_t q_heads, int32_t max_new,
                                int32_t shared_pages, AttnLayout* l) {
   palu_status st = paged_check(c);
   if (st != PALU_OK) return st;
@@ -329,9 +330,10 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   if (shared_pages < 0 || shared_pages > c->table_width)
     return fail(PALU_ERR_INVALID_ARG, "shared_pages must be in [0, table_width]");
   const int64_t own_rows = std::min<int64_t>(max_new, tokens) * Gq, all_rows = tokens * Gq;
-  l->shared = share_pays(c, tokens, q_heads, max_new, shared_pages);
-  l->R_prefix = all_rows <= 8 ? 8 : all_rows <= 16 ? 16 : kManyRows;
-  const int R_rows = own_rows <= 8 ? 8 : own_rows <= 16 ? 16 : kManyRows;
+  l->shared = share_pays(c, four, tokens, q_heads, max_new, shared_pages);
+  auto row_tile = [&](int64_t rows) { return rows <= 8 ? 8 : rows <= 16 || four ? 16 : kManyRows; };
+  l->R_prefix = row_tile(all_rows);
+  const int R_rows = row_tile(own_rows);
   // Otherwise one line: up to 16 rows in all go to the prefix's row tiles, and so do own units of more than 16.
   l->both = l->shared && l->R_prefix == kManyRows && R_rows < kManyRows && device_sm_count() > 1;
   l->R_own = l->shared && !l->both ? l->R_prefix : R_rows;
@@ -351,7 +353,7 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
   // With shared pages the size is the same whether or not they are read once here: it also serves fewer tokens, and
   // any other number of them.
   const bool may_share = shared_pages > 0 && c->batch > 1;
-  const size_t records = may_share ? 2 * (size_t)std::min(tokens, most_shared_tokens(c, q_heads)) * q_heads : 0;
+  const size_t records = may_share ? 2 * (size_t)std::min(tokens, most_shared_tokens(c, four, q_heads)) * q_heads : 0;
   l->row_ml = take(records * sizeof(float2));
   l->row_acc = take(records * kHeadDim * sizeof(float));
   const size_t parts = o;
@@ -372,22 +374,16 @@ static palu_status attn_layout(const palu_paged_cache* c, int64_t tokens, int32_
 
 using namespace palu;
 
-extern "C" palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_t tokens, int32_t q_heads,
-                                                      int32_t max_new, int32_t shared_pages, size_t* bytes) {
-  AttnLayout l;
-  palu_status st = attn_layout(cache, tokens, q_heads, max_new, shared_pages, &l);
-  if (st != PALU_OK) return st;
-  if (!bytes) return fail(PALU_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = l.total;
-  return PALU_OK;
-}
+namespace palu {
 
-extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t tokens, const int32_t* offsets,
-                                       int32_t max_new, int32_t q_heads, const void* q, const int64_t q_strides[2],
-                                       int32_t shared_pages, float softmax_scale, void* out, void* workspace,
-                                       size_t workspace_bytes, void* stream) {
-  AttnLayout l;
-  palu_status st = attn_layout(cache, tokens, q_heads, max_new, shared_pages, &l);
+// The call's arguments checked, and the kernels' parameters but for the pages.
+static palu_status attn_params(const palu_paged_cache* cache, bool four, int64_t tokens, const int32_t* offsets, int32_t max_new,
+                               int32_t q_heads, const void* q, const int64_t* q_strides, int32_t shared_pages,
+                               float softmax_scale, void* out, void* workspace, size_t workspace_bytes, AttnLayout* layout,
+                               AttnParams* params) {
+  AttnLayout& l = *layout;
+  AttnParams& p = *params;
+  palu_status st = attn_layout(cache, four, tokens, q_heads, max_new, shared_pages, &l);
   if (st != PALU_OK) return st;
   if (!q || !q_strides || !offsets || !out || !workspace) return fail(PALU_ERR_INVALID_ARG, "NULL pointer");
   if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15 || (uintptr_t)offsets & 3)
@@ -400,13 +396,8 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   if (!(softmax_scale >= 0.f) || isinf(softmax_scale))
     return fail(PALU_ERR_INVALID_ARG, "softmax_scale must be finite and not negative");
   if (workspace_bytes < l.total) return fail(PALU_ERR_INVALID_ARG, "workspace too small");
-  CUtensorMap km, vm;
-  if ((st = page_map(&km, cache, cache->k_pages, cache->k_strides)) != PALU_OK ||
-      (st = page_map(&vm, cache, cache->v_pages, cache->v_strides)) != PALU_OK)
-    return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttnParams p = {};
-  p.c = paged_view(cache);
+  p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.qs0 = q_strides[0], p.qs1 = q_strides[1];
   p.offsets = offsets;
@@ -426,31 +417,100 @@ extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t to
   if (l.both)
     p.prefix = {reinterpret_cast<float2*>(ws + l.ml_p), reinterpret_cast<float*>(ws + l.acc_p),
                 reinterpret_cast<long long*>(ws + l.plan_p), reinterpret_cast<UnitMeta*>(ws + l.begun_p), l.R_prefix};
+  return PALU_OK;
+}
+
+// The joins behind an attention kernel.
+template <bool BF16, bool FOUR>
+static palu_status launch_joins(const AttnLayout& l, const AttnParams& p, cudaStream_t s) {
+  if (!l.shared) {
+    if (l.R_own < kManyRows)
+      return launch(paged_join_units_kernel<BF16, 1>, dim3(device_sm_count(), l.R_own), 32 * kJoinWarps, 0, true, s,
+                    "paged_join_units_kernel launch", p);
+    return launch(paged_join_units_kernel<BF16, kJoinWarps>, dim3(device_sm_count(), l.R_own / kJoinWarps), 32 * kJoinWarps, 0,
+                  true, s, "paged_join_units_kernel launch", p);
+  }
+  const long long rows = (long long)p.N * p.Hq;
+  if (rows <= kJoinRows)
+    return launch(paged_join_rows_kernel<BF16, 1, FOUR>, dim3((unsigned)rows), 32 * kJoinWarps, 0, true, s,
+                  "paged_join_rows_kernel launch", p);
+  return launch(paged_join_rows_kernel<BF16, kJoinWarps, FOUR>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
+                32 * kJoinWarps, 0, true, s, "paged_join_rows_kernel launch", p);
+}
+
+// A 4-bit cache's sizes, for the plan that both kinds of pages share.
+static palu_status sizes_of(const palu_paged4_cache* c, palu_paged_cache* p) {
+  palu_status st = paged4_check(c);
+  if (st != PALU_OK) return st;
+  *p = {};
+  p->magic = kPagedMagic;
+  p->dtype = c->dtype;
+  p->kv_heads = c->kv_heads;
+  p->page_size = c->page_size;
+  p->batch = c->batch;
+  p->table_width = c->table_width;
+  p->n_pages = c->n_pages;
+  return PALU_OK;
+}
+
+}  // namespace palu
+
+extern "C" palu_status palu_paged_attn_workspace_size(const palu_paged_cache* cache, int64_t tokens, int32_t q_heads,
+                                                      int32_t max_new, int32_t shared_pages, size_t* bytes) {
+  AttnLayout l;
+  palu_status st = attn_layout(cache, false, tokens, q_heads, max_new, shared_pages, &l);
+  if (st != PALU_OK) return st;
+  if (!bytes) return fail(PALU_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = l.total;
+  return PALU_OK;
+}
+
+extern "C" palu_status palu_paged_attn(const palu_paged_cache* cache, int64_t tokens, const int32_t* offsets,
+                                       int32_t max_new, int32_t q_heads, const void* q, const int64_t q_strides[2],
+                                       int32_t shared_pages, float softmax_scale, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  AttnLayout l;
+  AttnParams p;
+  palu_status st = attn_params(cache, false, tokens, offsets, max_new, q_heads, q, q_strides, shared_pages, softmax_scale, out,
+                               workspace, workspace_bytes, &l, &p);
+  if (st != PALU_OK) return st;
+  CUtensorMap km, vm;
+  if ((st = page_map(&km, cache, cache->k_pages, cache->k_strides)) != PALU_OK ||
+      (st = page_map(&vm, cache, cache->v_pages, cache->v_strides)) != PALU_OK)
+    return st;
+  p.c = paged_view(cache);
   const bool bf16 = cache->dtype == PALU_TYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto* const attend = l.both ? launch_both : l.R_own == kManyRows ? launch_many : launch_few;
   if ((st = attend(p, km, vm, bf16, s)) != PALU_OK) return st;
-  if (!l.shared) {
-    if (l.R_own < kManyRows) {
-      const dim3 jgrid(device_sm_count(), l.R_own);
-      return bf16 ? launch(paged_join_units_kernel<true, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p)
-                  : launch(paged_join_units_kernel<false, 1>, jgrid, 32 * kJoinWarps, 0, true, s, "paged_join_units_kernel launch", p);
-    }
-    const dim3 jgrid(device_sm_count(), l.R_own / kJoinWarps);
-    return bf16 ? launch(paged_join_units_kernel<true, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
-                         "paged_join_units_kernel launch", p)
-                : launch(paged_join_units_kernel<false, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
-                         "paged_join_units_kernel launch", p);
-  }
-  const long long rows = (long long)p.N * p.Hq;
-  if (rows <= kJoinRows)
-    return bf16 ? launch(paged_join_rows_kernel<true, 1>, dim3((unsigned)rows), 32 * kJoinWarps, 0, true, s,
-                         "paged_join_rows_kernel launch", p)
-                : launch(paged_join_rows_kernel<false, 1>, dim3((unsigned)rows), 32 * kJoinWarps, 0, true, s,
-                         "paged_join_rows_kernel launch", p);
-  const dim3 jgrid((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
-  return bf16 ? launch(paged_join_rows_kernel<true, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
-                       "paged_join_rows_kernel launch", p)
-              : launch(paged_join_rows_kernel<false, kJoinWarps>, jgrid, 32 * kJoinWarps, 0, true, s,
-                       "paged_join_rows_kernel launch", p);
+  return bf16 ? launch_joins<true, false>(l, p, s) : launch_joins<false, false>(l, p, s);
+}
+
+extern "C" palu_status palu_paged4_attn_workspace_size(const palu_paged4_cache* cache, int64_t tokens, int32_t q_heads,
+                                                       int32_t max_new, int32_t shared_pages, size_t* bytes) {
+  AttnLayout l;
+  palu_paged_cache sizes;
+  palu_status st = sizes_of(cache, &sizes);
+  if (st != PALU_OK || (st = attn_layout(&sizes, true, tokens, q_heads, max_new, shared_pages, &l)) != PALU_OK) return st;
+  if (!bytes) return fail(PALU_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = l.total;
+  return PALU_OK;
+}
+
+extern "C" palu_status palu_paged4_attn(const palu_paged4_cache* cache, int64_t tokens, const int32_t* offsets,
+                                        int32_t max_new, int32_t q_heads, const void* q, const int64_t q_strides[2],
+                                        int32_t shared_pages, float softmax_scale, void* out, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  AttnLayout l;
+  AttnParams p;
+  palu_paged_cache sizes;
+  palu_status st = sizes_of(cache, &sizes);
+  if (st != PALU_OK || (st = attn_params(&sizes, true, tokens, offsets, max_new, q_heads, q, q_strides, shared_pages, softmax_scale,
+                                         out, workspace, workspace_bytes, &l, &p)) != PALU_OK)
+    return st;
+  p.c = paged4_view(cache);
+  const bool bf16 = cache->dtype == PALU_TYPE_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = launch_few4(p, bf16, s)) != PALU_OK) return st;
+  return bf16 ? launch_joins<true, true>(l, p, s) : launch_joins<false, true>(l, p, s);
 }

@@ -78,8 +78,8 @@ struct AttnParams {
 };
 
 // What a unit costs, in ticks of kClocks, in the kernel with row tiles of R: to
-// begin and end it, and a 128-key tile of it.
-template <int R>
+// begin and end it, and a 128-key tile of it.  FOUR: over pages of 4-bit codes.
+template <int R, bool FOUR>
 struct LineCost {
   static __device__ int unit(int rows) { return 2; }  // 5,700 clocks
   static __device__ int tile(int rows) { return 1; }  // 2,900
@@ -92,11 +92,19 @@ struct LineCost {
 // time of its 64 KB at memory speed).
 constexpr int kManyRows = 256;
 template <>
-struct LineCost<kManyRows> {
+struct LineCost<kManyRows, false> {
   static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 100 : 60; }
   static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 16 : 14; }
   static constexpr int kMaxTile = 16;
   static constexpr float kClocks = 200.f;
+};
+// A tile of codes is 20 KB.
+template <int R>
+struct LineCost<R, true> {
+  static __device__ int unit(int rows) { return 6; }
+  static __device__ int tile(int rows) { return 1; }
+  static constexpr int kMaxTile = 1;
+  static constexpr float kClocks = 1000.f;
 };
 
 // Row r (of a unit) -> token and query head, r < 256: g0 + r < 320 and Gq <= 64,
@@ -153,36 +161,36 @@ __device__ __forceinline__ int div_small(long long a, long long b) {
 }
 
 // Ticks of a unit of n tiles.
-template <int R>
+template <int R, bool FOUR>
 __device__ __forceinline__ long long unit_ticks(int rows, int n) {
-  return n ? LineCost<R>::unit(rows) + (long long)n * LineCost<R>::tile(rows) : 0;
+  return n ? LineCost<R, FOUR>::unit(rows) + (long long)n * LineCost<R, FOUR>::tile(rows) : 0;
 }
 
 // Ticks of a sequence's own units before row tile `rts`.
-template <int R>
+template <int R, bool FOUR>
 __device__ __forceinline__ long long seq_ticks(const SeqSpan& s, int rts, int Gq, int S0, int kv_heads) {
   long long t = 0;
   for (int rt = 0; rt < rts; ++rt) {
     const int rows = min(R, s.n * Gq - rt * R);
-    t += unit_ticks<R>(rows, own_tiles(s, rt * R, rows, Gq, S0));
+    t += unit_ticks<R, FOUR>(rows, own_tiles(s, rt * R, rows, Gq, S0));
   }
   return t * kv_heads;
 }
-template <int R>
+template <int R, bool FOUR>
 __device__ __forceinline__ long long seq_ticks(const SeqSpan& s, int Gq, int S0, int kv_heads) {
   if (s.n * Gq <= R) {  // one row tile, the usual case: its last token sees everything
     const int keys = s.n ? s.len - S0 : 0;
-    return unit_ticks<R>(s.n * Gq, keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 0) * kv_heads;
+    return unit_ticks<R, FOUR>(s.n * Gq, keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 0) * kv_heads;
   }
-  return seq_ticks<R>(s, (s.n * Gq + R - 1) / R, Gq, S0, kv_heads);
+  return seq_ticks<R, FOUR>(s, (s.n * Gq + R - 1) / R, Gq, S0, kv_heads);
 }
 
 // Ticks of one KV head's prefix units before row tile `rts` (all: rts row tiles).
-template <int R>
+template <int R, bool FOUR>
 __device__ __forceinline__ long long prefix_ticks(int all_rows, int rts, int tiles) {
   const int full = min(rts, all_rows / R);
-  long long t = full * unit_ticks<R>(R, tiles);
-  if (rts > full) t += unit_ticks<R>(all_rows - full * R, tiles);
+  long long t = full * unit_ticks<R, FOUR>(R, tiles);
+  if (rts > full) t += unit_ticks<R, FOUR>(all_rows - full * R, tiles);
   return t;
 }
 
@@ -222,7 +230,7 @@ __device__ __forceinline__ int split_ctas(float a, float b, int grid) {
 
 // R: row tiles of the own units; RP: of the prefix units.  RP != R: a line of
 // each.
-template <int R, int RP, int THREADS>
+template <int R, int RP, int THREADS, bool FOUR = false>
 __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc, int tid) {
   constexpr int nthr = THREADS, nwarp = THREADS / 32;
   constexpr bool SPLIT = R != RP;
@@ -244,7 +252,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
     const SeqSpan s = seq_span(p, b, &bad);
     if (s.n && row_limit(s, 0) < p.S0) sc->cut_prefix = 1;
     if (s.n) longest = max(longest, s.len);
-    mine += seq_ticks<R>(s, p.Gq, p.S0, Hkv);
+    mine += seq_ticks<R, FOUR>(s, p.Gq, p.S0, Hkv);
     // without a prefix nothing joins parts of every row: rows that see nothing, or that are before the first
     // sequence, are zeroed here, all CTAs sharing them
     if (p.S0 == 0) {
@@ -275,12 +283,12 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
 #pragma unroll
     for (int w = 0; w < nwarp; ++w) longest = max(longest, sc->warp_longest[w]);
     longest = min(longest, p.S0);
-    prefix = Hkv * prefix_ticks<RP>(all_rows, (all_rows + RP - 1) / RP, prefix_tiles_of(longest));
+    prefix = Hkv * prefix_ticks<RP, FOUR>(all_rows, (all_rows + RP - 1) / RP, prefix_tiles_of(longest));
   }
   int cta = blockIdx.x, grid = gridDim.x;
   bool has_prefix = p.S0 > 0, has_own = true;
   if (SPLIT) {
-    const int g = split_ctas((float)prefix * LineCost<RP>::kClocks, (float)own * LineCost<R>::kClocks, grid);
+    const int g = split_ctas((float)prefix * LineCost<RP, FOUR>::kClocks, (float)own * LineCost<R, FOUR>::kClocks, grid);
     has_prefix = cta < g;
     has_own = !has_prefix;
     grid = has_prefix ? g : grid - g;
@@ -291,7 +299,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
   before += prefix;
   const long long total = prefix + (has_own ? own : 0);
   // a stretch is never shorter than a tile, so that every CTA between a unit's first and last holds a part of it
-  const long long tile = SPLIT && has_prefix ? LineCost<RP>::kMaxTile : LineCost<R>::kMaxTile;
+  const long long tile = SPLIT && has_prefix ? LineCost<RP, FOUR>::kMaxTile : LineCost<R, FOUR>::kMaxTile;
   const long long W = max((total + grid - 1) / grid, tile);
   const long long w0 = cta * W, w1 = min(w0 + W, total);
   if (has_own) {
@@ -302,7 +310,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
       long long base = before;
       for (int b = b0; b < b1; ++b) {
         if (cta == 0) part.plan[1 + b] = base;
-        const long long t = per == 1 ? mine : seq_ticks<R>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
+        const long long t = per == 1 ? mine : seq_ticks<R, FOUR>(seq_span(p, b, &bad), p.Gq, p.S0, Hkv);
         if (here && at >= base && at < base + t) {
           sc->b = b;
           sc->base = base;
@@ -333,7 +341,7 @@ __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc,
 // Calls unit(meta) for each unit of which the CTA's stretch of the line has
 // tiles, in order, until it returns false: run by one warp, all its lanes.
 // SPLIT: the line is one of two, of the prefix or of the own units.
-template <int R, bool SPLIT, class F>
+template <int R, bool SPLIT, bool FOUR = false, class F>
 __device__ __forceinline__ void plan_walk(const AttnParams& p, const PartSet& part, const PlanScratch* sc, F&& unit) {
   const int Hkv = p.c.kv_heads;
   const long long w0 = sc->w0, w1 = sc->w1;
@@ -342,8 +350,8 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PartSet& pa
   UnitMeta m = {};
   // the tiles of a unit [u0, u0 + ticks) that begin in [w0, w1)
   auto run_unit = [&](long long u0, int n, int key_base, int key_end) -> bool {
-    const int t = LineCost<R>::tile(m.rows);
-    const long long f = u0 + LineCost<R>::unit(m.rows);
+    const int t = LineCost<R, FOUR>::tile(m.rows);
+    const long long f = u0 + LineCost<R, FOUR>::unit(m.rows);
     // tiles that begin before x
     auto before = [&](long long x) -> int {
       if (x <= f) return 0;
@@ -365,7 +373,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PartSet& pa
   long long base = 0;
   if (has_prefix) {
     const int all_rows = p.N * p.Gq, rts = (all_rows + R - 1) / R, tiles = prefix_tiles_of(sc->prefix_end);
-    const long long head = prefix_ticks<R>(all_rows, rts, tiles), full = unit_ticks<R>(R, tiles);
+    const long long head = prefix_ticks<R, FOUR>(all_rows, rts, tiles), full = unit_ticks<R, FOUR>(R, tiles);
     m.pos = m.seq = 0;
     m.prefix = 1;
     if (w0 < head * Hkv) {
@@ -393,7 +401,7 @@ __device__ __forceinline__ void plan_walk(const AttnParams& p, const PartSet& pa
       m.rows = min(R, s.n * p.Gq - rt * R);
       const int n = own_tiles(s, rt * R, m.rows, p.Gq, p.S0);
       if (!n) continue;
-      const long long ticks = unit_ticks<R>(m.rows, n);
+      const long long ticks = unit_ticks<R, FOUR>(m.rows, n);
       const int end = row_limit(s, (rt * R + m.rows - 1) / p.Gq), i = rt * R / p.Gq;
       m.tok = s.tok0 + i;
       m.g0 = rt * R - i * p.Gq;
@@ -490,5 +498,7 @@ palu_status launch(K kernel, dim3 grid, int threads, int smem, bool dependent, c
 palu_status launch_few(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 palu_status launch_many(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 palu_status launch_both(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
+// Over pages of 4-bit codes (paged4_few.cu).
+palu_status launch_few4(const AttnParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace palu

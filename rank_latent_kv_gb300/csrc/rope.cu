@@ -1,0 +1,115 @@
+// Rotation tables (include/rope.h).
+//
+// A table is written once and read by every layer; 131,072 positions of 128
+// are 67 MB, so writing them is the bound if a value costs few instructions.
+// The angles of far positions are the difficulty: p f_i needs more bits than
+// fp32 has, and fp64 arithmetic is 1/60 of fp32's rate here.  So a pair's turn a
+// position, f_i / 2 pi, is a 64-bit fraction of a whole turn, and its product
+// with the position wraps around exactly: two integer additions from one row to
+// the next.  Of the fraction the nearest quarter turn is taken off, and the rest,
+// at most an eighth of a turn, goes through the Taylor series of sine (to the
+// 9th power, off by 2e-9) and cosine (to the 10th, 1e-10).
+#include <math.h>
+
+#include "palu_internal.cuh"
+#include "rope.h"
+
+namespace palu {
+
+struct RopeParams {
+  uint64_t turn[kHeadDim / 2];  // f_i / 2 pi in 2^-64 of a turn
+  float* out;
+  long long start, positions;
+  float magnitude;
+  int rope;
+};
+
+constexpr int kRopeThreads = 256;
+
+// cos and sin of `turn` / 2^64 turns, times m
+__device__ __forceinline__ void turn_cos_sin(uint64_t turn, float m, float& co, float& si) {
+  const uint64_t near = turn + (1ULL << 61);   // the quarter turns, rounded, in the top two bits
+  const int64_t rest = (int64_t)(turn - (near & (3ULL << 62)));
+  const unsigned quarter = (unsigned)(near >> 62);
+  // both halves: where the high one is short, the low one's bits count
+  const float f = fmaf((float)(uint32_t)rest, 0x1p-64f, (float)(int32_t)(rest >> 32) * 0x1p-32f);
+  const float x = f * 6.28318530717958648f, u = x * x;
+  const float s = x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), 1.f);
+  const float c = fmaf(u, fmaf(u, fmaf(u, fmaf(u, fmaf(u, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+  co = (quarter == 1 || quarter == 2) ? -a * m : a * m;
+  si = quarter & 2 ? -b * m : b * m;
+}
+
+// A thread has four pairs and goes down the rows; rope_dim / 8 threads a row.
+__global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const __grid_constant__ RopeParams p) {
+  const int per_row = p.rope >> 3;
+  const long long t = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+  const long long step = (long long)gridDim.x * kRopeThreads / per_row;  // rows; threads behind them have none
+  const int part = (int)(t % per_row);
+  long long row = t / per_row;
+  if (row >= step) return;
+  uint64_t at[4], by[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    at[i] = (uint64_t)(p.start + row) * p.turn[4 * part + i];
+    by[i] = (uint64_t)step * p.turn[4 * part + i];
+  }
+  for (; row < p.positions; row += step) {
+    float co[4], si[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn_cos_sin(at[i], p.magnitude, co[i], si[i]);
+      at[i] += by[i];
+    }
+    float* to = p.out + row * p.rope + 4 * part;
+    *reinterpret_cast<float4*>(to) = make_float4(co[0], co[1], co[2], co[3]);
+    *reinterpret_cast<float4*>(to + (p.rope >> 1)) = make_float4(si[0], si[1], si[2], si[3]);
+  }
+}
+
+}  // namespace palu
+
+using namespace palu;
+
+extern "C" palu_status palu_rope_table(const palu_rope_scaling* scaling, int64_t start, int64_t positions, float* out,
+                                       void* stream) {
+  if (!scaling) return fail(PALU_ERR_INVALID_ARG, "scaling is NULL");
+  const palu_rope_scaling& s = *scaling;
+  const int d = s.rope_dim;
+  if (d < 16 || d > kHeadDim || d % 16) return fail(PALU_ERR_UNSUPPORTED, "rope_dim must be a multiple of 16 in [16, 128]");
+  if (s.kind < PALU_ROPE_PLAIN || s.kind > PALU_ROPE_PARTS) return fail(PALU_ERR_INVALID_ARG, "unknown kind of scaling");
+  if (!(s.base > 1.0) || isinf(s.base)) return fail(PALU_ERR_INVALID_ARG, "base must be finite and above 1");
+  if (s.kind != PALU_ROPE_PLAIN && (!(s.factor >= 1.0) || isinf(s.factor)))
+    return fail(PALU_ERR_INVALID_ARG, "factor must be finite and at least 1");
+  if (s.kind == PALU_ROPE_PARTS && (!(s.original > 0.0) || isinf(s.original) || !(s.low_turns >= 0.0) ||
+                                    !(s.high_turns > s.low_turns) || isinf(s.high_turns)))
+    return fail(PALU_ERR_INVALID_ARG, "original must be positive, and 0 <= low_turns < high_turns, all finite");
+  if (!(fabs(s.magnitude) < (double)INFINITY)) return fail(PALU_ERR_INVALID_ARG, "magnitude must be finite");
+  if (start < 0 || start > (1LL << 40) || positions < 0 || positions > 0x7fffffff)
+    return fail(PALU_ERR_INVALID_ARG, "start must be in [0, 2^40], positions in [0, 2^31)");
+  if (positions == 0) return PALU_OK;
+  if (!out || ((uintptr_t)out & 15)) return fail(PALU_ERR_INVALID_ARG, "out must be given, 16-byte aligned");
+  RopeParams p = {};
+  const double two_pi = 6.283185307179586476925286766559;
+  const double base = s.kind == PALU_ROPE_NTK ? s.base * pow(s.factor, (double)d / (d - 2)) : s.base;
+  for (int i = 0; i < d / 2; ++i) {
+    double f = pow(base, -2.0 * i / d);
+    if (s.kind == PALU_ROPE_LINEAR) f /= s.factor;
+    if (s.kind == PALU_ROPE_PARTS) {
+      const double r = s.original * f / two_pi, t = fmin(fmax((r - s.low_turns) / (s.high_turns - s.low_turns), 0.0), 1.0);
+      f *= t + (1.0 - t) / s.factor;
+    }
+    p.turn[i] = (uint64_t)ldexp(f / two_pi, 64);  // f <= 1: below 2^62
+  }
+  p.out = out;
+  p.start = start;
+  p.positions = positions;
+  p.magnitude = (float)s.magnitude;
+  p.rope = d;
+  // eight CTAs an SM, and at least one row a thread
+  const long long threads = positions * (d >> 3), most = 8LL * device_sm_count();
+  const long long grid = (threads + kRopeThreads - 1) / kRopeThreads;
+  rope_table_kernel<<<(unsigned)(grid < most ? grid : most), kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return cuda_check(cudaGetLastError(), "rope_table_kernel launch");
+}

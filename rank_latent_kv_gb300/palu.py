@@ -8,6 +8,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 from ctypes import c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p, POINTER
@@ -33,6 +34,8 @@ PALU_DEVERR_SPAN = 128
 PALU_DEVERR_POSITION = 256
 PALU_TYPE_F16 = 0
 PALU_TYPE_BF16 = 1
+PALU_PAGED4_BLOCK = 2560    # bytes of 16 tokens of a head, keys and values
+PALU_ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "parts": 3}
 STATUS_NAMES = {0: "PALU_OK", 1: "PALU_ERR_INVALID_ARG", 2: "PALU_ERR_UNSUPPORTED", 3: "PALU_ERR_CAPACITY",
                 4: "PALU_ERR_NOT_INITIALIZED", 5: "PALU_ERR_CUDA", 6: "PALU_ERR_DEVICE"}
 
@@ -80,6 +83,23 @@ class palu_paged_cache(ctypes.Structure):
                 ("batch", c_int32), ("table_width", c_int32), ("n_pages", c_int64), ("k_pages", c_void_p),
                 ("v_pages", c_void_p), ("k_strides", c_int64 * 3), ("v_strides", c_int64 * 3),
                 ("page_table", c_void_p), ("lengths", c_void_p), ("error", c_void_p)]
+
+
+class palu_paged4_cache(ctypes.Structure):
+    _fields_ = [("magic", c_int32), ("dtype", c_int32), ("kv_heads", c_int32), ("page_size", c_int32),
+                ("batch", c_int32), ("table_width", c_int32), ("n_pages", c_int64), ("pages", c_void_p),
+                ("strides", c_int64 * 2), ("page_table", c_void_p), ("lengths", c_void_p), ("error", c_void_p)]
+
+
+class palu_page_pool(ctypes.Structure):
+    _fields_ = [("magic", c_int32), ("page_size", c_int32), ("batch", c_int32), ("table_width", c_int32),
+                ("n_pages", c_int64), ("page_table", c_void_p), ("lengths", c_void_p), ("held", c_void_p),
+                ("free_pages", c_void_p), ("n_free", c_void_p), ("error", c_void_p)]
+
+
+class palu_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", c_int32), ("rope_dim", c_int32), ("base", c_double), ("factor", c_double),
+                ("original", c_double), ("low_turns", c_double), ("high_turns", c_double), ("magnitude", c_double)]
 
 
 _P = POINTER
@@ -145,6 +165,20 @@ _SIGNATURES = {
     "palu_paged_attn": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_float,
                                   c_void_p, c_void_p, c_size_t, c_void_p]),
     "palu_paged_sync": (c_int32, [c_void_p, _P(c_uint32), c_void_p]),
+    "palu_paged4_cache_init": (c_int32, [_P(palu_paged4_cache), c_int32, c_int32, c_int32, c_int64, c_void_p, c_void_p,
+                                         c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
+    "palu_paged4_append": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "palu_paged4_read": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "palu_paged4_attn_workspace_size": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_int32, _P(c_size_t)]),
+    "palu_paged4_attn": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_float,
+                                   c_void_p, c_void_p, c_size_t, c_void_p]),
+    "palu_paged4_sync": (c_int32, [c_void_p, _P(c_uint32), c_void_p]),
+    "palu_page_pool_init": (c_int32, [_P(palu_page_pool), c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_void_p, c_void_p]),
+    "palu_page_plan": (c_int32, [c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "palu_page_pool_sync": (c_int32, [c_void_p, _P(c_uint32), c_void_p]),
+    "palu_rope_table": (c_int32, [_P(palu_rope_scaling), c_int64, c_int64, c_void_p, c_void_p]),
     "palu_draft_verify": (c_int32, [c_int64, c_int32, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
 }
@@ -601,37 +635,24 @@ def qk_norm_rope(q, k, positions, cos_sin=None, q_weight=None, k_weight=None, ep
     return q_out, k_out
 
 
-class PagedCache:
-    """A paged key/value cache (include/paged.h) on the caller's tensors.
-    k_pages, v_pages: fp16 or bf16 [n_pages, Hkv, page_size, 128], any strides with contiguous channels (a pool kept
-    token-major, or keys and values interleaved, is passed as a view).  page_table int32 [B, width] and lengths int64
-    [B]: the program's own, read by every call; change them in place to hand out pages and to roll tokens back."""
+class _Paged:
+    """What the paged caches have in common: the calls on page table, lengths and offsets."""
 
-    def __init__(self, k_pages, v_pages, page_table, lengths):
-        dev = _here(k_pages, "k_pages")
-        if k_pages.dtype not in _TYPES:
-            raise ValueError(f"k_pages has dtype {k_pages.dtype}; expected torch.float16 or torch.bfloat16")
-        self.dtype, self.device, self._dev = k_pages.dtype, k_pages.device, dev
-        n_pages, self.kv_heads, self.page_size, _ = shape = _shape_of(k_pages, "k_pages", 4)
-        _rows(k_pages, "k_pages", shape, self.dtype, dev)
-        _rows(v_pages, "v_pages", shape, self.dtype, dev)
+    def _bind(self, kind):
+        l = lib()
+        self._append, self._workspace = getattr(l, kind + "_append"), getattr(l, kind + "_attn_workspace_size")
+        self._attn, self._sync = getattr(l, kind + "_attn"), getattr(l, kind + "_sync")
+        self._c = ctypes.addressof(self.c)
+        self._offsets = (self.batch + 1,)
+
+    def _tables(self, page_table, lengths, dev):
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be a tensor [batch, width]")
         self.batch, self.width = page_table.shape
         _at(page_table, "page_table", (self.batch, self.width), _I32, dev)
         _at(lengths, "lengths", (self.batch,), _I64, dev)
-        self.k_pages, self.v_pages, self.page_table, self.lengths = k_pages, v_pages, page_table, lengths
+        self.page_table, self.lengths = page_table, lengths
         self.error = torch.zeros(1, dtype=_I32, device=self.device)
-
-        def strides(t):  # of a dimension of one element: anything that is aligned
-            return _pack3(*[s if n > 1 else D for s, n in zip(t.stride()[:3], shape)])
-        self.c = palu_paged_cache()
-        _check(lib().palu_paged_cache_init(ctypes.byref(self.c), _TYPES[self.dtype], self.kv_heads, self.page_size, n_pages,
-                                           k_pages.data_ptr(), strides(k_pages), v_pages.data_ptr(), strides(v_pages),
-                                           page_table.data_ptr(), self.batch, self.width, lengths.data_ptr(),
-                                           self.error.data_ptr()))
-        self._c = ctypes.addressof(self.c)
-        self._offsets = (self.batch + 1,)
 
     def _on_current(self):
         if self._dev != torch._C._cuda_getDevice():
@@ -663,14 +684,14 @@ class PagedCache:
         elif q_out is not None:
             raise ValueError("q_out is given without q")
         if n:
-            _check(lib().palu_paged_append(self._c, tr, n, op, hq, qp, qs, kp, ks, vp, vs, pos, out, _raw_stream(stream, dev)))
+            _check(self._append(self._c, tr, n, op, hq, qp, qs, kp, ks, vp, vs, pos, out, _raw_stream(stream, dev)))
         return q_out
 
     def attend_workspace(self, tokens, q_heads, max_new, shared_pages=0, stream=None):
         """A workspace for attend calls of up to these sizes, with any number of shared pages unless this is 0 (calls that
         share one must not overlap on the GPU)."""
         n = c_size_t()
-        _check(lib().palu_paged_attn_workspace_size(self._c, max(tokens, 1), q_heads, max_new, shared_pages, ctypes.byref(n)))
+        _check(self._workspace(self._c, max(tokens, 1), q_heads, max_new, shared_pages, ctypes.byref(n)))
         return _empty(max(n.value, 256), torch.uint8, self.device, stream)
 
     def attend(self, q, offsets, max_new, shared_pages=0, softmax_scale=0.0, workspace=None, out=None, stream=None):
@@ -691,15 +712,172 @@ class PagedCache:
             workspace = self.attend_workspace(n, hq, max_new, shared_pages, stream)
         size = workspace.numel()
         ws = _at(workspace, "workspace", (size,), torch.uint8, dev)
-        _check(lib().palu_paged_attn(self._c, n, op, max_new, hq, qp, qs, shared_pages, softmax_scale, to, ws, size,
+        _check(self._attn(self._c, n, op, max_new, hq, qp, qs, shared_pages, softmax_scale, to, ws, size,
                                      _raw_stream(stream, dev)))
         return out
 
     def sync(self, stream=None):
         """Synchronise; raises PaluError if the device error word was set (and clears it)."""
         e = c_uint32()
-        _check(lib().palu_paged_sync(self._c, ctypes.byref(e), _raw_stream(stream, self._dev)))
+        _check(self._sync(self._c, ctypes.byref(e), _raw_stream(stream, self._dev)))
         return e.value
+
+
+class PagedCache(_Paged):
+    """A paged key/value cache (include/paged.h) on the caller's tensors.
+    k_pages, v_pages: fp16 or bf16 [n_pages, Hkv, page_size, 128], any strides with contiguous channels (a pool kept
+    token-major, or keys and values interleaved, is passed as a view).  page_table int32 [B, width] and lengths int64
+    [B]: the program's own, read by every call; change them in place to hand out pages and to roll tokens back."""
+
+    def __init__(self, k_pages, v_pages, page_table, lengths):
+        dev = _here(k_pages, "k_pages")
+        if k_pages.dtype not in _TYPES:
+            raise ValueError(f"k_pages has dtype {k_pages.dtype}; expected torch.float16 or torch.bfloat16")
+        self.dtype, self.device, self._dev = k_pages.dtype, k_pages.device, dev
+        n_pages, self.kv_heads, self.page_size, _ = shape = _shape_of(k_pages, "k_pages", 4)
+        _rows(k_pages, "k_pages", shape, self.dtype, dev)
+        _rows(v_pages, "v_pages", shape, self.dtype, dev)
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self._tables(page_table, lengths, dev)
+
+        def strides(t):  # of a dimension of one element: anything that is aligned
+            return _pack3(*[s if n > 1 else D for s, n in zip(t.stride()[:3], shape)])
+        self.c = palu_paged_cache()
+        _check(lib().palu_paged_cache_init(ctypes.byref(self.c), _TYPES[self.dtype], self.kv_heads, self.page_size, n_pages,
+                                           k_pages.data_ptr(), strides(k_pages), v_pages.data_ptr(), strides(v_pages),
+                                           page_table.data_ptr(), self.batch, self.width, lengths.data_ptr(),
+                                           self.error.data_ptr()))
+        self._bind("palu_paged")
+
+
+class PagedCache4(_Paged):
+    """A paged cache held in 4 bits (include/paged4.h) on the caller's tensors: 160 bytes a token and KV head.
+    pages: uint8 [n_pages, Hkv, 10 * 16 * page_size] (PagedCache4.page_bytes(page_size)), pages of a head contiguous,
+    in any order otherwise; no initial contents are needed.  dtype: of the queries, keys, values and outputs (fp16 or
+    bf16).  page_table and lengths as in PagedCache, and append, attend_workspace, attend and sync as there, over the
+    values that the codes stand for."""
+
+    @staticmethod
+    def page_bytes(page_size):
+        return page_size // 16 * PALU_PAGED4_BLOCK
+
+    def __init__(self, pages, page_table, lengths, page_size, dtype):
+        dev = _here(pages, "pages")
+        if dtype not in _TYPES:
+            raise ValueError(f"dtype is {dtype}; expected torch.float16 or torch.bfloat16")
+        if pages.dtype is not torch.uint8 or pages.dim() != 3 or pages.shape[2] != self.page_bytes(page_size):
+            raise ValueError(f"pages is {pages.dtype} {tuple(pages.shape)}; expected torch.uint8 [n_pages, Hkv, "
+                             f"{self.page_bytes(page_size)}]")
+        n_pages, self.kv_heads, _ = pages.shape
+        st = [s if n > 1 else PALU_PAGED4_BLOCK for s, n in zip(pages.stride()[:2], pages.shape)]
+        if pages.stride(2) != 1 or pages.data_ptr() % 16 or any(s % 16 for s in st):
+            raise ValueError(f"pages must have contiguous, 16-byte aligned pages (strides {pages.stride()})")
+        self.dtype, self.device, self._dev, self.page_size, self.pages = dtype, pages.device, dev, page_size, pages
+        self._tables(page_table, lengths, dev)
+        self.c = palu_paged4_cache()
+        _check(lib().palu_paged4_cache_init(ctypes.byref(self.c), _TYPES[dtype], self.kv_heads, page_size, n_pages,
+                                            pages.data_ptr(), _pack2(*st), page_table.data_ptr(), self.batch, self.width,
+                                            lengths.data_ptr(), self.error.data_ptr()))
+        self._bind("palu_paged4")
+
+    def read(self, offsets, tokens, starts=None, k_out=None, v_out=None, stream=None):
+        """Tokens as the cache holds them: rows offsets[b] .. offsets[b+1]-1 of (k, v) [tokens, Hkv, 128] are sequence b's
+        tokens from place starts[b] (int64 [B]) on, or its last ones without starts.  Rows behind offsets[B] are left as
+        they were (undefined where the outputs are made here)."""
+        dev = self._on_current()
+        shape = (tokens, self.kv_heads, D)
+        op = _at(offsets, "offsets", self._offsets, _I32, dev)
+        sp = None if starts is None else _at(starts, "starts", (self.batch,), _I64, dev)
+        if k_out is None:
+            k_out = _empty(shape, self.dtype, self.device, stream)
+        if v_out is None:
+            v_out = _empty(shape, self.dtype, self.device, stream)
+        ko, vo = _at(k_out, "k_out", shape, self.dtype, dev), _at(v_out, "v_out", shape, self.dtype, dev)
+        if tokens:
+            _check(lib().palu_paged4_read(self._c, tokens, op, sp, ko, vo, _raw_stream(stream, dev)))
+        return k_out, v_out
+
+
+class PagePool:
+    """Pages handed out on the device (include/pages.h) for the caches that read page_table int32 [B, width] and lengths
+    int64 [B].  held int32 [B]: how many entries of its row a sequence has (default: none); free_pages int32 [n] and
+    n_free int32 [1]: the stack of free pages (default: pages n_pages-1 .. 0, so that page 0 is taken first).  All of
+    them are the program's to read and, between calls, to write."""
+
+    def __init__(self, page_table, lengths, page_size, held=None, free_pages=None, n_free=None, n_pages=None):
+        dev = _here(page_table, "page_table")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be a tensor [batch, width]")
+        self.batch, self.width = page_table.shape
+        self.device, self._dev, self.page_size = page_table.device, dev, page_size
+        if free_pages is None:
+            if n_pages is None or n_free is not None:
+                raise ValueError("free_pages and n_free come together, or n_pages instead of them")
+            free_pages = torch.arange(n_pages - 1, -1, -1, dtype=_I32, device=self.device)
+            n_free = torch.full((1,), n_pages, dtype=_I32, device=self.device)
+        elif n_free is None or n_pages is not None:
+            raise ValueError("free_pages and n_free come together, or n_pages instead of them")
+        if held is None:
+            held = torch.zeros(self.batch, dtype=_I32, device=self.device)
+        n = free_pages.numel()
+        self.page_table, self.lengths, self.held, self.free_pages, self.n_free = page_table, lengths, held, free_pages, n_free
+        self.error = torch.zeros(1, dtype=_I32, device=self.device)
+        self.c = palu_page_pool()
+        _check(lib().palu_page_pool_init(ctypes.byref(self.c), page_size, self.batch, self.width, n,
+                                         _at(page_table, "page_table", (self.batch, self.width), _I32, dev),
+                                         _at(lengths, "lengths", (self.batch,), _I64, dev),
+                                         _at(held, "held", (self.batch,), _I32, dev),
+                                         _at(free_pages, "free_pages", (n,), _I32, dev),
+                                         _at(n_free, "n_free", (1,), _I32, dev), self.error.data_ptr()))
+        self._c = ctypes.addressof(self.c)
+
+    def plan(self, new_tokens, tokens, shared_pages=0, offsets=None, positions=None, slots=None, stream=None):
+        """One step: sequence b brings new_tokens[b] (int32 [B]) tokens.  Lengths grow by them, pages behind the new lengths
+        go back (not the first shared_pages of a row) and missing ones are taken.  Returns (offsets int32 [B + 1],
+        positions int64 [tokens], slots int64 [tokens]: page * page_size + place in the page); rows behind offsets[B] are
+        -1.  Where the pages do not suffice nothing is changed, offsets are 0 and sync() tells."""
+        if self._dev != torch._C._cuda_getDevice():
+            raise ValueError(f"the pool is on {self.device}, which is not the current device")
+        dev = self._dev
+        np_ = _at(new_tokens, "new_tokens", (self.batch,), _I32, dev)
+        if offsets is None:
+            offsets = _empty((self.batch + 1,), _I32, self.device, stream)
+        if positions is None:
+            positions = _empty((tokens,), _I64, self.device, stream)
+        if slots is None:
+            slots = _empty((tokens,), _I64, self.device, stream)
+        op = _at(offsets, "offsets", (self.batch + 1,), _I32, dev)
+        pp, sp = _at(positions, "positions", (tokens,), _I64, dev), _at(slots, "slots", (tokens,), _I64, dev)
+        _check(lib().palu_page_plan(self._c, np_, tokens, shared_pages, op, pp, sp, _raw_stream(stream, dev)))
+        return offsets, positions, slots
+
+    def sync(self, stream=None):
+        """Synchronise; raises PaluError if the device error word was set (and clears it)."""
+        e = c_uint32()
+        _check(lib().palu_page_pool_sync(self._c, ctypes.byref(e), _raw_stream(stream, self._dev)))
+        return e.value
+
+
+def rope_table(positions, rope_dim, base=10000.0, scaling="plain", factor=1.0, original=0, low_turns=1.0, high_turns=32.0,
+               magnitude=None, start=0, out=None, device=None, stream=None):
+    """The rotation table of positions start .. start + positions - 1 (include/rope.h): fp32 [positions, rope_dim], cosines
+    then sines, as qk_norm_rope and the caches' append take it.  scaling: "plain", "linear", "ntk" or "parts" (`original`
+    tokens of the training's context, low_turns, high_turns).  magnitude multiplies the table: by default
+    0.1 ln(factor) + 1 for "parts", else 1."""
+    if scaling not in PALU_ROPE_KINDS:
+        raise ValueError(f"scaling is {scaling!r}; expected one of {', '.join(PALU_ROPE_KINDS)}")
+    if magnitude is None:
+        magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "parts" and factor > 0 else 1.0
+    cur = torch.cuda.current_device()
+    if out is None:
+        where = torch.device("cuda", cur) if device is None else torch.device(device)
+        if where.type != "cuda" or where.index not in (None, cur):
+            raise ValueError(f"{where} is not the current device")
+        out = _empty((positions, rope_dim), _F32, torch.device("cuda", cur), stream)
+    to = _at(out, "out", (positions, rope_dim), _F32, _here(out, "out"))
+    s = palu_rope_scaling(PALU_ROPE_KINDS[scaling], rope_dim, base, factor, original, low_turns, high_turns, magnitude)
+    _check(lib().palu_rope_table(ctypes.byref(s), start, positions, to, _raw_stream(stream, cur)))
+    return out
 
 
 def _table(t, name, shape, dev):
