@@ -21,10 +21,10 @@
 //   when a weight would pass 2^14; where a scale above 1 is met both bounds are
 //   lowered by its power of two, so that no p s passes 2^15.  Weights down to
 //   2^-20 of the largest keep all their bits.
-// A persistent CTA an SM; a loading warp copies a tile's blocks, a page of a
-// head by one bulk copy, into a ring of stages; the other warps take a block
-// of 16 tokens of a tile each, in two groups that take tiles in turn (one group
-// for 9 to 16 rows, whose accumulators need the registers).
+// A persistent CTA an SM; a loading warp copies 240 keys at a time, a page of a
+// head by one bulk copy, into a ring of stages; 15 warps take a block of 16
+// tokens of a stage each (for 9 to 16 rows, whose accumulators need the
+// registers, 8 warps two blocks of 256 keys each).
 #pragma once
 
 #include <math.h>
@@ -35,35 +35,37 @@
 
 namespace palu {
 
-constexpr int kTile4 = kKeyTile / 16 * kBlock4;  // 20 KB of codes, scales and zeros
 template <int NT>
-constexpr int kFew4Warps = NT == 1 ? 16 : 8;
+constexpr int kFew4Warps = NT == 1 ? 15 : 8;
 template <int NT>
 constexpr int kFew4Threads = 32 * (kFew4Warps<NT> + 1);
+template <int NT>
+constexpr int kFew4Blocks = NT == 1 ? 15 : 16;                 // of a stage
+template <int NT>
+constexpr int kFew4StageBytes = kFew4Blocks<NT> * kBlock4;     // about 40 KB of codes, scales and zeros
+constexpr int kFew4Stages = 4;
 constexpr int kMerge4Stride = kHeadDim + 2;
 template <int NT>
 constexpr int kFew4MergeBytes = kFew4Warps<NT> * 8 * kMerge4Stride * 4;
-template <int NT>
-constexpr int kFew4Stages = NT == 1 ? 7 : 9;
 constexpr float kLift4 = 6.f;      // log2: the reference's distance from the maximum
 constexpr float kRaise4 = 14.f;    // log2: the largest weight before it is raised
 constexpr float kNothing4 = -1e30f;  // a reference before any key has been seen
 
-// One tile, as the loading warp hands it to the others.
-struct Tile4Meta {
-  UnitMeta u;
+// One stage, as the loading warp hands it to the others.
+struct Stage4Meta {
   int key0;         // place of the first key
-  int valid;        // keys of the tile that exist (1 .. 128); 0: the line has ended
+  int valid;        // keys of the stage that exist; 0: the line has ended
   int first, last;  // of the stretch
+  UnitMeta u;
 };
-template <int NT>
 struct Few4Smem {
-  uint64_t full[kFew4Stages<NT>], empty[kFew4Stages<NT>], join;
-  Tile4Meta meta[kFew4Stages<NT>];
-  int failed;  // a wait ran out: the remaining ones are not begun
+  alignas(16) Stage4Meta meta[kFew4Stages];
+  uint64_t full[kFew4Stages], empty[kFew4Stages], join;
+  UnitMeta unit[16];           // each warp's, while it works on it
+  int failed;                 // a wait ran out: the remaining ones are not begun
 };
 template <int NT>
-constexpr int kFew4SmemBytes = 128 + kFew4Stages<NT> * kTile4 + kFew4MergeBytes<NT> + (int)sizeof(Few4Smem<NT>);
+constexpr int kFew4SmemBytes = 128 + kFew4Stages * kFew4StageBytes<NT> + kFew4MergeBytes<NT> + (int)sizeof(Few4Smem);
 static_assert(kFew4SmemBytes<1> + sizeof(PlanScratch) <= 232448 && kFew4SmemBytes<2> + sizeof(PlanScratch) <= 232448,
               "shared memory of a few-rows CTA");
 
@@ -71,15 +73,15 @@ __device__ __forceinline__ uint8_t* few4_smem(uint8_t* raw) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
 }
 template <int NT>
-__device__ __forceinline__ Few4Smem<NT>& few4_shared(uint8_t* smem) {
-  return *reinterpret_cast<Few4Smem<NT>*>(smem + kFew4Stages<NT> * kTile4 + kFew4MergeBytes<NT>);
+__device__ __forceinline__ Few4Smem& few4_shared(uint8_t* smem) {
+  return *reinterpret_cast<Few4Smem*>(smem + kFew4Stages * kFew4StageBytes<NT> + kFew4MergeBytes<NT>);
 }
 template <int NT>
-__device__ __forceinline__ void few4_init(Few4Smem<NT>& sh) {
-  for (int i = 0; i < kFew4Stages<NT>; ++i) {
+__device__ __forceinline__ void few4_init(Few4Smem& sh) {
+  for (int i = 0; i < kFew4Stages; ++i) {
     mbar_init(&sh.full[i], 1);
     mbar_init(&sh.empty[i], kFew4Warps<NT>);
-    sh.meta[i] = Tile4Meta{};
+    sh.meta[i] = Stage4Meta{};
   }
   mbar_init(&sh.join, kFew4Warps<NT>);
   sh.failed = 0;
@@ -111,11 +113,20 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-// D = A(16x8) * B(8x8) + D in tf32
-__device__ __forceinline__ void mma_tf32(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+// D = A(16x8) * B(8x8) in tf32
+__device__ __forceinline__ void first_tf32(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D = A(16x16) * B(16x8) (+ D) in fp16, free to be moved
+__device__ __forceinline__ void first_f16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void add_f16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -172,25 +183,27 @@ __device__ __forceinline__ void few4_queries(const AttnParams& p, const uint16_t
   mine *= 0x1p-24f;
   qz[0] = to_tf32(mine);
   qz[1] = to_tf32(mine - __uint_as_float(qz[0]));
-  *factor = __uint_as_float((uint32_t)(127 - e) << 23) * (p.scale_log2 * 0x1p24f);
+  // not 0, whatever the scale: a masked score of -infinity stays one
+  *factor = fmaxf(__uint_as_float((uint32_t)(127 - e) << 23) * (p.scale_log2 * 0x1p24f), 0x1p-120f);
 }
 
-// The stretch, by kFew4Threads<NT> threads.  NT: n8 tiles of rows (8 or 16 rows
-// a unit).
+// The stretch, by kFew4Threads<NT> threads.  NT: n8 tiles of rows (8 or 16 rows a
+// unit).
 template <bool BF16, int NT, bool SPLIT>
 __device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet& part, const PlanScratch& plan, uint8_t* smem) {
-  constexpr int kWarps = kFew4Warps<NT>, kStages = kFew4Stages<NT>, kGroups = kWarps / 8, R = 8 * NT;
-  float* merge = reinterpret_cast<float*>(smem + kStages * kTile4);
-  Few4Smem<NT>& sh = few4_shared<NT>(smem);
+  constexpr int R = 8 * NT, kWarps = kFew4Warps<NT>, kBlocks = kFew4Blocks<NT>, kStage = kFew4StageBytes<NT>;
+  float* merge = reinterpret_cast<float*>(smem + kFew4Stages * kStage);
+  Few4Smem& sh = few4_shared<NT>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (plan.w1 <= plan.w0) return;
   if (warp == kWarps) {
     // ---- the loading warp
     unsigned bad = 0;
     int it = 0;
-    // room for the next tile: all lanes go on or stop together
+    // room for the next stage: all lanes go on or stop together
     auto room = [&] {
-      if (it >= kStages) wait_or_fail(&sh.empty[it % kStages], ((it / kStages) - 1) & 1, &sh.failed, p.c.error);
+      if (it >= kFew4Stages)
+        wait_or_fail(&sh.empty[it % kFew4Stages], ((it / kFew4Stages) - 1) & 1, &sh.failed, p.c.error);
       return !__any_sync(0xffffffffu, *(volatile int*)&sh.failed);
     };
     plan_walk<R, SPLIT, true>(p, part, &plan, [&](const UnitMeta& u) -> bool {
@@ -199,40 +212,51 @@ __device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet&
         asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
       }
-      for (int k = 0; k < u.n; ++k, ++it) {
-        const int st = it % kStages, key0 = u.key0 + k * kKeyTile, valid = min(kKeyTile, u.key_end - key0);
-        const int pages = (valid + p.c.page - 1) >> p.c.page_shift, blocks = (valid + 15) >> 4, per = p.c.page >> 4;
-        const int page = lane < pages ? page_of(p, u.seq, key0 + lane * p.c.page, &bad) : 0;
+      const int end = min(u.key0 + u.n * kKeyTile, u.key_end), per = p.c.page >> 4;
+      // a stage's pages, one a lane: the blocks of each that it has
+      struct Piece {
+        int page, from, first, n;  // from: block of the page; first: block of the stage
+      };
+      auto lookup = [&](int key0) {
+        const int b0 = key0 >> 4, b1 = min(b0 + kBlocks, (end + 15) >> 4), pi = (key0 >> p.c.page_shift) + lane;
+        const int lo = max(b0, pi * per), hi = min(b1, (pi + 1) * per);
+        Piece x = {0, lo - pi * per, lo - b0, hi - lo};
+        if (x.n > 0) x.page = page_of(p, u.seq, lo << 4, &bad);
+        return x;
+      };
+      Piece next = lookup(u.key0);
+      for (int key0 = u.key0; key0 < end; key0 += 16 * kBlocks, ++it) {
+        const int st = it % kFew4Stages, valid = min(16 * kBlocks, end - key0);
+        const Piece x = next;
+        next = lookup(key0 + 16 * kBlocks);  // in flight while this stage waits for room
         if (!room()) return false;
         if (lane == 0) {
-          sh.meta[st] = Tile4Meta{u, key0, valid, k == 0, k == u.n - 1};
-          mbar_arrive_expect_tx(&sh.full[st], blocks * kBlock4);
+          sh.meta[st] = Stage4Meta{key0, valid, key0 == u.key0, key0 + valid == end, u};
+          mbar_arrive_expect_tx(&sh.full[st], ((valid + 15) >> 4) * kBlock4);
         }
         __syncwarp();
-        if (lane < pages)
-          bulk_g2s(smem + st * kTile4 + lane * per * kBlock4, page4(p.c, page, u.kh), min(per, blocks - lane * per) * kBlock4,
-                   &sh.full[st]);
+        if (x.n > 0)
+          bulk_g2s(smem + st * kStage + x.first * kBlock4, page4(p.c, x.page, u.kh) + x.from * kBlock4, x.n * kBlock4, &sh.full[st]);
       }
       return true;
     });
     const bool ended = room();
-    if (ended && lane == 0) {  // a tile of no keys ends the line
-      sh.meta[it % kStages].valid = 0;
-      mbar_arrive(&sh.full[it % kStages]);
+    if (ended && lane == 0) {  // a stage of no keys ends the line
+      sh.meta[it % kFew4Stages].valid = 0;
+      mbar_arrive(&sh.full[it % kFew4Stages]);
     }
     if (bad) atomicOr(p.c.error, bad);
     // no copy is in flight when the block ends, also where the others gave up (the stage that the end took had
     // been emptied)
-    for (int k = max(it - kStages + (ended ? 1 : 0), 0); k < it; ++k)
-      if (!mbar_wait_bounded(&sh.full[k % kStages], (k / kStages) & 1)) break;
+    for (int k = max(it - kFew4Stages + (ended ? 1 : 0), 0); k < it; ++k)
+      if (!mbar_wait_bounded(&sh.full[k % kFew4Stages], (k / kFew4Stages) & 1)) break;
     return;
   }
-  // ---- 16 tokens of each tile of its group a warp
-  const int g = lane >> 2, c = lane & 3, group = warp >> 3, r0 = 16 * (warp & 7);
-  float ref[NT][2], l_run[NT][2], acc[NT][8][4], zacc[NT][4], factor[NT][2];
+  // ---- block `warp` of each stage (and `warp` + 8)
+  const int g = lane >> 2, c = lane & 3;
+  float ref[NT][2], acc[NT][8][4], zacc[NT][4], factor[NT][2];
   uint32_t qb[NT][4][4], qz[NT][2];
   int lim[NT][2], all_see = 0;  // tokens that every row of the unit sees
-  UnitMeta m = {};
   uint32_t joins = 0;
   // the warps meet (bounded, unlike a named barrier)
   auto join = [&] {
@@ -242,15 +266,20 @@ __device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet&
     ++joins;
     __syncwarp();
   };
-  for (int it = 0;; ++it) {
-    const int st = it % kStages;
-    wait_or_fail(&sh.full[st], (it / kStages) & 1, &sh.failed, p.c.error);
-    if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) break;
-    const Tile4Meta& tm = sh.meta[st];
-    const int valid = tm.valid, key0 = tm.key0, last = tm.last;
+  // the zeros' product: rows 0 .. 3 are the groups, row 4, of ones, gives the weights' sum
+  const uint32_t z_keep = g < 4 ? 0xffffffffu : 0u, z_ones = g == 4 ? 0x3c003c00u : 0u;
+  for (uint32_t st = 0, turn = 0;;) {
+    if (!__all_sync(0xffffffffu, mbar_try_wait(&sh.full[st], turn))) {
+      wait_or_fail(&sh.full[st], turn, &sh.failed, p.c.error);
+      if (__any_sync(0xffffffffu, *(volatile int*)&sh.failed)) break;
+    }
+    const uint4 head = lds128(smem_addr(&sh.meta[st]));
+    const int key0 = (int)head.x, valid = (int)head.y;
+    const bool last = head.w != 0;
     if (valid == 0) break;
-    if (tm.first) {
-      m = tm.u;
+    if (head.z) {
+      const UnitMeta m = sh.meta[st].u;
+      if (lane == 0) sh.unit[warp] = m;
       all_see = 0x7fffffff;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -264,7 +293,6 @@ __device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet&
           lim[nt][e] = r < m.rows ? unit_row_limit(p, plan, m, r) : 0;
           all_see = r < m.rows ? min(all_see, lim[nt][e]) : all_see;
           ref[nt][e] = kNothing4;
-          l_run[nt][e] = 0.f;
           zacc[nt][e] = zacc[nt][e + 2] = 0.f;
         }
 #pragma unroll
@@ -274,106 +302,106 @@ __device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet&
       }
       all_see = __reduce_min_sync(0xffffffffu, all_see);
     }
-    if (it % kGroups == group && r0 < valid) {
-      const uint32_t blk = smem_addr(smem + st * kTile4) + (warp & 7) * kBlock4;
+#pragma unroll 1
+    for (int r0 = 16 * warp; r0 < min(valid, 16 * kBlocks); r0 += 16 * kWarps) {
+      // a lane's codes lie 16 bytes a lane in a block, of the keys as of the values
+      const uint32_t blk = smem_addr(smem) + st * kStage + (r0 >> 4) * kBlock4, codes = blk + 16 * lane;
+      const uint32_t ks = blk + kKeyScales4 + 16 * g, vs = blk + kValueScales4 + 32 * c;
       // ---- scores
-      const uint4 k0 = lds128(blk + 64 * g + 16 * c), k1 = lds128(blk + 64 * (g + 8) + 16 * c);
-      const uint2 s0 = lds64(blk + kKeyScales4 + 16 * g), s1 = lds64(blk + kKeyScales4 + 16 * (g + 8));
-      const uint32_t z0 = __float_as_uint(lds_half(blk + kKeyScales4 + 16 * g + 8 + 2 * c));
-      const uint32_t z1 = __float_as_uint(lds_half(blk + kKeyScales4 + 16 * (g + 8) + 8 + 2 * c));
-      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-      const float2 f0a = half2_f(s0.x), f0b = half2_f(s0.y), f1a = half2_f(s1.x), f1b = half2_f(s1.y);
-      const float f0[4] = {f0a.x, f0a.y, f0b.x, f0b.y}, f1[4] = {f1a.x, f1a.y, f1b.x, f1b.y};
       float sc[NT][4];
+      {
+        const uint4 k0 = lds128(codes), k1 = lds128(codes + 512);
+        const uint2 s0 = lds64(ks), s1 = lds64(ks + 128);
+        const uint32_t z0 = __float_as_uint(lds_half(ks + 8 + 2 * c)), z1 = __float_as_uint(lds_half(ks + 136 + 2 * c));
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        const float2 f0a = half2_f(s0.x), f0b = half2_f(s0.y), f1a = half2_f(s1.x), f1b = half2_f(s1.y);
+        const float f0[4] = {f0a.x, f0a.y, f0b.x, f0b.y}, f1[4] = {f1a.x, f1a.y, f1b.x, f1b.y};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-        mma_tf32(sc[nt], z0, z1, z0, z1, qz[nt][0], qz[nt][1]);
-      }
+        for (int nt = 0; nt < NT; ++nt) first_tf32(sc[nt], z0, z1, z0, z1, qz[nt][0], qz[nt][1]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t h0 = w0[j] >> 8, h1 = w1[j] >> 8;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t h0 = w0[j] >> 8, h1 = w1[j] >> 8;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(d, w0[j] & kLow4, w1[j] & kLow4, w0[j] & kHigh4, w1[j] & kHigh4, qb[nt][j][0], qb[nt][j][1]);
-          mma_f16(d, h0 & kLow4, h1 & kLow4, h0 & kHigh4, h1 & kHigh4, qb[nt][j][2], qb[nt][j][3]);
-          sc[nt][0] = fmaf(f0[j], d[0], sc[nt][0]);
-          sc[nt][1] = fmaf(f0[j], d[1], sc[nt][1]);
-          sc[nt][2] = fmaf(f1[j], d[2], sc[nt][2]);
-          sc[nt][3] = fmaf(f1[j], d[3], sc[nt][3]);
+          for (int nt = 0; nt < NT; ++nt) {
+            float d[4];
+            first_f16(d, w0[j] & kLow4, w1[j] & kLow4, w0[j] & kHigh4, w1[j] & kHigh4, qb[nt][j][0], qb[nt][j][1]);
+            add_f16(d, h0 & kLow4, h1 & kLow4, h0 & kHigh4, h1 & kHigh4, qb[nt][j][2], qb[nt][j][3]);
+            float* const s = sc[nt];
+            s[0] = fmaf(f0[j], d[0], s[0]);
+            s[1] = fmaf(f0[j], d[1], s[1]);
+            s[2] = fmaf(f1[j], d[2], s[2]);
+            s[3] = fmaf(f1[j], d[3], s[3]);
+          }
         }
       }
       // ---- the values' scales, and how far they leave room for the weights
-      const uint32_t vb = blk + kValueCodes4, vs = blk + kValueScales4 + 32 * c;
       const uint4 sa = lds128(vs), sb = lds128(vs + 16);  // tokens 2 c, 2 c + 1; 2 c + 8, 2 c + 9
       uint32_t s2[2][4] = {{sa.x, sa.y, sa.z, sa.w}, {sb.x, sb.y, sb.z, sb.w}};
-      uint32_t z2[2] = {0u, 0u};
-      if (g < 4) {
-        z2[0] = lds32(vs + 128 + 4 * g);
-        z2[1] = lds32(vs + 128 + 16 + 4 * g);
-      }
-      const int t0 = key0 + r0;
-      const bool cut = t0 + 16 > all_see;
-      if (cut) {
-        // what lies behind the last key must not reach the products: 0 * NaN is NaN
+      uint32_t z2[2] = {(lds32(vs + 128 + 4 * (g & 3)) & z_keep) | z_ones, (lds32(vs + 144 + 4 * (g & 3)) & z_keep) | z_ones};
+      if (__builtin_expect(key0 + r0 + 16 > min(all_see, key0 + valid), 0)) {
+        // keys that some row does not see; what lies behind the last key must not reach the products: 0 * NaN is NaN
         const int left = valid - r0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t keep = (2 * c + 8 * h < left ? 0xffffu : 0u) | (2 * c + 8 * h + 1 < left ? 0xffff0000u : 0u);
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t keep = (2 * c + 8 * i < left ? 0xffffu : 0u) | (2 * c + 8 * i + 1 < left ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s2[h][j] &= keep;
-          z2[h] &= keep;
+          for (int j = 0; j < 4; ++j) s2[i][j] &= keep;
+          z2[i] &= keep;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int at = g + 8 * i;
+              if (at >= left || key0 + r0 + at >= lim[nt][e]) sc[nt][2 * i + e] = -INFINITY;
+            }
         }
       }
-      uint32_t smax = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) smax = max_u16x2(smax, max_u16x2(s2[0][j], s2[1][j]));
+      const uint32_t any = s2[0][0] | s2[0][1] | s2[0][2] | s2[0][3] | s2[1][0] | s2[1][1] | s2[1][2] | s2[1][3];
       float high = kRaise4;  // the largest weight, log2
-      if (__any_sync(0xffffffffu, (smax & 0xffffu) > 0x3c00u || (smax >> 16) > 0x3c00u)) {
-        const uint32_t x = __reduce_max_sync(0xffffffffu, max(smax & 0xffffu, smax >> 16));
-        high = kRaise4 - (float)(min((int)(x >> 10), 30) - 14);  // below 2^(exponent + 1)
+      // a scale of 2 or more (the exponent's top bit)?
+      if (__builtin_expect(__any_sync(0xffffffffu, any & 0x40004000u), 0)) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x = __vmaxu2(x, s2[i][j]);
+        x = __reduce_max_sync(0xffffffffu, max(x & 0x7fffu, x >> 16 & 0x7fffu));
+        high = kRaise4 - (float)(min((int)(x >> 10), 30) - 15);  // below 2^(exponent + 1)
       }
-      const float lift = kLift4 - (kRaise4 - high);
       // ---- weights
       uint32_t ph[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float* s = sc[nt];
+        float x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] *= factor[nt][e & 1];
-        if (cut)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[e] = t0 + g + 8 * (e >> 1) < lim[nt][e & 1] ? s[e] : -INFINITY;
-        const bool over = fmaxf(s[0], s[2]) > ref[nt][0] + high || fmaxf(s[1], s[3]) > ref[nt][1] + high;
-        if (__any_sync(0xffffffffu, over)) {
+        for (int e = 0; e < 4; ++e) x[e] = fmaf(sc[nt][e], factor[nt][e & 1], -ref[nt][e & 1]);
+        if (__builtin_expect(__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > high), 0)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float bm = fmaxf(s[e], s[e + 2]);
+            // the scores themselves: next to a reference that says "nothing yet" they were lost
+            x[e] = sc[nt][e] * factor[nt][e];
+            x[e + 2] = sc[nt][e + 2] * factor[nt][e];
+            float bm = fmaxf(x[e], x[e + 2]);
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
-            const float to = bm > ref[nt][e] + high ? bm - lift : ref[nt][e], al = ex2f_(ref[nt][e] - to);
+            for (int i = 4; i < 32; i <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, i));
+            const float to = bm > ref[nt][e] + high ? bm - (kLift4 - (kRaise4 - high)) : ref[nt][e], al = ex2f_(ref[nt][e] - to);
             ref[nt][e] = to;
-            l_run[nt][e] *= al;
             zacc[nt][e] *= al;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               acc[nt][mt][e] *= al;
               acc[nt][mt][e + 2] *= al;
             }
+            x[e] -= to;
+            x[e + 2] -= to;
           }
         }
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pr[e] = ex2f_(s[e] - ref[nt][e & 1]);
-        l_run[nt][0] += pr[0] + pr[2];
-        l_run[nt][1] += pr[1] + pr[3];
-        ph[nt][0] = movmatrix_t(pack_f16x2(pr[0], pr[1]));
-        ph[nt][1] = movmatrix_t(pack_f16x2(pr[2], pr[3]));
-        mma_f16(zacc[nt], z2[0], 0u, z2[1], 0u, ph[nt][0], ph[nt][1]);
+        ph[nt][0] = movmatrix_t(pack_f16x2(ex2f_(x[0]), ex2f_(x[1])));
+        ph[nt][1] = movmatrix_t(pack_f16x2(ex2f_(x[2]), ex2f_(x[3])));
+        add_f16(zacc[nt], z2[0], 0u, z2[1], 0u, ph[nt][0], ph[nt][1]);
       }
       // ---- values
-      const uint4 v0 = lds128(vb + 16 * lane), v1 = lds128(vb + 512 + 16 * lane);
+      const uint4 v0 = lds128(codes + kValueCodes4), v1 = lds128(codes + kValueCodes4 + 512);
       const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -384,17 +412,22 @@ __device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet&
           b[nt][1] = mul_f16x2(ph[nt][1], s2[1][j]);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = w[2 * j + h], y = x >> 8;
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = w[2 * j + i], y = x >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma_f16(acc[nt][2 * j + h], x & kLow4, x & kHigh4, y & kLow4, y & kHigh4, b[nt][0], b[nt][1]);
+            add_f16(acc[nt][2 * j + i], x & kLow4, x & kHigh4, y & kLow4, y & kHigh4, b[nt][0], b[nt][1]);
         }
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty[st]);
+    if (++st == kFew4Stages) {
+      st = 0;
+      turn ^= 1;
+    }
     if (last) {
+      const UnitMeta& m = sh.unit[warp];
       // join the warps' states, 8 rows at a time, and write the unit's result
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -402,9 +435,7 @@ __device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet&
         float* mw = merge + warp * 8 * kMerge4Stride;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float l = l_run[nt][e];
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+          const float l = __shfl_sync(0xffffffffu, zacc[nt][e], 4 * 4 + c);
           if (g == 0) {
             mw[(2 * c + e) * kMerge4Stride + kHeadDim] = ref[nt][e] == kNothing4 ? -INFINITY : ref[nt][e];
             mw[(2 * c + e) * kMerge4Stride + kHeadDim + 1] = l;
