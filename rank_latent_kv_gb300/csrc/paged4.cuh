@@ -36,6 +36,18 @@ __device__ __forceinline__ uint8_t* page4(const PagedView& c, int page, int head
   return reinterpret_cast<uint8_t*>(c.k) + (long long)page * c.ks0 + (long long)head * c.ks1;
 }
 
+// Queries enter fp16 products times 2^e, e such that the row's largest value
+// `big` comes to 2^13 .. 2^14 (rows of zeros or of infinities: as they are), and
+// the factor that takes the products back to log2 (not 0, whatever the scale: a
+// masked score of -infinity stays one).
+__device__ __forceinline__ int query_shift(float big) {
+  const int ex = (int)(__float_as_uint(big) >> 23);
+  return ex == 0 || ex == 255 ? 0 : max(min(13 + 127 - ex, 100), -113);
+}
+__device__ __forceinline__ float query_factor(int e, float scale_log2) {
+  return fmaxf(__uint_as_float((uint32_t)(127 - e) << 23) * scale_log2, 0x1p-120f);
+}
+
 // Work on whole blocks without a scan over the sequences: n rows touch at most
 // n / 16 + 2 blocks wherever they begin, so sequence b has the CTAs from
 // offsets[b] / 16 + 2 b on, and there are tokens / 16 + 2 batch of them.

@@ -158,9 +158,7 @@ __device__ __forceinline__ void few4_queries(const AttnParams& p, const uint16_t
   }
   big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
   big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-  // 2^e with big 2^e in [2^13, 2^14); rows of zeros or of infinities as they are
-  const int ex = (int)(__float_as_uint(big) >> 23);
-  const int e = ex == 0 || ex == 255 ? 0 : max(min(13 + 127 - ex, 100), -113);
+  const int e = query_shift(big);
   const float up = __uint_as_float((uint32_t)(e + 127) << 23);
   float mine = 0.f;
 #pragma unroll
@@ -183,8 +181,7 @@ __device__ __forceinline__ void few4_queries(const AttnParams& p, const uint16_t
   mine *= 0x1p-24f;
   qz[0] = to_tf32(mine);
   qz[1] = to_tf32(mine - __uint_as_float(qz[0]));
-  // not 0, whatever the scale: a masked score of -infinity stays one
-  *factor = fmaxf(__uint_as_float((uint32_t)(127 - e) << 23) * (p.scale_log2 * 0x1p24f), 0x1p-120f);
+  *factor = query_factor(e, p.scale_log2 * 0x1p24f);
 }
 
 // The stretch, by kFew4Threads<NT> threads.  NT: n8 tiles of rows (8 or 16 rows a

@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   grid_dep_launch();
   plan_start<8 * NT, kManyRows, kManyThreads>(p, &plan, threadIdx.x);
   if (plan.has_prefix) {
-    many_stretch<BF16, true>(p, p.prefix, kmap, vmap, plan, many_smem(smem_raw), [] {});
+    many_stretch<BF16, true, false>(p, p.prefix, &kmap, &vmap, plan, many_smem(smem_raw), [] {});
   } else {
     uint8_t* smem = few_smem(smem_raw);
     if (threadIdx.x == 0) few_init(few_shared(smem));

@@ -10,7 +10,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ PlanScratch plan;
   grid_dep_launch();
-  many_stretch<BF16, false>(p, p.part, kmap, vmap, plan, many_smem(smem_raw),
+  many_stretch<BF16, false, false>(p, p.part, &kmap, &vmap, plan, many_smem(smem_raw),
                      [&] { plan_start<kManyRows, kManyRows, kManyThreads - 256>(p, &plan, threadIdx.x - 256); });
 }
 

@@ -38,6 +38,7 @@
 // instead of adding up.
 #pragma once
 
+#include "paged4.cuh"
 #include "paged_attn.cuh"
 #include "splitk_attend.cuh"
 
@@ -62,6 +63,13 @@ struct ManySmem {
 };
 constexpr int kManySmemBytes = 1024 + (2 + kRing) * kTileBytes + (int)sizeof(ManySmem);
 static_assert(kManySmemBytes + sizeof(PlanScratch) <= 232448, "shared memory of a many-rows CTA");
+// Over pages of 4-bit codes: four warps more, which turn codes into the ring's tiles.
+constexpr int kMany4Threads = kManyThreads + 128;
+struct Many4Smem : ManySmem {
+  float factor[kManyRows];  // of each row: from the products back to log2
+};
+constexpr int kMany4SmemBytes = 1024 + (2 + kRing) * kTileBytes + (int)sizeof(Many4Smem);
+static_assert(kMany4SmemBytes + sizeof(PlanScratch) <= 232448, "shared memory of a many-rows CTA");
 
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_alloc(uint32_t* dst) {
@@ -205,24 +213,95 @@ __device__ __forceinline__ uint8_t* many_smem(uint8_t* raw) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
 }
 
-// The CTA's stretch, by all kManyThreads threads; `start` is run by warps 8 to
-// 10 before the others may need the plan (they would only wait for the same
-// code to arrive).
-template <bool BF16, bool SPLIT, class Start>
-__device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet& part, const CUtensorMap& kmap, const CUtensorMap& vmap,
+// ---------------------------------------------------------------- tiles from 4-bit codes
+// A thread's part of a 128-key tile, as it lies in the pages: one token's key
+// codes and scales; of the value codes the words of two m (of 16 channels each)
+// for four tokens, and those tokens' scales of the one group that these are in.
+struct Key4 {
+  uint4 codes[4], sz;
+};
+struct Value4 {
+  uint2 codes[8];
+  uint32_t s[2], z[2];
+};
+__device__ __forceinline__ uint32_t same_f16x2(uint32_t v, int high) { return __byte_perm(v, 0, high ? 0x3232 : 0x1010); }
+// z + s c of two codes that are 1024 + c, or 1024 + 16 c, in fp16
+__device__ __forceinline__ uint32_t value_low(uint32_t x, uint32_t s, uint32_t z) {
+  return fma_f16x2(sub_f16x2((x & 0x000f000fu) | 0x64006400u, 0x64006400u), s, z);
+}
+__device__ __forceinline__ uint32_t value_high(uint32_t x, uint32_t s, uint32_t z) {
+  return fma_f16x2(fma_f16x2((x & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u), s, z);
+}
+__device__ __forceinline__ void st128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Row `row` of a tile of keys: thread = token.
+__device__ __forceinline__ void store_keys(uint32_t tile, int row, const Key4& k) {
+  const uint32_t s[4] = {same_f16x2(k.sz.x, 0), same_f16x2(k.sz.x, 1), same_f16x2(k.sz.y, 0), same_f16x2(k.sz.y, 1)};
+  const uint32_t z[4] = {same_f16x2(k.sz.z, 0), same_f16x2(k.sz.z, 1), same_f16x2(k.sz.w, 0), same_f16x2(k.sz.w, 1)};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w[4] = {k.codes[c].x, k.codes[c].y, k.codes[c].z, k.codes[c].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t y = w[j] >> 8;
+      st128(panel_addr(tile, row, 4 * j + c), value_low(w[j], s[j], z[j]), value_high(w[j], s[j], z[j]), value_low(y, s[j], z[j]),
+            value_high(y, s[j], z[j]));
+    }
+  }
+}
+// The four tokens 2 c + odd + 8 e of block rows from `row0` on, 32 channels each:
+// chunks of eight channels, of which a word holds one code a token and nibble.
+// Lanes of the two m pairs take the odd and the even token first, so that eight
+// lanes write to all banks.
+__device__ __forceinline__ void store_values(uint32_t tile, int row0, int half, int c, int pair, const Value4& v) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      const int odd = step ^ pair, row = row0 + 2 * c + odd + 8 * e;
+      const uint32_t s = same_f16x2(v.s[e], odd), z = same_f16x2(v.z[e], odd), b = 2 * odd + e, sel = b | (b + 4) << 8;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t w0 = m ? v.codes[2 * g].y : v.codes[2 * g].x, w1 = m ? v.codes[2 * g + 1].y : v.codes[2 * g + 1].x;
+          const uint32_t x = __byte_perm(w0, w1, sel);  // the token's byte of each, low in either half
+          lo[g] = value_low(x, s, z);
+          hi[g] = value_high(x, s, z);
+        }
+        const int ch = 8 * half + 4 * pair + 2 * m;
+        st128(panel_addr(tile, row, ch), lo[0], lo[1], lo[2], lo[3]);
+        st128(panel_addr(tile, row, ch + 1), hi[0], hi[1], hi[2], hi[3]);
+      }
+    }
+}
+
+// The CTA's stretch, by all kManyThreads (FOUR: kMany4Threads, or more) threads;
+// `start` is run by warps 8 and up before the others may need the plan (they
+// would only wait for the same code to arrive).
+// FOUR: the pages hold 4-bit codes.  Warp 8 only plans; four warps fetch the
+// codes into registers, a tile ahead, and write fp16 tiles into the ring.  All
+// products are in fp16 then, also in a bf16 cache: the queries are brought into
+// its range by a power of two a row, which comes off again with the scores'
+// factor.
+template <bool BF16, bool SPLIT, bool FOUR, class Start>
+__device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet& part, const CUtensorMap* kmap, const CUtensorMap* vmap,
                                              const PlanScratch& plan, uint8_t* smem, Start&& start) {
+  constexpr bool MB = BF16 && !FOUR;  // the products' type
   uint8_t* ring = smem + 2 * kTileBytes;
   ManySmem& sh = *reinterpret_cast<ManySmem*>(ring + kRing * kTileBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned* const err = p.c.error;
   if (tid == 0) {
-    for (int i = 0; i < kFull; ++i) mbar_init(&sh.kv_full[i], 1);
+    for (int i = 0; i < kFull; ++i) mbar_init(&sh.kv_full[i], FOUR ? 4 : 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.kv_empty[i], 2);  // both halves, or one of them twice
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.meta_full[i], 1);
-      mbar_init(&sh.meta_empty[i], 10);  // eight softmax warps, two product warps
+      mbar_init(&sh.meta_empty[i], FOUR ? 14 : 10);  // eight softmax warps, two product warps, those of the tiles
       mbar_init(&sh.drain[i], 1);
       mbar_init(&sh.token[i], 1);
       mbar_init(&sh.s_full[i], 1);
@@ -260,7 +339,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       return true;
     };
     bool ok = true;
-    plan_walk<kManyRows, SPLIT>(p, part, &plan, [&](const UnitMeta& u) -> bool {
+    plan_walk<kManyRows, SPLIT, FOUR>(p, part, &plan, [&](const UnitMeta& u) -> bool {
       // the unit's queries are on their way to L2 while the unit before it is worked on
       for (int r = lane; r < u.rows; r += 32) {
         const uint16_t* q = row_query(p, u, r);
@@ -268,6 +347,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
       }
       if (!(ok = publish(u))) return false;
+      if (FOUR) return true;
       auto lookup = [&](int k) {
         const int place = u.key0 + k * kKeyTile + lane * p.c.page;
         return k < u.n && lane * p.c.page < kKeyTile && place < u.key_end ? page_of(p, u.seq, place, &bad) : -1;
@@ -286,8 +366,8 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
           __syncwarp();
           if (page >= 0) {
             const uint32_t dst = smem_addr(ring + st * kTileBytes) + lane * p.c.page * 128;
-            tma_page(dst, kv ? &vmap : &kmap, &sh.kv_full[item % kFull], 0, u.kh, page);
-            tma_page(dst + kPanelBytes, kv ? &vmap : &kmap, &sh.kv_full[item % kFull], 64, u.kh, page);
+            tma_page(dst, kv ? vmap : kmap, &sh.kv_full[item % kFull], 0, u.kh, page);
+            tma_page(dst + kPanelBytes, kv ? vmap : kmap, &sh.kv_full[item % kFull], 64, u.kh, page);
           }
         }
       }
@@ -301,11 +381,102 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
     // no copy is in flight when the block ends, also where the others gave up
     for (int i = max(item - kRing, 0); i < item; ++i)
       if (!mbar_wait_bounded(&sh.kv_full[i % kFull], (i / kFull) & 1)) break;
+  } else if (FOUR && warp > 10) {
+    // ---- tiles from codes, by warps 11 to 14
+    if (warp < 15) {
+      const int t = tid - 11 * 32, row = t & 15;                            // one token of block t / 16
+      const int half = row >> 3, c = row >> 1 & 3, pair = row & 1;          // and this part of its values
+      unsigned bad = 0;
+      struct Tile {
+        int seq, kh, key0, end, n;  // the unit's; n: tiles left
+      };
+      int units = 0;
+      bool ok = true;
+      // the next unit with its tiles (n 0: none)
+      auto next_unit = [&] {
+        Tile u = {};
+        wait_or_fail(&sh.meta_full[units & 1], (units >> 1) & 1, &sh.failed, err);
+        __syncwarp();
+        if (__any_sync(0xffffffffu, failed())) return u;
+        const UnitMeta& m = sh.meta[units & 1];
+        u.seq = m.seq, u.kh = m.kh, u.key0 = m.key0, u.end = m.key_end, u.n = m.n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meta_empty[units & 1]);
+        ++units;
+        return u;
+      };
+      // where the thread's block of the unit's next tile lies (nullptr: behind the last key), and how many tokens it has
+      auto block_of = [&](const Tile& u, int* left) -> const uint8_t* {
+        const int place = u.key0 + (t & ~15);
+        *left = u.end - place;
+        if (*left <= 0) return nullptr;
+        return page4(p.c, page_of(p, u.seq, place, &bad), u.kh) + (place & (p.c.page - 1)) / 16 * kBlock4;
+      };
+      auto load_keys = [&](const uint8_t* b) {
+        Key4 k = {};
+        if (b) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) k.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + 64 * row) + i);
+          k.sz = __ldg(reinterpret_cast<const uint4*>(b + kKeyScales4 + 16 * row));
+        }
+        return k;
+      };
+      auto load_values = [&](const uint8_t* b, int left) {
+        Value4 v = {};
+        if (b) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            v.codes[g] = __ldg(reinterpret_cast<const uint2*>(b + kValueCodes4 + 512 * half + 64 * g + 16 * c + 8 * pair));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint8_t* sz = b + kValueScales4 + 32 * c + 16 * e + 4 * (2 * half + pair);
+            // what lies behind the last key is 0: 0 * NaN is NaN
+            const uint32_t keep = (2 * c + 8 * e < left ? 0xffffu : 0u) | (2 * c + 8 * e + 1 < left ? 0xffff0000u : 0u);
+            v.s[e] = __ldg(reinterpret_cast<const uint32_t*>(sz)) & keep;
+            v.z[e] = __ldg(reinterpret_cast<const uint32_t*>(sz + 128)) & keep;
+          }
+        }
+        return v;
+      };
+      int item = 0;
+      // room for the next tile of the ring; then it is told
+      auto room = [&] {
+        if (item >= kRing) wait_or_fail(&sh.kv_empty[item % kRing], (item / kRing - 1) & 1, &sh.failed, err);
+        __syncwarp();
+        return !__any_sync(0xffffffffu, failed());
+      };
+      auto done = [&] {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[item % kFull]);
+        ++item;
+      };
+      Tile u = next_unit();
+      int left = 0;
+      const uint8_t* b = u.n ? block_of(u, &left) : nullptr;
+      Key4 k = load_keys(b);
+      Value4 v = load_values(b, left);
+      while (u.n) {
+        // the tile behind this one
+        u.key0 += kKeyTile;
+        if (--u.n == 0) u = next_unit();
+        b = u.n ? block_of(u, &left) : nullptr;
+        if (!(ok = room())) break;
+        store_keys(smem_addr(ring + item % kRing * kTileBytes), t, k);
+        done();
+        k = load_keys(b);
+        if (!(ok = room())) break;
+        store_values(smem_addr(ring + item % kRing * kTileBytes), t & ~15, half, c, pair, v);
+        done();
+        v = load_values(b, left);
+      }
+      if (bad) atomicOr(err, bad);
+    }
   } else if (warp >= 9) {
     // ---- products of half s
     const int s = warp - 9;
     const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
-    constexpr uint32_t idesc_s = instr_desc<BF16>(false), idesc_o = instr_desc<BF16>(true);
+    constexpr uint32_t idesc_s = instr_desc<MB>(false), idesc_o = instr_desc<MB>(true);
     // Waits on several barriers at once, one a lane: a wait costs about 150 clocks even when there is nothing to wait
     // for.  All lanes see the same outcome, so the control flow is uniform.
     auto wait_all = [&](int count, uint64_t* bar, uint32_t parity) {  // lanes 0 .. count - 1, each its own bar
@@ -407,7 +578,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
     // every product has ended before TMEM is given back
     commit(&sh.drain[s]);
     mbar_wait_bounded(&sh.drain[s], 0);
-  } else {
+  } else if (warp < 8) {
     // ---- softmax: half `s`, a row a thread
     const int s = warp >> 2, t = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of TMEM
@@ -434,16 +605,36 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         u.tok = m.tok, u.g0 = m.g0, u.kh = m.kh, u.rows = m.rows;
         const int r_base = both ? s * kHalf : 0, q_rows = both ? kHalf : kHalf / 2, q0 = both ? 0 : s * (kHalf / 2);
         const uint32_t q_tile = smem_addr(smem) + (both ? s : 0) * kTileBytes;
-        for (int i = t; i < q_rows * 16; i += kHalf) {
-          const int r = q0 + (i >> 4), ch = i & 15;
-          const bool there = r_base + r < u.rows;
-          const uint16_t* src = there ? row_query(p, u, r_base + r) + ch * 8 : p.q;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(panel_addr(q_tile, r, ch)), "l"(src),
-                       "r"(there ? 16 : 0)
-                       : "memory");
+        if constexpr (FOUR) {  // through registers: a half-warp a row
+#pragma unroll 4
+          for (int i = t >> 4; i < q_rows; i += kHalf / 16) {
+            const int r = q0 + i, ch = t & 15;
+            const uint4 raw = r_base + r < u.rows ? __ldg(reinterpret_cast<const uint4*>(row_query(p, u, r_base + r)) + ch)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+            const float2 f[4] = {unpack2<BF16>(raw.x), unpack2<BF16>(raw.y), unpack2<BF16>(raw.z), unpack2<BF16>(raw.w)};
+            float big = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) big = fmaxf(big, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+#pragma unroll
+            for (int x = 8; x; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+            const int e = query_shift(big);
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            st128(panel_addr(q_tile, r, ch), pack_f16x2(f[0].x * up, f[0].y * up), pack_f16x2(f[1].x * up, f[1].y * up),
+                  pack_f16x2(f[2].x * up, f[2].y * up), pack_f16x2(f[3].x * up, f[3].y * up));
+            if (ch == 0) static_cast<Many4Smem&>(sh).factor[r_base + r] = query_factor(e, p.scale_log2);
+          }
+        } else {
+          for (int i = t; i < q_rows * 16; i += kHalf) {
+            const int r = q0 + (i >> 4), ch = i & 15;
+            const bool there = r_base + r < u.rows;
+            const uint16_t* src = there ? row_query(p, u, r_base + r) + ch * 8 : p.q;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(panel_addr(q_tile, r, ch)), "l"(src),
+                         "r"(there ? 16 : 0)
+                         : "memory");
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
         }
-        cp_async_commit();
-        cp_async_wait<0>();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
@@ -456,7 +647,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       const int step = both ? 1 : 2;
       for (int j = both ? 0 : s; j < m.n; j += step, ++sc) {
         const int tile_key = m.key0 + j * kKeyTile, valid = m.key_end - tile_key;
-        if (valid < kKeyTile) {
+        if (!FOUR && valid < kKeyTile) {
           // the last tile's values behind the last key: 0 * NaN is NaN, so they are zeroed before the product (by both
           // halves, where both use them)
           const int vi = 2 * (tile0 + j) + 1;
@@ -470,6 +661,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         wait_or_fail(&sh.s_full[s], sc & 1, &sh.failed, err);
         __syncwarp();
         tc_fence_after();
+        const float scale = FOUR ? static_cast<const Many4Smem&>(sh).factor[r] : p.scale_log2;
         // The scores pass twice, 64 at a time, for the maximum and for the weights (a thread with all 128 spills).  Both
         // loops are kept rolled: a launch has to fetch its code, and the softmax has time to spare.
         uint32_t x[64];
@@ -496,10 +688,10 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
         }
-        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * p.scale_log2;
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale;
         // raise the maximum?  O of this half is complete up to the tile before: its product was issued before these scores
         float alpha = 1.f;
-        constexpr float kLift = BF16 ? 0.f : 6.f;
+        constexpr float kLift = MB ? 0.f : 6.f;
         if (top > ref + (kLift + kRaise) || (!seen && top != -INFINITY)) {
           alpha = seen ? ex2f_(ref - (top - kLift)) : 1.f;  // nothing but zeros so far: no factor
           ref = top - kLift;
@@ -525,11 +717,11 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float a = f[2 * i], b = f[2 * i + 1];
-            fma2(a, b, p.scale_log2, -ref);
+            fma2(a, b, scale, -ref);
             a = ex2f_(a);
             b = ex2f_(b);
             add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], a, b);
-            w[i] = pack2<BF16>(a, b);
+            w[i] = pack2<MB>(a, b);
           }
           tc_st32(s_addr + 32 * u, w);
           tc_wait_st();
