@@ -101,7 +101,7 @@ struct LineCost<kManyRows, false> {
 template <>
 struct LineCost<kManyRows, true> {
   static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 100 : 60; }
-  static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 16 : 8; }
+  static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 16 : 12; }
   static constexpr int kMaxTile = 16;
   static constexpr float kClocks = 200.f;
 };

@@ -388,11 +388,9 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       const int half = row >> 3, c = row >> 1 & 3, pair = row & 1;          // and this part of its values
       unsigned bad = 0;
       struct Tile {
-        int seq, kh, key0, end, n;  // the unit's; n: tiles left
+        int seq, kh, key0, end, n;  // the unit's; n: tiles left, 0: none
       };
       int units = 0;
-      bool ok = true;
-      // the next unit with its tiles (n 0: none)
       auto next_unit = [&] {
         Tile u = {};
         wait_or_fail(&sh.meta_full[units & 1], (units >> 1) & 1, &sh.failed, err);
@@ -405,70 +403,64 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         ++units;
         return u;
       };
-      // where the thread's block of the unit's next tile lies (nullptr: behind the last key), and how many tokens it has
-      auto block_of = [&](const Tile& u, int* left) -> const uint8_t* {
+      // The thread's block of a tile is looked up one tile before it is loaded, and loaded one tile before it is written.
+      auto lookup = [&](const Tile& u) {  // the page's number, or -1 behind the last key
         const int place = u.key0 + (t & ~15);
-        *left = u.end - place;
-        if (*left <= 0) return nullptr;
-        return page4(p.c, page_of(p, u.seq, place, &bad), u.kh) + (place & (p.c.page - 1)) / 16 * kBlock4;
+        return u.n && place < u.end ? __ldg(p.c.table + (long long)u.seq * p.c.width + (place >> p.c.page_shift)) : -1;
       };
-      auto load_keys = [&](const uint8_t* b) {
-        Key4 k = {};
-        if (b) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) k.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + 64 * row) + i);
-          k.sz = __ldg(reinterpret_cast<const uint4*>(b + kKeyScales4 + 16 * row));
+      Key4 k;
+      Value4 v;
+      auto load = [&](const Tile& u, int page) {
+        k = {};
+        v = {};
+        const int place = u.key0 + (t & ~15), left = u.end - place;
+        if (u.n == 0 || left <= 0) return;
+        if (page < 0 || page >= p.c.n_pages) {
+          bad |= PALU_DEVERR_PAGE;
+          page = 0;
         }
-        return k;
-      };
-      auto load_values = [&](const uint8_t* b, int left) {
-        Value4 v = {};
-        if (b) {
+        const uint8_t* b = page4(p.c, page, u.kh) + (place & (p.c.page - 1)) / 16 * kBlock4;
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            v.codes[g] = __ldg(reinterpret_cast<const uint2*>(b + kValueCodes4 + 512 * half + 64 * g + 16 * c + 8 * pair));
+        for (int i = 0; i < 4; ++i) k.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + 64 * row) + i);
+        k.sz = __ldg(reinterpret_cast<const uint4*>(b + kKeyScales4 + 16 * row));
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint8_t* sz = b + kValueScales4 + 32 * c + 16 * e + 4 * (2 * half + pair);
-            // what lies behind the last key is 0: 0 * NaN is NaN
-            const uint32_t keep = (2 * c + 8 * e < left ? 0xffffu : 0u) | (2 * c + 8 * e + 1 < left ? 0xffff0000u : 0u);
-            v.s[e] = __ldg(reinterpret_cast<const uint32_t*>(sz)) & keep;
-            v.z[e] = __ldg(reinterpret_cast<const uint32_t*>(sz + 128)) & keep;
-          }
+        for (int g = 0; g < 8; ++g)
+          v.codes[g] = __ldg(reinterpret_cast<const uint2*>(b + kValueCodes4 + 512 * half + 64 * g + 16 * c + 8 * pair));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint8_t* sz = b + kValueScales4 + 32 * c + 16 * e + 4 * (2 * half + pair);
+          // what lies behind the last key is 0: 0 * NaN is NaN
+          const uint32_t keep = (2 * c + 8 * e < left ? 0xffffu : 0u) | (2 * c + 8 * e + 1 < left ? 0xffff0000u : 0u);
+          v.s[e] = __ldg(reinterpret_cast<const uint32_t*>(sz)) & keep;
+          v.z[e] = __ldg(reinterpret_cast<const uint32_t*>(sz + 128)) & keep;
         }
-        return v;
       };
-      int item = 0;
-      // room for the next tile of the ring; then it is told
-      auto room = [&] {
-        if (item >= kRing) wait_or_fail(&sh.kv_empty[item % kRing], (item / kRing - 1) & 1, &sh.failed, err);
-        __syncwarp();
-        return !__any_sync(0xffffffffu, failed());
-      };
-      auto done = [&] {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.kv_full[item % kFull]);
-        ++item;
+      auto step = [&](Tile u) {  // the tile behind it
+        u.key0 += kKeyTile;
+        return --u.n ? u : next_unit();
       };
       Tile u = next_unit();
-      int left = 0;
-      const uint8_t* b = u.n ? block_of(u, &left) : nullptr;
-      Key4 k = load_keys(b);
-      Value4 v = load_values(b, left);
-      while (u.n) {
-        // the tile behind this one
-        u.key0 += kKeyTile;
-        if (--u.n == 0) u = next_unit();
-        b = u.n ? block_of(u, &left) : nullptr;
-        if (!(ok = room())) break;
-        store_keys(smem_addr(ring + item % kRing * kTileBytes), t, k);
-        done();
-        k = load_keys(b);
-        if (!(ok = room())) break;
-        store_values(smem_addr(ring + item % kRing * kTileBytes), t & ~15, half, c, pair, v);
-        done();
-        v = load_values(b, left);
+      load(u, lookup(u));
+      Tile u1 = u.n ? step(u) : u;
+      int page = lookup(u1);
+      for (int item = 0; u.n; item += 2) {
+        // room for both of the tile's items in the ring
+        const int i0 = item % kRing, i1 = (item + 1) % kRing;
+        if (item >= kRing) wait_or_fail(&sh.kv_empty[i0], (item / kRing - 1) & 1, &sh.failed, err);
+        if (item + 1 >= kRing) wait_or_fail(&sh.kv_empty[i1], ((item + 1) / kRing - 1) & 1, &sh.failed, err);
+        __syncwarp();
+        if (__any_sync(0xffffffffu, failed())) break;
+        store_keys(smem_addr(ring + i0 * kTileBytes), t, k);
+        store_values(smem_addr(ring + i1 * kTileBytes), t & ~15, half, c, pair, v);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane < 2) mbar_arrive(&sh.kv_full[(item + lane) % kFull]);
+        u = u1;
+        load(u, page);
+        if (u.n) {
+          u1 = step(u);
+          page = lookup(u1);
+        }
       }
       if (bad) atomicOr(err, bad);
     }
