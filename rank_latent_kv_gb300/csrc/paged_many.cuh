@@ -63,8 +63,10 @@ struct ManySmem {
 };
 constexpr int kManySmemBytes = 1024 + (2 + kRing) * kTileBytes + (int)sizeof(ManySmem);
 static_assert(kManySmemBytes + sizeof(PlanScratch) <= 232448, "shared memory of a many-rows CTA");
-// Over pages of 4-bit codes: four warps more, which turn codes into the ring's tiles.
-constexpr int kMany4Threads = kManyThreads + 128;
+// Over pages of 4-bit codes: warps 12 to 15 turn codes into the ring's tiles of keys, 16 to 19 into those of values.
+// The registers of a thread: 96 at launch, then 128 in the softmax, 64 in warps 8 to 11 and 80 in the others, 480 for
+// five threads in either case.
+constexpr int kMany4Threads = 640;
 struct Many4Smem : ManySmem {
   float factor[kManyRows];  // of each row: from the products back to log2
 };
@@ -223,6 +225,7 @@ struct Key4 {
 struct Value4 {
   uint2 codes[8];
   uint32_t s[2], z[2];
+  int left;  // tokens that the block has
 };
 __device__ __forceinline__ uint32_t same_f16x2(uint32_t v, int high) { return __byte_perm(v, 0, high ? 0x3232 : 0x1010); }
 // z + s c of two codes that are 1024 + c, or 1024 + 16 c, in fp16
@@ -260,7 +263,10 @@ __device__ __forceinline__ void store_values(uint32_t tile, int row0, int half, 
 #pragma unroll
     for (int step = 0; step < 2; ++step) {
       const int odd = step ^ pair, row = row0 + 2 * c + odd + 8 * e;
-      const uint32_t s = same_f16x2(v.s[e], odd), z = same_f16x2(v.z[e], odd), b = 2 * odd + e, sel = b | (b + 4) << 8;
+      // what lies behind the last key is 0: 0 * NaN is NaN
+      const bool there = 2 * c + odd + 8 * e < v.left;
+      const uint32_t s = there ? same_f16x2(v.s[e], odd) : 0u, z = there ? same_f16x2(v.z[e], odd) : 0u;
+      const uint32_t b = 2 * odd + e, sel = b | (b + 4) << 8;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         uint32_t lo[4], hi[4];
@@ -281,7 +287,7 @@ __device__ __forceinline__ void store_values(uint32_t tile, int row0, int half, 
 // The CTA's stretch, by all kManyThreads (FOUR: kMany4Threads, or more) threads;
 // `start` is run by warps 8 and up before the others may need the plan (they
 // would only wait for the same code to arrive).
-// FOUR: the pages hold 4-bit codes.  Warp 8 only plans; four warps fetch the
+// FOUR: the pages hold 4-bit codes.  Warp 8 only plans; eight warps fetch the
 // codes into registers, a tile ahead, and write fp16 tiles into the ring.  All
 // products are in fp16 then, also in a bf16 cache: the queries are brought into
 // its range by a power of two a row, which comes off again with the scores'
@@ -301,7 +307,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.meta_full[i], 1);
-      mbar_init(&sh.meta_empty[i], FOUR ? 14 : 10);  // eight softmax warps, two product warps, those of the tiles
+      mbar_init(&sh.meta_empty[i], FOUR ? 18 : 10);  // eight softmax warps, two product warps, those of the tiles
       mbar_init(&sh.drain[i], 1);
       mbar_init(&sh.token[i], 1);
       mbar_init(&sh.s_full[i], 1);
@@ -323,8 +329,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
   if (warp >= 8) start();
   auto failed = [&] { return *(volatile int*)&sh.failed != 0; };
 
-  if (warp == 8) {
-    // ---- loads
+  auto loads = [&] {  // ---- warp 8
     unsigned bad = 0;
     int item = 0, units = 0;  // ring items (a K or a V tile each) and units so far
     auto publish = [&](const UnitMeta& u) -> bool {
@@ -381,11 +386,12 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
     // no copy is in flight when the block ends, also where the others gave up
     for (int i = max(item - kRing, 0); i < item; ++i)
       if (!mbar_wait_bounded(&sh.kv_full[i % kFull], (i / kFull) & 1)) break;
-  } else if (FOUR && warp > 10) {
-    // ---- tiles from codes, by warps 11 to 14
-    if (warp < 15) {
-      const int t = tid - 11 * 32, row = t & 15;                            // one token of block t / 16
-      const int half = row >> 3, c = row >> 1 & 3, pair = row & 1;          // and this part of its values
+  };
+  auto tiles = [&] {  // ---- tiles from codes
+    if constexpr (FOUR) {
+      const bool values = warp >= 16;
+      const int t = tid & 127, row = t & 15;                                // one token of block t / 16
+      const int half = row >> 3, c = row >> 1 & 3, pair = row & 1;          // or this part of its values
       unsigned bad = 0;
       struct Tile {
         int seq, kh, key0, end, n;  // the unit's; n: tiles left, 0: none
@@ -403,69 +409,79 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         ++units;
         return u;
       };
-      // The thread's block of a tile is looked up one tile before it is loaded, and loaded one tile before it is written.
-      auto lookup = [&](const Tile& u) {  // the page's number, or -1 behind the last key
-        const int place = u.key0 + (t & ~15);
-        return u.n && place < u.end ? __ldg(p.c.table + (long long)u.seq * p.c.width + (place >> p.c.page_shift)) : -1;
-      };
-      Key4 k;
-      Value4 v;
-      auto load = [&](const Tile& u, int page) {
-        k = {};
-        v = {};
-        const int place = u.key0 + (t & ~15), left = u.end - place;
-        if (u.n == 0 || left <= 0) return;
-        if (page < 0 || page >= p.c.n_pages) {
-          bad |= PALU_DEVERR_PAGE;
-          page = 0;
-        }
-        const uint8_t* b = page4(p.c, page, u.kh) + (place & (p.c.page - 1)) / 16 * kBlock4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + 64 * row) + i);
-        k.sz = __ldg(reinterpret_cast<const uint4*>(b + kKeyScales4 + 16 * row));
-#pragma unroll
-        for (int g = 0; g < 8; ++g)
-          v.codes[g] = __ldg(reinterpret_cast<const uint2*>(b + kValueCodes4 + 512 * half + 64 * g + 16 * c + 8 * pair));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint8_t* sz = b + kValueScales4 + 32 * c + 16 * e + 4 * (2 * half + pair);
-          // what lies behind the last key is 0: 0 * NaN is NaN
-          const uint32_t keep = (2 * c + 8 * e < left ? 0xffffu : 0u) | (2 * c + 8 * e + 1 < left ? 0xffff0000u : 0u);
-          v.s[e] = __ldg(reinterpret_cast<const uint32_t*>(sz)) & keep;
-          v.z[e] = __ldg(reinterpret_cast<const uint32_t*>(sz + 128)) & keep;
-        }
-      };
       auto step = [&](Tile u) {  // the tile behind it
         u.key0 += kKeyTile;
         return --u.n ? u : next_unit();
       };
-      Tile u = next_unit();
-      load(u, lookup(u));
-      Tile u1 = u.n ? step(u) : u;
-      int page = lookup(u1);
-      for (int item = 0; u.n; item += 2) {
-        // room for both of the tile's items in the ring
-        const int i0 = item % kRing, i1 = (item + 1) % kRing;
-        if (item >= kRing) wait_or_fail(&sh.kv_empty[i0], (item / kRing - 1) & 1, &sh.failed, err);
-        if (item + 1 >= kRing) wait_or_fail(&sh.kv_empty[i1], ((item + 1) / kRing - 1) & 1, &sh.failed, err);
-        __syncwarp();
-        if (__any_sync(0xffffffffu, failed())) break;
-        store_keys(smem_addr(ring + i0 * kTileBytes), t, k);
-        store_values(smem_addr(ring + i1 * kTileBytes), t & ~15, half, c, pair, v);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane < 2) mbar_arrive(&sh.kv_full[(item + lane) % kFull]);
-        u = u1;
-        load(u, page);
-        if (u.n) {
-          u1 = step(u);
-          page = lookup(u1);
+      // The thread's block of a tile is looked up one tile before it is loaded, and loaded one tile before it is written.
+      // No branch around the loads, which would wait for them: behind the last key its page is read, and not used.
+      auto lookup = [&](const Tile& u) {
+        const int place = max(min(u.key0 + (t & ~15), u.end - 1), 0);
+        return __ldg(p.c.table + (long long)u.seq * p.c.width + (place >> p.c.page_shift));
+      };
+      auto block_of = [&](const Tile& u, int page) -> const uint8_t* {
+        const int place = u.key0 + (t & ~15);
+        if (page < 0 || page >= p.c.n_pages) {
+          if (place < u.end) bad |= PALU_DEVERR_PAGE;
+          page = 0;
         }
+        return page4(p.c, page, u.kh) + (place & (p.c.page - 1)) / 16 * kBlock4;
+      };
+      // load(u, page), then store(tile of the ring): items `kv`, `kv` + 2, ...
+      auto run = [&](int kv, auto&& load, auto&& store) {
+        Tile u = next_unit();
+        load(u, block_of(u, lookup(u)));
+        Tile u1 = u.n ? step(u) : u;
+        int page = lookup(u1);
+        for (int item = kv; u.n; item += 2) {
+          const int slot = item % kRing;
+          if (item >= kRing) wait_or_fail(&sh.kv_empty[slot], (item / kRing - 1) & 1, &sh.failed, err);
+          __syncwarp();
+          if (__any_sync(0xffffffffu, failed())) break;
+          store(smem_addr(ring + slot * kTileBytes));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kv_full[item % kFull]);
+          u = u1;
+          load(u, block_of(u, page));
+          if (u.n) {
+            u1 = step(u);
+            page = lookup(u1);
+          }
+        }
+      };
+      if (!values) {
+        Key4 k;
+        run(
+            0,
+            [&](const Tile&, const uint8_t* b) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) k.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + 64 * row) + i);
+              k.sz = __ldg(reinterpret_cast<const uint4*>(b + kKeyScales4 + 16 * row));
+            },
+            [&](uint32_t tile) { store_keys(tile, t, k); });
+      } else {
+        Value4 v;
+        run(
+            1,
+            [&](const Tile& u, const uint8_t* b) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g)
+                v.codes[g] = __ldg(reinterpret_cast<const uint2*>(b + kValueCodes4 + 512 * half + 64 * g + 16 * c + 8 * pair));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint8_t* sz = b + kValueScales4 + 32 * c + 16 * e + 4 * (2 * half + pair);
+                v.s[e] = __ldg(reinterpret_cast<const uint32_t*>(sz));
+                v.z[e] = __ldg(reinterpret_cast<const uint32_t*>(sz + 128));
+              }
+              v.left = u.end - u.key0 - (t & ~15);
+            },
+            [&](uint32_t tile) { store_values(tile, t & ~15, half, c, pair, v); });
       }
       if (bad) atomicOr(err, bad);
     }
-  } else if (warp >= 9) {
-    // ---- products of half s
+  };
+  auto products = [&] {  // ---- of half s, warps 9 and 10
     const int s = warp - 9;
     const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
     constexpr uint32_t idesc_s = instr_desc<MB>(false), idesc_o = instr_desc<MB>(true);
@@ -570,8 +586,8 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
     // every product has ended before TMEM is given back
     commit(&sh.drain[s]);
     mbar_wait_bounded(&sh.drain[s], 0);
-  } else if (warp < 8) {
-    // ---- softmax: half `s`, a row a thread
+  };
+  auto softmax = [&] {  // ---- half `s`, a row a thread
     const int s = warp >> 2, t = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of TMEM
     const uint32_t s_addr = tmem + lanes + s * 128, o_addr = tmem + lanes + 256 + s * 128;
@@ -633,6 +649,8 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       }
       const int r = (both ? s * kHalf : 0) + t;  // row of the unit
       const bool live = r < m.rows;
+      // A warp without a row has nothing to weigh; what its lanes of TMEM hold stays in rows that nothing reads.
+      const bool idle = FOUR && (r & ~31) >= m.rows;
       const int lim = live ? unit_row_limit(p, plan, m, r) : 0x7fffffff;
       float ref = 0.f, l = 0.f;  // the weights' reference (log2), their sum
       bool seen = false;         // whether there is a reference yet
@@ -653,6 +671,12 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         wait_or_fail(&sh.s_full[s], sc & 1, &sh.failed, err);
         __syncwarp();
         tc_fence_after();
+        if (idle) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane < 2) mbar_arrive(&sh.p_full[s][lane]);
+          continue;
+        }
         const float scale = FOUR ? static_cast<const Many4Smem&>(sh).factor[r] : p.scale_log2;
         // The scores pass twice, 64 at a time, for the maximum and for the weights (a thread with all 128 spills).  Both
         // loops are kept rolled: a launch has to fetch its code, and the softmax has time to spare.
@@ -833,6 +857,28 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.meta_empty[unit & 1]);
     }
+  };
+  if constexpr (FOUR) {
+    // by whole warpgroups
+    if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+      softmax();
+    } else if (warp < 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      if (warp == 8)
+        loads();
+      else if (warp < 11)
+        products();
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      tiles();
+    }
+  } else if (warp == 8) {
+    loads();
+  } else if (warp > 8) {
+    products();
+  } else {
+    softmax();
   }
   tc_fence_before();
   __syncthreads();
