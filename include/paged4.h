@@ -28,8 +28,9 @@ extern "C" {
 #endif
 
 /* What is held of 32 channels x of one token and KV head, in fp32 without
- * fused operations, ties to even:
- *   z = fp16(min x), s = fp16((max x - min x) / 15), both cut to +-65504,
+ * fused operations, ties to even, with min x and max x cut to +-65504:
+ *   z = fp16(min x), s = fp16((max x - min x) / 15), the next smaller number
+ *   where z + 15 s would pass 65504,
  *   c = min(max(rint((x - z) / s), 0), 15), or 0 where s is 0,
  * and reads back as z + s c.  Channels of which one is not finite all read
  * back as NaN.

@@ -16,9 +16,10 @@ def quantise(x):
     y = x.reshape(*x.shape[:-1], 4, G)
     with np.errstate(all="ignore"):
         fine = np.isfinite(y).all(-1)
-        lo, hi = np.where(fine, y.min(-1), 0), np.where(fine, y.max(-1), 0)
-        s = np.minimum((hi - lo).astype(np.float32) / np.float32(15), np.float32(65504)).astype(np.float16)
-        z = np.clip(lo, -65504, 65504).astype(np.float16)
+        lo, hi = (np.clip(np.where(fine, f(-1), 0), -65504, 65504).astype(np.float32) for f in (y.min, y.max))
+        s = ((hi - lo) / np.float32(15)).astype(np.float16)
+        z = lo.astype(np.float16)
+        s = np.where(z.astype(np.float64) + 15 * s.astype(np.float64) > 65504, np.nextafter(s, np.float16(0)), s)
         sf, zf = s.astype(np.float32)[..., None], z.astype(np.float32)[..., None]
         c = np.rint((y - zf) / np.where(sf > 0, sf, np.float32(1)))
         c = np.where((sf > 0) & fine[..., None], np.clip(np.nan_to_num(c), 0, 15), 0)

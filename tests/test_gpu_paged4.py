@@ -219,6 +219,10 @@ def test_values_of_every_kind(P, dt):
     x[8, 1, 40] = -math.inf
     x[8, 2, 100] = math.nan
     x[9] = torch.linspace(-1, 1, D)
+    x[12] = torch.linspace(-65504, 65504, D)
+    x[13] = torch.linspace(60000, 65504, D)
+    x[14] = torch.arange(D) % 31 * 0.5 - 7.5                      # z = -7.5 s: every second value on a border
+    x[15] = x[14] * (1 + 2.0 ** -9)
     if dt == torch.bfloat16:
         x[10] *= 1e7                                              # scales and zeros that fp16 does not have
         x[11] *= 2e38

@@ -52,3 +52,12 @@ def test_write_and_read_back():
     for t in rng.permutation(16):
         O4.write(block, t, k[t], v[t])
     assert np.array_equal(O4.rows(block, False), O4.held(k)) and np.array_equal(O4.rows(block, True), O4.held(v))
+
+
+def test_what_is_held_is_finite_in_fp16():
+    x = np.zeros(O4.D, np.float32)
+    x[:32] = np.linspace(-65504, 65504, 32)
+    x[32:64] = np.linspace(65000, 65504, 32)
+    x[64:96] = np.linspace(-3e38, 1e38, 32)                       # bf16's range: cut
+    c, s, z = O4.quantise(x)
+    assert (O4.held(x) <= 65504).all() and s[0] == np.float16(8728) and z[2] == -65504 and c[95] == 15
