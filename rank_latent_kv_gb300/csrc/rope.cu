@@ -93,8 +93,13 @@ extern "C" palu_status palu_rope_table(const palu_rope_scaling* scaling, int64_t
   RopeParams p = {};
   const double two_pi = 6.283185307179586476925286766559;
   const double base = s.kind == PALU_ROPE_NTK ? s.base * pow(s.factor, (double)d / (d - 2)) : s.base;
+  // base^(-2i/d) from the powers 1, 2, 4 .. 32 of its first: 64 calls of pow take longer than the launch
+  double bit[6];
+  for (int b = 0; b < 6; ++b) bit[b] = pow(base, -2.0 * (1 << b) / d);
   for (int i = 0; i < d / 2; ++i) {
-    double f = pow(base, -2.0 * i / d);
+    double f = 1.0;
+    for (int b = 0; b < 6; ++b)
+      if (i >> b & 1) f *= bit[b];
     if (s.kind == PALU_ROPE_LINEAR) f /= s.factor;
     if (s.kind == PALU_ROPE_PARTS) {
       const double r = s.original * f / two_pi, t = fmin(fmax((r - s.low_turns) / (s.high_turns - s.low_turns), 0.0), 1.0);

@@ -178,7 +178,7 @@ _SIGNATURES = {
                                       c_void_p, c_void_p, c_void_p]),
     "palu_page_plan": (c_int32, [c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
     "palu_page_pool_sync": (c_int32, [c_void_p, _P(c_uint32), c_void_p]),
-    "palu_rope_table": (c_int32, [_P(palu_rope_scaling), c_int64, c_int64, c_void_p, c_void_p]),
+    "palu_rope_table": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
     "palu_draft_verify": (c_int32, [c_int64, c_int32, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
 }
@@ -518,6 +518,7 @@ _TYPES = {torch.float16: PALU_TYPE_F16, torch.bfloat16: PALU_TYPE_BF16}
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _pack2, _pack3 = struct.Struct("2q").pack, struct.Struct("3q").pack
 _pack_transform = struct.Struct("PPPqiifi").pack    # palu_qk_transform
+_pack_rope = struct.Struct("ii6d").pack             # palu_rope_scaling
 
 
 # These calls take a few microseconds on the GPU, so their checks are written for the case that all is well: one
@@ -680,7 +681,9 @@ class _Paged:
             qp, qs = _rows(q, "q", (n, hq, D), dt, dev)
             if q_out is None:
                 q_out = _empty((n, hq, D), dt, self.device, stream)
-            out = _at(q_out, "q_out", (n, hq, D), dt, dev)
+                out = q_out.data_ptr()
+            else:
+                out = _at(q_out, "q_out", (n, hq, D), dt, dev)
         elif q_out is not None:
             raise ValueError("q_out is given without q")
         if n:
@@ -705,7 +708,9 @@ class _Paged:
         op = _at(offsets, "offsets", self._offsets, _I32, dev)
         if out is None:
             out = _empty(shape, self.dtype, self.device, stream)
-        to = _at(out, "out", shape, self.dtype, dev)
+            to = out.data_ptr()
+        else:
+            to = _at(out, "out", shape, self.dtype, dev)
         if n == 0:
             return out
         if workspace is None:
@@ -713,7 +718,7 @@ class _Paged:
         size = workspace.numel()
         ws = _at(workspace, "workspace", (size,), torch.uint8, dev)
         _check(self._attn(self._c, n, op, max_new, hq, qp, qs, shared_pages, softmax_scale, to, ws, size,
-                                     _raw_stream(stream, dev)))
+                          _raw_stream(stream, dev)))
         return out
 
     def sync(self, stream=None):
@@ -830,6 +835,7 @@ class PagePool:
                                          _at(free_pages, "free_pages", (n,), _I32, dev),
                                          _at(n_free, "n_free", (1,), _I32, dev), self.error.data_ptr()))
         self._c = ctypes.addressof(self.c)
+        self._offsets, self._none = (self.batch + 1,), torch.empty(0, dtype=_I64, device=self.device)
 
     def plan(self, new_tokens, tokens, shared_pages=0, offsets=None, positions=None, slots=None, stream=None):
         """One step: sequence b brings new_tokens[b] (int32 [B]) tokens.  Lengths grow by them, pages behind the new lengths
@@ -841,12 +847,15 @@ class PagePool:
         dev = self._dev
         np_ = _at(new_tokens, "new_tokens", (self.batch,), _I32, dev)
         if offsets is None:
-            offsets = _empty((self.batch + 1,), _I32, self.device, stream)
+            offsets = _empty(self._offsets, _I32, self.device, stream)
+            op = offsets.data_ptr()
+        else:
+            op = _at(offsets, "offsets", self._offsets, _I32, dev)
+        # an allocation costs as much as the launch: none for no rows
         if positions is None:
-            positions = _empty((tokens,), _I64, self.device, stream)
+            positions = _empty((tokens,), _I64, self.device, stream) if tokens else self._none
         if slots is None:
-            slots = _empty((tokens,), _I64, self.device, stream)
-        op = _at(offsets, "offsets", (self.batch + 1,), _I32, dev)
+            slots = _empty((tokens,), _I64, self.device, stream) if tokens else self._none
         pp, sp = _at(positions, "positions", (tokens,), _I64, dev), _at(slots, "slots", (tokens,), _I64, dev)
         _check(lib().palu_page_plan(self._c, np_, tokens, shared_pages, op, pp, sp, _raw_stream(stream, dev)))
         return offsets, positions, slots
@@ -868,15 +877,18 @@ def rope_table(positions, rope_dim, base=10000.0, scaling="plain", factor=1.0, o
         raise ValueError(f"scaling is {scaling!r}; expected one of {', '.join(PALU_ROPE_KINDS)}")
     if magnitude is None:
         magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "parts" and factor > 0 else 1.0
-    cur = torch.cuda.current_device()
+    dev = torch.cuda.current_device()
     if out is None:
-        where = torch.device("cuda", cur) if device is None else torch.device(device)
-        if where.type != "cuda" or where.index not in (None, cur):
-            raise ValueError(f"{where} is not the current device")
-        out = _empty((positions, rope_dim), _F32, torch.device("cuda", cur), stream)
-    to = _at(out, "out", (positions, rope_dim), _F32, _here(out, "out"))
-    s = palu_rope_scaling(PALU_ROPE_KINDS[scaling], rope_dim, base, factor, original, low_turns, high_turns, magnitude)
-    _check(lib().palu_rope_table(ctypes.byref(s), start, positions, to, _raw_stream(stream, cur)))
+        if device is not None:
+            where = torch.device(device)
+            if where.type != "cuda" or where.index not in (None, dev):
+                raise ValueError(f"{where} is not the current device")
+        out = _empty((positions, rope_dim), _F32, dev, stream)
+        to = out.data_ptr()
+    else:
+        to = _at(out, "out", (positions, rope_dim), _F32, _here(out, "out"))
+    s = _pack_rope(PALU_ROPE_KINDS[scaling], rope_dim, base, factor, original, low_turns, high_turns, magnitude)
+    _check(lib().palu_rope_table(s, start, positions, to, _raw_stream(stream, dev)))
     return out
 
 

@@ -41,6 +41,9 @@ int main(void) {
     c, p, r = palu.palu_paged4_cache, palu.palu_page_pool, palu.palu_rope_scaling
     assert vals[:10] == [ctypes.sizeof(c), c.strides.offset, c.error.offset, ctypes.sizeof(p), p.page_table.offset, p.error.offset,
                          ctypes.sizeof(r), r.base.offset, r.magnitude.offset, palu.PALU_PAGED4_BLOCK]
+    packed = palu._pack_rope(1, 2, 3.0, 4.0, 5.0, 6.0, 7.0, 8.0)
+    x = r.from_buffer_copy(packed)
+    assert len(packed) == ctypes.sizeof(r) and (x.kind, x.rope_dim, x.base, x.magnitude) == (1, 2, 3.0, 8.0)
     assert vals[10:] == [palu.PALU_ROPE_KINDS[k] for k in ("plain", "linear", "ntk", "parts")]
 
 
