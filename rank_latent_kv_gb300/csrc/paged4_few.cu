@@ -12,7 +12,10 @@ __global__ void __launch_bounds__(kFew4Threads<NT>, 1) paged4_few_kernel(const A
   grid_dep_launch();
   if (threadIdx.x == 0) few4_init<NT>(few4_shared<NT>(smem));
   plan_start<8 * NT, 8 * NT, kFew4Threads<NT>, true>(p, &plan, threadIdx.x);  // all threads meet in it
-  few4_stretch<BF16, NT, false>(p, p.part, plan, smem);
+  if (threadIdx.x < 32 * kFew4Warps<NT>)
+    few4_work<BF16, NT>(p, p.part, plan, smem);
+  else
+    few4_load<NT, false>(p, p.part, plan, smem);
 }
 
 template <bool BF16, int NT>

@@ -184,71 +184,76 @@ __device__ __forceinline__ void few4_queries(const AttnParams& p, const uint16_t
   *factor = query_factor(e, p.scale_log2 * 0x1p24f);
 }
 
-// The stretch, by kFew4Threads<NT> threads.  NT: n8 tiles of rows (8 or 16 rows a
+// The stretch, by kFew4Threads<NT> threads: few4_work by the first kFew4Warps<NT>
+// warps, few4_load by the one behind them.  NT: n8 tiles of rows (8 or 16 rows a
 // unit).
-template <bool BF16, int NT, bool SPLIT>
-__device__ __forceinline__ void few4_stretch(const AttnParams& p, const PartSet& part, const PlanScratch& plan, uint8_t* smem) {
+template <int NT, bool SPLIT>
+__device__ __forceinline__ void few4_load(const AttnParams& p, const PartSet& part, const PlanScratch& plan, uint8_t* smem) {
+  constexpr int R = 8 * NT, kBlocks = kFew4Blocks<NT>, kStage = kFew4StageBytes<NT>;
+  Few4Smem& sh = few4_shared<NT>(smem);
+  const int lane = threadIdx.x & 31;
+  if (plan.w1 <= plan.w0) return;
+  unsigned bad = 0;
+  int it = 0;
+  // room for the next stage: all lanes go on or stop together
+  auto room = [&] {
+    if (it >= kFew4Stages)
+      wait_or_fail(&sh.empty[it % kFew4Stages], ((it / kFew4Stages) - 1) & 1, &sh.failed, p.c.error);
+    return !__any_sync(0xffffffffu, *(volatile int*)&sh.failed);
+  };
+  plan_walk<R, SPLIT, true>(p, part, &plan, [&](const UnitMeta& u) -> bool {
+    if (lane < u.rows) {  // the unit's queries, to L2 while the tiles before it are worked on
+      const uint16_t* q = row_query(p, u, lane);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+    }
+    const int end = min(u.key0 + u.n * kKeyTile, u.key_end), per = p.c.page >> 4;
+    // a stage's pages, one a lane: the blocks of each that it has
+    struct Piece {
+      int page, from, first, n;  // from: block of the page; first: block of the stage
+    };
+    auto lookup = [&](int key0) {
+      const int b0 = key0 >> 4, b1 = min(b0 + kBlocks, (end + 15) >> 4), pi = (key0 >> p.c.page_shift) + lane;
+      const int lo = max(b0, pi * per), hi = min(b1, (pi + 1) * per);
+      Piece x = {0, lo - pi * per, lo - b0, hi - lo};
+      if (x.n > 0) x.page = page_of(p, u.seq, lo << 4, &bad);
+      return x;
+    };
+    Piece next = lookup(u.key0);
+    for (int key0 = u.key0; key0 < end; key0 += 16 * kBlocks, ++it) {
+      const int st = it % kFew4Stages, valid = min(16 * kBlocks, end - key0);
+      const Piece x = next;
+      next = lookup(key0 + 16 * kBlocks);  // in flight while this stage waits for room
+      if (!room()) return false;
+      if (lane == 0) {
+        sh.meta[st] = Stage4Meta{key0, valid, key0 == u.key0, key0 + valid == end, u};
+        mbar_arrive_expect_tx(&sh.full[st], ((valid + 15) >> 4) * kBlock4);
+      }
+      __syncwarp();
+      if (x.n > 0)
+        bulk_g2s(smem + st * kStage + x.first * kBlock4, page4(p.c, x.page, u.kh) + x.from * kBlock4, x.n * kBlock4, &sh.full[st]);
+    }
+    return true;
+  });
+  const bool ended = room();
+  if (ended && lane == 0) {  // a stage of no keys ends the line
+    sh.meta[it % kFew4Stages].valid = 0;
+    mbar_arrive(&sh.full[it % kFew4Stages]);
+  }
+  if (bad) atomicOr(p.c.error, bad);
+  // no copy is in flight when the block ends, also where the others gave up (the stage that the end took had
+  // been emptied)
+  for (int k = max(it - kFew4Stages + (ended ? 1 : 0), 0); k < it; ++k)
+    if (!mbar_wait_bounded(&sh.full[k % kFew4Stages], (k / kFew4Stages) & 1)) break;
+}
+
+template <bool BF16, int NT>
+__device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& part, const PlanScratch& plan, uint8_t* smem) {
   constexpr int R = 8 * NT, kWarps = kFew4Warps<NT>, kBlocks = kFew4Blocks<NT>, kStage = kFew4StageBytes<NT>;
   float* merge = reinterpret_cast<float*>(smem + kFew4Stages * kStage);
   Few4Smem& sh = few4_shared<NT>(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (plan.w1 <= plan.w0) return;
-  if (warp == kWarps) {
-    // ---- the loading warp
-    unsigned bad = 0;
-    int it = 0;
-    // room for the next stage: all lanes go on or stop together
-    auto room = [&] {
-      if (it >= kFew4Stages)
-        wait_or_fail(&sh.empty[it % kFew4Stages], ((it / kFew4Stages) - 1) & 1, &sh.failed, p.c.error);
-      return !__any_sync(0xffffffffu, *(volatile int*)&sh.failed);
-    };
-    plan_walk<R, SPLIT, true>(p, part, &plan, [&](const UnitMeta& u) -> bool {
-      if (lane < u.rows) {  // the unit's queries, to L2 while the tiles before it are worked on
-        const uint16_t* q = row_query(p, u, lane);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
-      }
-      const int end = min(u.key0 + u.n * kKeyTile, u.key_end), per = p.c.page >> 4;
-      // a stage's pages, one a lane: the blocks of each that it has
-      struct Piece {
-        int page, from, first, n;  // from: block of the page; first: block of the stage
-      };
-      auto lookup = [&](int key0) {
-        const int b0 = key0 >> 4, b1 = min(b0 + kBlocks, (end + 15) >> 4), pi = (key0 >> p.c.page_shift) + lane;
-        const int lo = max(b0, pi * per), hi = min(b1, (pi + 1) * per);
-        Piece x = {0, lo - pi * per, lo - b0, hi - lo};
-        if (x.n > 0) x.page = page_of(p, u.seq, lo << 4, &bad);
-        return x;
-      };
-      Piece next = lookup(u.key0);
-      for (int key0 = u.key0; key0 < end; key0 += 16 * kBlocks, ++it) {
-        const int st = it % kFew4Stages, valid = min(16 * kBlocks, end - key0);
-        const Piece x = next;
-        next = lookup(key0 + 16 * kBlocks);  // in flight while this stage waits for room
-        if (!room()) return false;
-        if (lane == 0) {
-          sh.meta[st] = Stage4Meta{key0, valid, key0 == u.key0, key0 + valid == end, u};
-          mbar_arrive_expect_tx(&sh.full[st], ((valid + 15) >> 4) * kBlock4);
-        }
-        __syncwarp();
-        if (x.n > 0)
-          bulk_g2s(smem + st * kStage + x.first * kBlock4, page4(p.c, x.page, u.kh) + x.from * kBlock4, x.n * kBlock4, &sh.full[st]);
-      }
-      return true;
-    });
-    const bool ended = room();
-    if (ended && lane == 0) {  // a stage of no keys ends the line
-      sh.meta[it % kFew4Stages].valid = 0;
-      mbar_arrive(&sh.full[it % kFew4Stages]);
-    }
-    if (bad) atomicOr(p.c.error, bad);
-    // no copy is in flight when the block ends, also where the others gave up (the stage that the end took had
-    // been emptied)
-    for (int k = max(it - kFew4Stages + (ended ? 1 : 0), 0); k < it; ++k)
-      if (!mbar_wait_bounded(&sh.full[k % kFew4Stages], (k / kFew4Stages) & 1)) break;
-    return;
-  }
   // ---- block `warp` of each stage (and `warp` + 8)
   const int g = lane >> 2, c = lane & 3;
   float ref[NT][2], acc[NT][8][4], zacc[NT][4], factor[NT][2];

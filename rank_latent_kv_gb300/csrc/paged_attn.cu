@@ -335,7 +335,7 @@ static palu_status attn_layout(const palu_paged_cache* c, bool four, int64_t tok
   l->R_prefix = row_tile(all_rows);
   const int R_rows = row_tile(own_rows);
   // Otherwise one line: up to 16 rows in all go to the prefix's row tiles, and so do own units of more than 16.
-  l->both = l->shared && l->R_prefix == kManyRows && R_rows < kManyRows && device_sm_count() > 1 && !four;
+  l->both = l->shared && l->R_prefix == kManyRows && R_rows < kManyRows && device_sm_count() > 1;
   l->R_own = l->shared && !l->both ? l->R_prefix : R_rows;
   const size_t slots = 2 * (size_t)device_sm_count();
   size_t o = 0;
@@ -511,6 +511,6 @@ extern "C" palu_status palu_paged4_attn(const palu_paged4_cache* cache, int64_t 
   p.c = paged4_view(cache);
   const bool bf16 = cache->dtype == PALU_TYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((st = (l.R_own == kManyRows ? launch_many4 : launch_few4)(p, bf16, s)) != PALU_OK) return st;
+  if ((st = (l.both ? launch_both4 : l.R_own == kManyRows ? launch_many4 : launch_few4)(p, bf16, s)) != PALU_OK) return st;
   return bf16 ? launch_joins<true, true>(l, p, s) : launch_joins<false, true>(l, p, s);
 }

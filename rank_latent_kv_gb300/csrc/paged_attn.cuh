@@ -101,8 +101,8 @@ struct LineCost<kManyRows, false> {
 template <>
 struct LineCost<kManyRows, true> {
   static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 100 : 60; }
-  static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 16 : 12; }
-  static constexpr int kMaxTile = 16;
+  static __device__ int tile(int rows) { return rows > kManyRows / 2 ? 22 : 14; }
+  static constexpr int kMaxTile = 22;
   static constexpr float kClocks = 200.f;
 };
 // A tile of codes is 20 KB.
@@ -505,8 +505,9 @@ palu_status launch(K kernel, dim3 grid, int threads, int smem, bool dependent, c
 palu_status launch_few(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 palu_status launch_many(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
 palu_status launch_both(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, bool bf16, cudaStream_t stream);
-// Over pages of 4-bit codes (paged4_few.cu, paged4_many.cu).
+// Over pages of 4-bit codes (paged4_few.cu, paged4_many.cu, paged4_both.cu).
 palu_status launch_few4(const AttnParams& p, bool bf16, cudaStream_t stream);
 palu_status launch_many4(const AttnParams& p, bool bf16, cudaStream_t stream);
+palu_status launch_both4(const AttnParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace palu
