@@ -68,6 +68,7 @@ static_assert(kManySmemBytes + sizeof(PlanScratch) <= 232448, "shared memory of 
 // five threads in either case.
 constexpr int kMany4Threads = 640;
 struct Many4Smem : ManySmem {
+  uint64_t first_done[2];   // a half's product with the first 64 values of a tile
   float factor[kManyRows];  // of each row: from the products back to log2
 };
 constexpr int kMany4SmemBytes = 1024 + (2 + kRing) * kTileBytes + (int)sizeof(Many4Smem);
@@ -313,6 +314,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i][0], 4);
       mbar_init(&sh.p_full[i][1], 4);
+      if constexpr (FOUR) mbar_init(&static_cast<Many4Smem&>(sh).first_done[i], 1);
     }
     mbar_init(&sh.q_full, 8);
     mbar_init(&sh.unit_done, 2);
@@ -553,7 +555,10 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         ok = wait_all(2, lane ? &sh.kv_full[vi % kFull] : &sh.p_full[s][0], lane ? (vi / kFull) & 1 : pc & 1);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) values(0, t, j >= step);
+        if (elect_one()) {
+          values(0, t, j >= step);
+          if constexpr (FOUR) tc_commit(&static_cast<Many4Smem&>(sh).first_done[s]);
+        }
         __syncwarp();
         // The halves take turns with their last values and next scores: left to themselves they fall into step, both in
         // the softmax and then both waiting for the tensor cores (3,900 clocks a tile pair).
@@ -695,26 +700,19 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
             for (int i = 0; i < 64; ++i) f[i] = i < n ? f[i] : -INFINITY;
           }
         };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          load(u);
-#pragma unroll
-          for (int i = 0; i < 64; i += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
-        }
-        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale;
-        // raise the maximum?  O of this half is complete up to the tile before: its product was issued before these scores
-        float alpha = 1.f;
         constexpr float kLift = MB ? 0.f : 6.f;
-        if (top > ref + (kLift + kRaise) || (!seen && top != -INFINITY)) {
-          alpha = seen ? ex2f_(ref - (top - kLift)) : 1.f;  // nothing but zeros so far: no factor
-          ref = top - kLift;
-          seen = true;
-          l *= alpha;
-        }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        // The row's reference for a maximum of `top`, and the factor of what was summed under the one before.
+        auto raise = [&](float top) {
+          float alpha = 1.f;
+          if (top > ref + (kLift + kRaise) || (!seen && top != -INFINITY)) {
+            alpha = seen ? ex2f_(ref - (top - kLift)) : 1.f;  // nothing but zeros so far: no factor
+            ref = top - kLift;
+            seen = true;
+            l *= alpha;
+          }
+          return alpha;
+        };
+        auto rescale = [&](float alpha) {
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             uint32_t o[16];
@@ -724,11 +722,15 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
             for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
             tc_st16(o_addr + 16 * i, o);
           }
-        }
+        };
+        auto maximum = [&](float* mx) {  // of the 64 scores in hand, to four
+#pragma unroll
+          for (int i = 0; i < 64; i += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], f[i + q], f[i + 4 + q]);
+        };
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          load(u);
+        auto weigh = [&](int u) {  // the 64 scores in hand
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -744,6 +746,44 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.p_full[s][u]);
+        };
+        if constexpr (FOUR) {
+          // Each 64 scores pass once: a reference that has to be raised in the tile's second half, which is rare, waits
+          // for the product with the first half's weights and rescales that too.  (Twice, as below: 3,000 clocks a
+          // tile and warp.)
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            load(u);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            maximum(mx);
+            const float alpha = raise(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale);
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+              if (u) {
+                wait_or_fail(&static_cast<Many4Smem&>(sh).first_done[s], sc & 1, &sh.failed, err);
+                __syncwarp();
+                tc_fence_after();
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) sum[q] *= alpha;
+              rescale(alpha);
+            }
+            weigh(u);
+          }
+        } else {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            load(u);
+            maximum(mx);
+          }
+          // raise the maximum?  O of this half is complete up to the tile before: its product was issued before these scores
+          const float alpha = raise(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale);
+          if (__any_sync(0xffffffffu, alpha != 1.f)) rescale(alpha);
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            load(u);
+            weigh(u);
+          }
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
