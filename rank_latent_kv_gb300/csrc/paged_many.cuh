@@ -228,6 +228,18 @@ struct Value4 {
   uint32_t s[2], z[2];
   int left;  // tokens that the block has
 };
+// Loaded registers pass through here where their use begins: nothing that waits for them moves in front.
+__device__ __forceinline__ void use(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+__device__ __forceinline__ void use(Key4& k) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) use(k.codes[i]);
+  use(k.sz);
+}
+__device__ __forceinline__ void use(Value4& v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(v.codes[i].x), "+r"(v.codes[i].y));
+  asm volatile("" : "+r"(v.s[0]), "+r"(v.s[1]), "+r"(v.z[0]), "+r"(v.z[1]));
+}
 __device__ __forceinline__ uint32_t same_f16x2(uint32_t v, int high) { return __byte_perm(v, 0, high ? 0x3232 : 0x1010); }
 // z + s c of two codes that are 1024 + c, or 1024 + 16 c, in fp16
 __device__ __forceinline__ uint32_t value_low(uint32_t x, uint32_t s, uint32_t z) {
@@ -397,6 +409,7 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       unsigned bad = 0;
       struct Tile {
         int seq, kh, key0, end, n;  // the unit's; n: tiles left, 0: none
+        int i;                      // tiles of the unit before it
       };
       int units = 0;
       auto next_unit = [&] {
@@ -413,28 +426,34 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
       };
       auto step = [&](Tile u) {  // the tile behind it
         u.key0 += kKeyTile;
+        ++u.i;
         return --u.n ? u : next_unit();
       };
-      // The thread's block of a tile is looked up one tile before it is loaded, and loaded one tile before it is written.
-      // No branch around the loads, which would wait for them: behind the last key its page is read, and not used.
+      // The thread's block of a tile is loaded one tile before it is written, and looked up another tile before that:
+      // the 16 threads of a block each for one of 16 tiles (each tile by itself: 1,000 clocks of waiting a tile).  No
+      // branch around the loads, which would wait for them: behind the last key its page is read, and not used.
+      int pages = 0;
       auto lookup = [&](const Tile& u) {
-        const int place = max(min(u.key0 + (t & ~15), u.end - 1), 0);
-        return __ldg(p.c.table + (long long)u.seq * p.c.width + (place >> p.c.page_shift));
+        if (u.i & 15) return;
+        const int place = max(min(u.key0 + row * kKeyTile + (t & ~15), u.end - 1), 0);
+        pages = __ldg(p.c.table + (long long)u.seq * p.c.width + (place >> p.c.page_shift));
       };
-      auto block_of = [&](const Tile& u, int page) -> const uint8_t* {
+      auto block_of = [&](const Tile& u) -> const uint8_t* {
         const int place = u.key0 + (t & ~15);
+        int page = __shfl_sync(0xffffffffu, pages, (lane & 16) + (u.i & 15));
         if (page < 0 || page >= p.c.n_pages) {
           if (place < u.end) bad |= PALU_DEVERR_PAGE;
           page = 0;
         }
         return page4(p.c, page, u.kh) + (place & (p.c.page - 1)) / 16 * kBlock4;
       };
-      // load(u, page), then store(tile of the ring): items `kv`, `kv` + 2, ...
+      // load(u, block), then store(tile of the ring): items `kv`, `kv` + 2, ...
       auto run = [&](int kv, auto&& load, auto&& store) {
         Tile u = next_unit();
-        load(u, block_of(u, lookup(u)));
+        lookup(u);
+        load(u, block_of(u));
         Tile u1 = u.n ? step(u) : u;
-        int page = lookup(u1);
+        lookup(u1);
         for (int item = kv; u.n; item += 2) {
           const int slot = item % kRing;
           if (item >= kRing) wait_or_fail(&sh.kv_empty[slot], (item / kRing - 1) & 1, &sh.failed, err);
@@ -445,10 +464,10 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.kv_full[item % kFull]);
           u = u1;
-          load(u, block_of(u, page));
+          load(u, block_of(u));
           if (u.n) {
             u1 = step(u);
-            page = lookup(u1);
+            lookup(u1);
           }
         }
       };
@@ -461,7 +480,10 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
               for (int i = 0; i < 4; ++i) k.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + 64 * row) + i);
               k.sz = __ldg(reinterpret_cast<const uint4*>(b + kKeyScales4 + 16 * row));
             },
-            [&](uint32_t tile) { store_keys(tile, t, k); });
+            [&](uint32_t tile) {
+              use(k);
+              store_keys(tile, t, k);
+            });
       } else {
         Value4 v;
         run(
@@ -478,7 +500,10 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
               }
               v.left = u.end - u.key0 - (t & ~15);
             },
-            [&](uint32_t tile) { store_values(tile, t & ~15, half, c, pair, v); });
+            [&](uint32_t tile) {
+              use(v);
+              store_values(tile, t & ~15, half, c, pair, v);
+            });
       }
       if (bad) atomicOr(err, bad);
     }
