@@ -643,23 +643,31 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         u.tok = m.tok, u.g0 = m.g0, u.kh = m.kh, u.rows = m.rows;
         const int r_base = both ? s * kHalf : 0, q_rows = both ? kHalf : kHalf / 2, q0 = both ? 0 : s * (kHalf / 2);
         const uint32_t q_tile = smem_addr(smem) + (both ? s : 0) * kTileBytes;
-        if constexpr (FOUR) {  // through registers: a half-warp a row
-#pragma unroll 4
-          for (int i = t >> 4; i < q_rows; i += kHalf / 16) {
-            const int r = q0 + i, ch = t & 15;
-            const uint4 raw = r_base + r < u.rows ? __ldg(reinterpret_cast<const uint4*>(row_query(p, u, r_base + r)) + ch)
-                                                  : make_uint4(0u, 0u, 0u, 0u);
-            const float2 f[4] = {unpack2<BF16>(raw.x), unpack2<BF16>(raw.y), unpack2<BF16>(raw.z), unpack2<BF16>(raw.w)};
-            float big = 0.f;
+        if constexpr (FOUR) {  // through registers: a half-warp a row, four rows' loads under way together
+          const int ch = t & 15;
+#pragma unroll 1
+          for (int i0 = t >> 4; i0 < q_rows; i0 += kHalf / 4) {
+            uint4 raw[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) big = fmaxf(big, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+            for (int j = 0; j < 4; ++j) {
+              const int r = r_base + q0 + i0 + j * (kHalf / 16);
+              raw[j] = r < u.rows ? __ldg(reinterpret_cast<const uint4*>(row_query(p, u, r)) + ch) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-            for (int x = 8; x; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-            const int e = query_shift(big);
-            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-            st128(panel_addr(q_tile, r, ch), pack_f16x2(f[0].x * up, f[0].y * up), pack_f16x2(f[1].x * up, f[1].y * up),
-                  pack_f16x2(f[2].x * up, f[2].y * up), pack_f16x2(f[3].x * up, f[3].y * up));
-            if (ch == 0) static_cast<Many4Smem&>(sh).factor[r_base + r] = query_factor(e, p.scale_log2);
+            for (int j = 0; j < 4; ++j) {
+              const int r = q0 + i0 + j * (kHalf / 16);
+              const float2 f[4] = {unpack2<BF16>(raw[j].x), unpack2<BF16>(raw[j].y), unpack2<BF16>(raw[j].z), unpack2<BF16>(raw[j].w)};
+              float big = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+#pragma unroll
+              for (int x = 8; x; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+              const int e = query_shift(big);
+              const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+              st128(panel_addr(q_tile, r, ch), pack_f16x2(f[0].x * up, f[0].y * up), pack_f16x2(f[1].x * up, f[1].y * up),
+                    pack_f16x2(f[2].x * up, f[2].y * up), pack_f16x2(f[3].x * up, f[3].y * up));
+              if (ch == 0) static_cast<Many4Smem&>(sh).factor[r_base + r] = query_factor(e, p.scale_log2);
+            }
           }
         } else {
           for (int i = t; i < q_rows * 16; i += kHalf) {
