@@ -71,9 +71,9 @@ __device__ __forceinline__ int find_block(const int* offsets, int batch, int x, 
 // What a CTA's 16 half-warps do: token `place` of sequence b, in row `row` of
 // the call, where `live`; all in one block.
 struct BlockWork {
-  int b, place, row;
+  int place, row;
   bool live;
-  uint8_t* block;  // of head 0
+  int page, in_page;  // the block's page, and its place there
 };
 
 // Which block CTA x has (uniform: false for all threads or none).  The tokens are
@@ -104,17 +104,21 @@ __device__ __forceinline__ bool block_work(const PagedView& c, const int* offset
   const int j = x - ((o0 >> 4) + 2 * b);
   const long long blk = (first >> 4) + j, at = blk * 16;  // the block's first place
   if (n == 0 || j < 0 || at >= first + n) return false;
-  const int page = __ldg(c.table + (long long)b * c.width + (at >> c.page_shift));
-  if (page < 0 || page >= c.n_pages) {
-    if (threadIdx.x == 0) atomicOr(c.error, PALU_DEVERR_PAGE);
-    return false;
-  }
-  w->b = b;
   w->place = (int)at + (threadIdx.x >> 4);
   w->live = w->place >= first && w->place < first + n;
   w->row = o0 + (int)(w->place - first);
-  w->block = page4(c, page, 0) + ((int)at & (c.page - 1)) / 16 * kBlock4;
+  w->page = __ldg(c.table + (long long)b * c.width + (at >> c.page_shift));
+  w->in_page = ((int)at & (c.page - 1)) >> 4;
   return true;
+}
+
+// Its block of head 0, or nullptr and an error bit (uniform); to be asked for when the rows' loads are under way.
+__device__ __forceinline__ uint8_t* block_of_work(const PagedView& c, const BlockWork& w) {
+  if (w.page < 0 || w.page >= c.n_pages) {
+    if (threadIdx.x == 0) atomicOr(c.error, PALU_DEVERR_PAGE);
+    return nullptr;
+  }
+  return page4(c, w.page, 0) + w.in_page * kBlock4;
 }
 
 }  // namespace palu

@@ -38,16 +38,53 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// The codes of a lane's eight channels, and the group's scale and zero.  Code i
-// stands in bits 4 i .. 4 i + 3, or, PAIRED, the even codes in the low half of
-// the word and the odd ones in the high half.
+// The word of a lane's eight codes: code i in bits 4 i .. 4 i + 3, or, PAIRED, the
+// even codes in its low half and the odd ones in the high half.  Codes are added
+// up in fp32, four in the low 16 bits of a number from 2^23 on.
+template <bool PAIRED>
+struct CodeSum {
+  float part[2] = {8388608.f, 8388608.f};
+  __device__ __forceinline__ void add(int i, float c) {
+    constexpr float kWeight[4] = {1.f, 16.f, 256.f, 4096.f};
+    float& to = part[PAIRED ? i & 1 : i >> 2];
+    to = fmaf(c, kWeight[PAIRED ? i >> 1 : i & 3], to);
+  }
+  __device__ __forceinline__ uint32_t word() const {
+    return __byte_perm(__float_as_uint(part[0]), __float_as_uint(part[1]), 0x5410);
+  }
+};
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& raw, float* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<BF16>(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+// By a division a channel.  (Out of line: it is rarely wanted, and its code is long.)
+template <bool BF16, bool PAIRED>
+__device__ __noinline__ uint32_t divide8(uint4 raw, float s, float z) {
+  float x[8];
+  unpack8<BF16>(raw, x);
+  CodeSum<PAIRED> sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    sum.add(i, s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], z), s)), 0.f), 15.f) : 0.f);
+  return sum.word();
+}
+
+// The codes of a lane's eight channels, and the group's scale and zero.
 //   rint((x - z) / s), cut to 0 .. 15, without a division a channel: with r near
 // 1 / (15.49 s), v = (x - z) r saturated to 0 .. 1 and y = 15.49 v are within
-// 1e-5 of the quotient (five roundings of 2^-24 at up to 15.5) where that is in
-// range, and y + 1.5 2^23 rounds to the nearest even integer.  Only where y lies
-// within 1e-5 of a border between two codes does the rounded quotient decide.
-// Codes are added up in fp32, four in 16 bits.  (With a division a channel the
-// append of 9,790 tokens took 67 us, 59 % of the ALU's slots.)
+// 1e-5 of the quotient (six roundings of 2^-24, one of them twice that, at up to
+// 15.5) where that is in range, and y + 1.5 2^23 rounds to the nearest even
+// integer.  Only where y lies within 1e-5 of a border between two codes does the
+// rounded quotient decide.  (max - min) / 15 is its product with 1 / 15 and one
+// step of correction, which gives the rounded quotient for every significand.
+// With a division each the append of 9,790 tokens took 67 us, 59 % of the ALU's
+// slots.
 template <bool BF16, bool PAIRED>
 __device__ __forceinline__ uint32_t quantise8(const uint4& raw, unsigned mask, uint16_t* scale, uint16_t* zero) {
   uint32_t mn = min2<BF16>(min2<BF16>(raw.x, raw.y), min2<BF16>(raw.z, raw.w));
@@ -69,7 +106,8 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& raw, unsigned mask, u
     lo = fminf(fmaxf(lo, -65504.f), 65504.f);
     hi = fminf(fmaxf(hi, -65504.f), 65504.f);
   }
-  __half s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+  const float range = __fsub_rn(hi, lo), q = __fmul_rn(range, 1.f / 15.f);
+  __half s = __float2half_rn(fmaf(fmaf(-15.f, q, range), 1.f / 15.f, q));
   const __half z = __float2half_rn(lo);
   const float zf = __half2float(z);
   // a step less where the largest code would stand for more than fp16 has
@@ -78,31 +116,20 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& raw, unsigned mask, u
   *scale = __half_as_ushort(s);
   *zero = __half_as_ushort(z);
   float x[8];
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<BF16>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-  constexpr float kTop = 15.49f, kRound = 12582912.f, kWeight[4] = {1.f, 16.f, 256.f, 4096.f};
-  const float r = sf > 0.f ? __frcp_rn(sf) * (1.f / kTop) : 0.f;
-  float part[2] = {8388608.f, 8388608.f}, off = 0.f;  // 2^23: the sums are the low bits
+  unpack8<BF16>(raw, x);
+  constexpr float kTop = 15.49f, kRound = 12582912.f;
+  const float r = sf > 0.f ? __fdividef(1.f / kTop, sf) : 0.f;
+  CodeSum<PAIRED> sum;
+  float off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = __saturatef(__fsub_rn(x[i], zf) * r), c = __fadd_rn(fmaf(v, kTop, kRound), -kRound);
+    float v;  // saturated in the product itself
+    asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(v) : "f"(__fsub_rn(x[i], zf)), "f"(r));
+    const float c = __fadd_rn(fmaf(v, kTop, kRound), -kRound);
     off = fmaxf(off, fabsf(fmaf(v, kTop, -c)));
-    part[PAIRED ? i & 1 : i >> 2] += c * kWeight[PAIRED ? i >> 1 : i & 3];
+    sum.add(i, c);
   }
-  if (off > 0.5f - 1e-5f) {
-    part[0] = part[1] = 8388608.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = sf > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], zf), sf)), 0.f), 15.f) : 0.f;
-      part[PAIRED ? i & 1 : i >> 2] += c * kWeight[PAIRED ? i >> 1 : i & 3];
-    }
-  }
-  return __byte_perm(__float_as_uint(part[0]), __float_as_uint(part[1]), 0x5410);
+  return off > 0.5f - 1e-5f ? divide8<BF16, PAIRED>(raw, sf, zf) : sum.word();
 }
 
 // Key codes back from the word that has the odd channels in its high half.
@@ -131,7 +158,7 @@ struct Append4Params {
 };
 
 template <bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kAppendThreads) paged4_append_kernel(const Append4Params a) {
+__global__ void __launch_bounds__(kAppendThreads, 5) paged4_append_kernel(const Append4Params a) {
   const QkParams& p = a.q;
   __shared__ __align__(16) uint8_t stage[kRunHeads * (kBlock4 - kValueCodes4)];
   __shared__ __align__(16) uint16_t turned[kAppendThreads / 16][kHeadDim];
@@ -149,7 +176,6 @@ __global__ void __launch_bounds__(kAppendThreads) paged4_append_kernel(const App
   BlockWork w;
   if (threadIdx.x == 0) live_s = 0;
   if (!block_work(p.c, p.offsets, nullptr, p.rows, x, run == 0, &w)) return;
-  uint8_t* const block = w.block + h0 * p.c.ks1;
   // the token's place in the rotation; without one it is not appended, neither keys nor values
   float4 co = {}, si = {};
   const bool pairs = lane < (p.tr.rope_dim >> 3);
@@ -169,13 +195,16 @@ __global__ void __launch_bounds__(kAppendThreads) paged4_append_kernel(const App
     const int ca = !INTERLEAVED && pairs ? 4 * lane : 8 * lane;
     const int cb = !INTERLEAVED && pairs ? (p.tr.rope_dim >> 1) + 4 * lane : 8 * lane + 4;
     const uint16_t* src = p.k + w.row * p.ks1 + h0 * p.ks2;
-    uint2 lo[kRunHeads], hi[kRunHeads];
-#pragma unroll
-    for (int i = 0; i < kRunHeads; ++i)
-      if (i < nh) {
-        lo[i] = __ldg(reinterpret_cast<const uint2*>(src + i * p.ks2 + ca));
-        hi[i] = __ldg(reinterpret_cast<const uint2*>(src + i * p.ks2 + cb));
-      }
+    // the loop over the heads is kept rolled, a load ahead: four times its code is more than the instruction cache likes
+    uint2 lo, hi;
+    auto load = [&](int i) {
+      lo = __ldg(reinterpret_cast<const uint2*>(src + i * p.ks2 + ca));
+      hi = __ldg(reinterpret_cast<const uint2*>(src + i * p.ks2 + cb));
+    };
+    load(0);
+    uint8_t* block = block_of_work(p.c, w);
+    if (!block) return;
+    block += h0 * p.c.ks1;
     const uint16_t* wsrc = static_cast<const uint16_t*>(p.tr.k_weight);
     float wt[8] = {};
     if (wsrc) {
@@ -188,57 +217,68 @@ __global__ void __launch_bounds__(kAppendThreads) paged4_append_kernel(const App
         wt[2 * i + 1] = f.y;
       }
     }
-#pragma unroll
-    for (int i = 0; i < kRunHeads; ++i)
-      if (i < nh) {
-        transform_row<BF16, INTERLEAVED>(lo[i], hi[i], wsrc != nullptr, wt, pairs && p.tr.cos_sin != nullptr, co, si, p.tr.eps, mask);
-        *reinterpret_cast<uint2*>(&turned[t][ca]) = lo[i];
-        *reinterpret_cast<uint2*>(&turned[t][cb]) = hi[i];
-        __syncwarp(mask);
-        const uint4 raw = *reinterpret_cast<const uint4*>(&turned[t][8 * lane]);
-        __syncwarp(mask);
-        uint16_t s, z;
-        const uint32_t codes = quantise8<BF16, true>(raw, mask, &s, &z);
-        uint8_t* to = block + i * p.c.ks1;
-        *reinterpret_cast<uint32_t*>(to + 64 * t + 16 * (lane & 3) + 4 * (lane >> 2)) = codes;
-        if ((lane & 3) == 0) {
-          uint16_t* sz = reinterpret_cast<uint16_t*>(to + kKeyScales4 + 16 * t) + (lane >> 2);
-          sz[0] = s;
-          sz[4] = z;
-        }
+#pragma unroll 1
+    for (int i = 0; i < nh; ++i) {
+      uint2 a = lo, b = hi;
+      if (i + 1 < nh) load(i + 1);
+      transform_row<BF16, INTERLEAVED>(a, b, wsrc != nullptr, wt, pairs && p.tr.cos_sin != nullptr, co, si, p.tr.eps, mask);
+      *reinterpret_cast<uint2*>(&turned[t][ca]) = a;
+      *reinterpret_cast<uint2*>(&turned[t][cb]) = b;
+      __syncwarp(mask);
+      const uint4 raw = *reinterpret_cast<const uint4*>(&turned[t][8 * lane]);
+      __syncwarp(mask);
+      uint16_t s, z;
+      const uint32_t codes = quantise8<BF16, true>(raw, mask, &s, &z);
+      uint8_t* to = block + i * p.c.ks1;
+      *reinterpret_cast<uint32_t*>(to + 64 * t + 16 * (lane & 3) + 4 * (lane >> 2)) = codes;
+      if ((lane & 3) == 0) {
+        uint16_t* sz = reinterpret_cast<uint16_t*>(to + kKeyScales4 + 16 * t) + (lane >> 2);
+        sz[0] = s;
+        sz[4] = z;
       }
+    }
     return;
   }
   // values: the block's image
+  const uint16_t* const src = p.v + (w.live ? w.row : 0) * p.vs1 + h0 * p.vs2 + 8 * lane;
+  uint4 next = {};
+  if (w.live) next = __ldg(reinterpret_cast<const uint4*>(src));
+  uint8_t* block = block_of_work(p.c, w);
+  if (!block) return;
+  block += h0 * p.c.ks1;
   __syncthreads();
   if (w.live) {
     if (lane == 0) atomicOr(&live_s, 1u << t);
-    const uint16_t* src = p.v + w.row * p.vs1 + h0 * p.vs2 + 8 * lane;
-    uint4 raw[kRunHeads];
+#pragma unroll 1
+    for (int i = 0; i < nh; ++i) {
+      const uint4 raw = next;
+      if (i + 1 < nh) next = __ldg(reinterpret_cast<const uint4*>(src + (i + 1) * p.vs2));
+      uint16_t s, z;
+      const uint32_t mine = quantise8<BF16, false>(raw, mask, &s, &z), other = __shfl_xor_sync(mask, mine, 1);
+      uint8_t* const im = stage + i * (kBlock4 - kValueCodes4);
+      // an even lane and the odd one behind it have the two nibbles of eight bytes: it writes those of g 0, 2, 4, 6, the
+      // odd one the others
+      const uint32_t bytes = lane & 1 ? (mine & 0xf0f0f0f0u) | (other >> 4 & 0x0f0f0f0fu) : (mine & 0x0f0f0f0fu) | (other & 0x0f0f0f0fu) << 4;
+      uint8_t* const to = im + value_byte(t, lane) + 64 * (lane & 1);
 #pragma unroll
-    for (int i = 0; i < kRunHeads; ++i)
-      if (i < nh) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + i * p.vs2));
-#pragma unroll
-    for (int i = 0; i < kRunHeads; ++i)
-      if (i < nh) {
-        uint16_t s, z;
-        const uint32_t mine = quantise8<BF16, false>(raw[i], mask, &s, &z), other = __shfl_xor_sync(mask, mine, 1);
-        uint8_t* const im = stage + i * (kBlock4 - kValueCodes4);
-        // an even lane and the odd one behind it have the two nibbles of eight bytes
-        const uint32_t low = lane & 1 ? other : mine, high = lane & 1 ? mine : other;
-        const int at = value_byte(t, lane), g0 = lane & 1 ? 4 : 0;
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          im[at + 64 * (g0 + g)] = (uint8_t)((low >> (4 * (g0 + g)) & 15) | (high >> (4 * (g0 + g)) & 15) << 4);
-        if ((lane & 3) == 0) {
-          uint8_t* sz = im + 1024 + value_scale(t, lane >> 2);
-          *reinterpret_cast<uint16_t*>(sz) = s;
-          *reinterpret_cast<uint16_t*>(sz + 128) = z;
-        }
+      for (int g = 0; g < 4; ++g) to[128 * g] = (uint8_t)(bytes >> (8 * g));
+      if ((lane & 3) == 0) {
+        uint8_t* sz = im + 1024 + value_scale(t, lane >> 2);
+        *reinterpret_cast<uint16_t*>(sz) = s;
+        *reinterpret_cast<uint16_t*>(sz + 128) = z;
       }
+    }
   }
   __syncthreads();
   const unsigned live = live_s;
+  if (live == 0xffffu) {
+    constexpr int kPieces = (kBlock4 - kValueCodes4) / 16;
+    for (int i = threadIdx.x; i < nh * kPieces; i += kAppendThreads) {
+      const int h = i / kPieces;
+      *reinterpret_cast<uint4*>(block + h * p.c.ks1 + kValueCodes4 + 16 * (i - h * kPieces)) = *reinterpret_cast<const uint4*>(stage + 16 * i);
+    }
+    return;
+  }
   constexpr int kWords = (kBlock4 - kValueCodes4) / 4;
   for (int i = threadIdx.x; i < nh * kWords; i += kAppendThreads) {
     const int h = i / kWords, k = i - h * kWords;
@@ -286,10 +326,11 @@ __global__ void __launch_bounds__(kAppendThreads) paged4_read_kernel(const Read4
   const int h0 = run * kRunHeads, nh = min(kRunHeads, p.c.kv_heads - h0);
   BlockWork w;
   if (!block_work(p.c, p.offsets, p.starts, p.rows, x, run == 0, &w)) return;
+  const uint8_t* const block = block_of_work(p.c, w);
+  if (!block) return;
   for (int i = threadIdx.x; i < nh * (kBlock4 / 16); i += kAppendThreads) {
     const int h = i / (kBlock4 / 16), k = i - h * (kBlock4 / 16);
-    *reinterpret_cast<uint4*>(blocks + 16 * i) =
-        __ldg(reinterpret_cast<const uint4*>(w.block + (h0 + h) * p.c.ks1) + k);
+    *reinterpret_cast<uint4*>(blocks + 16 * i) = __ldg(reinterpret_cast<const uint4*>(block + (h0 + h) * p.c.ks1) + k);
   }
   __syncthreads();
   if (!w.live) return;
