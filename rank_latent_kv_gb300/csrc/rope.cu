@@ -28,21 +28,24 @@ constexpr int kRopeThreads = 256;
 
 // cos and sin of `turn` / 2^64 turns, times m
 __device__ __forceinline__ void turn_cos_sin(uint64_t turn, float m, float& co, float& si) {
-  const uint64_t near = turn + (1ULL << 61);   // the quarter turns, rounded, in the top two bits
-  const int64_t rest = (int64_t)(turn - (near & (3ULL << 62)));
-  const unsigned quarter = (unsigned)(near >> 62);
-  // both halves: where the high one is short, the low one's bits count
-  const float f = fmaf((float)(uint32_t)rest, 0x1p-64f, (float)(int32_t)(rest >> 32) * 0x1p-32f);
-  const float x = f * 6.28318530717958648f, u = x * x;
+  // an eighth of a turn more: the quarter turns, rounded, in the top two bits, the rest of the turn behind them; 32
+  // bits of it are enough for angles to 2^-33
+  const uint32_t near = (uint32_t)(turn >> 32) + (1u << 29);
+  const int rest = (int)(__funnelshift_l((uint32_t)turn, near, 2) ^ 0x80000000u);
+  const float x = (float)rest * (6.28318530717958648f * 0x1p-34f), u = x * x;
   const float s = x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), 1.f);
   const float c = fmaf(u, fmaf(u, fmaf(u, fmaf(u, fmaf(u, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
-  const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
-  co = (quarter == 1 || quarter == 2) ? -a * m : a * m;
-  si = quarter & 2 ? -b * m : b * m;
+  // a quarter turn swaps the two; the cosine is negative in the second and third, the sine in the third and fourth
+  const bool odd = near & (1u << 30);
+  const uint32_t a = __float_as_uint((odd ? s : c) * m), b = __float_as_uint((odd ? c : s) * m);
+  co = __uint_as_float(a ^ ((near ^ near << 1) & 0x80000000u));
+  si = __uint_as_float(b ^ (near & 0x80000000u));
 }
 
 // A thread has four pairs and goes down the rows; rope_dim / 8 threads a row.
-__global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const __grid_constant__ RopeParams p) {
+// All CTAs are resident: a second wave of the table's 131,072 rows is a third more time.
+constexpr int kRopeCtas = 5;  // an SM
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_table_kernel(const __grid_constant__ RopeParams p) {
   const int per_row = p.rope >> 3;
   const long long t = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
   const long long step = (long long)gridDim.x * kRopeThreads / per_row;  // rows; threads behind them have none
@@ -112,8 +115,8 @@ extern "C" palu_status palu_rope_table(const palu_rope_scaling* scaling, int64_t
   p.positions = positions;
   p.magnitude = (float)s.magnitude;
   p.rope = d;
-  // eight CTAs an SM, and at least one row a thread
-  const long long threads = positions * (d >> 3), most = 8LL * device_sm_count();
+  // at least one row a thread
+  const long long threads = positions * (d >> 3), most = (long long)kRopeCtas * device_sm_count();
   const long long grid = (threads + kRopeThreads - 1) / kRopeThreads;
   rope_table_kernel<<<(unsigned)(grid < most ? grid : most), kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cuda_check(cudaGetLastError(), "rope_table_kernel launch");
