@@ -299,22 +299,27 @@ struct AttnLayout {
 // sequences of 1 token behind 1024 keys 16.5 and 14.5 us, behind 4096 20.1 and 23.9; 256 sequences of 5 behind 256 128 and
 // 96 us, behind 4096 182 and 353; 16 of 1024 new tokens behind 8192 1972 and 1456.  In clocks, summed over the SMs:
 constexpr double kShareTile = 2900., kShareRow = 350., kShareLaunch = 13300.;
+// Of 4-bit codes, where own units have up to 16 rows (with more a tile's products and weights take as long as above):
+// 32 sequences of 1 token (24 heads of 8, 777 own keys) behind 1024 keys 26 and 25 us, behind 2048 29 and 30, behind
+// 8192 36 and 70; 256 (28 of 4, 300 own) behind 1024 66 and 61, behind 4096 81 and 127; 4 behind 32,768 29 and 23.
+constexpr double kShareTile4 = 600.;
 
 // The most new tokens a call for which it can (the tiles saved are at most one a sequence, KV head and tile of the table).
-static int64_t most_shared_tokens(const palu_paged_cache* c, bool four, int32_t q_heads) {
+static int64_t most_shared_tokens(const palu_paged_cache* c, int32_t q_heads) {
   const double tiles = prefix_tiles_of(c->table_width * c->page_size);
   const double n = (kShareTile * c->kv_heads * tiles * c->batch - kShareLaunch * device_sm_count()) / (kShareRow * q_heads);
   return std::max<int64_t>(1, (int64_t)n);
 }
 static bool share_pays(const palu_paged_cache* c, bool four, int64_t tokens, int32_t q_heads, int32_t max_new, int32_t shared_pages) {
-  if (shared_pages == 0 || c->batch == 1 || tokens > most_shared_tokens(c, four, q_heads)) return false;
+  if (shared_pages == 0 || c->batch == 1 || tokens > most_shared_tokens(c, q_heads)) return false;
   const int Gq = q_heads / c->kv_heads;
   auto row_tiles = [&](double new_tokens) { return ceil(new_tokens * Gq / kManyRows); };
   // the counts are the device's: as many sequences as can be with the most new tokens, one token for the others
   const double many = std::min<int64_t>(max_new, tokens), B = std::min<int64_t>(c->batch, tokens);
   const double full = many > 1 ? std::min(B, (tokens - B) / (many - 1)) : 0;
   const double saved = full * row_tiles(many) + (B - full) * row_tiles(1) - row_tiles((double)tokens);
-  return kShareTile * c->kv_heads * prefix_tiles_of(shared_pages * c->page_size) * saved >
+  const double tile = four && many * Gq <= 16 ? kShareTile4 : kShareTile;
+  return tile * c->kv_heads * prefix_tiles_of(shared_pages * c->page_size) * saved >
          kShareRow * (double)tokens * q_heads + kShareLaunch * device_sm_count();
 }
 
@@ -353,7 +358,7 @@ static palu_status attn_layout(const palu_paged_cache* c, bool four, int64_t tok
   // With shared pages the size is the same whether or not they are read once here: it also serves fewer tokens, and
   // any other number of them.
   const bool may_share = shared_pages > 0 && c->batch > 1;
-  const size_t records = may_share ? 2 * (size_t)std::min(tokens, most_shared_tokens(c, four, q_heads)) * q_heads : 0;
+  const size_t records = may_share ? 2 * (size_t)std::min(tokens, most_shared_tokens(c, q_heads)) * q_heads : 0;
   l->row_ml = take(records * sizeof(float2));
   l->row_acc = take(records * kHeadDim * sizeof(float));
   const size_t parts = o;
