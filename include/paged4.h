@@ -111,8 +111,10 @@ palu_status palu_paged4_attn_workspace_size(const palu_paged4_cache* cache, int6
  * Up to 16 rows a KV head the codes enter the products as they are, and the
  * scales in fp32 (keys) or with the weights (values: a weight and its product
  * with the scale are each rounded to fp16, in a range that follows the scales).
- * With more rows keys, values and weights are each rounded once to the cache's
- * type.  Sums, maxima and accumulators are fp32. */
+ * With more rows keys, values and weights are each rounded once to fp16 (weights
+ * under 2^-20 of a row's largest lose bits), in bf16 caches too.  Sums, maxima
+ * and accumulators are fp32; queries lose nothing but what lies 2^-24 under a
+ * row's largest. */
 palu_status palu_paged4_attn(const palu_paged4_cache* cache, int64_t tokens, const int32_t* offsets, int32_t max_new,
                              int32_t q_heads, const void* q, const int64_t q_strides[2], int32_t shared_pages,
                              float softmax_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);

@@ -7,10 +7,10 @@ a few, about 2^-16 absolute in the exponent, which enters every weight
 relatively.  With few rows a KV head a weight p and its product p s with the
 scale are each rounded to fp16 (2^-11); with w the weights and C = sum w (s c + |z|)
 per output: |got - ref| <= (2^-10 + 2^-12) C + (eps / 2) |ref|.  With many rows
-keys, values and weights are each rounded once to the type (eps / 2): a key's
-rounding moves its score by at most d_t = (eps / 2) scale sum |q| |k|, so with A
-= sum w |v| the bar gains sum w d |v| + |ref| sum w d, and weights and values
-cost (eps / 2) A each: |got - ref| <= (eps + 2^-12) A + that + (eps / 2) |ref|.
+keys, values and weights are each rounded once to fp16 (2^-11): a key's rounding
+moves its score by at most d_t = 2^-11 scale sum |q| |k|, so with A = sum w |v|
+the bar gains sum w d |v| + |ref| sum w d, and weights and values cost 2^-11 A
+each: |got - ref| <= (2^-10 + 2^-12) A + that + (eps / 2) |ref|.
 Second-order terms are covered by 1 + 2^-5.
 """
 import math
@@ -135,9 +135,9 @@ def check_attend(case, q, new, got, scale=None, rows_behind=0, only=None):
             w = torch.softmax(s, -1).nan_to_num(0.0)             # a row that sees nothing
             ref = torch.einsum("hnt,thd->nhd", w, v)
             bar = (2.0 ** -10 + 2.0 ** -12) * torch.einsum("hnt,thd->nhd", w, size)
-            d = eps / 2 * scale * torch.einsum("nhd,thd->hnt", x.abs(), k.abs()) * seen
+            d = 2.0 ** -11 * scale * torch.einsum("nhd,thd->hnt", x.abs(), k.abs()) * seen
             A = torch.einsum("hnt,thd->nhd", w, v.abs())
-            full = (eps + 2.0 ** -12) * A + torch.einsum("hnt,thd->nhd", w * d, v.abs()) + \
+            full = (2.0 ** -10 + 2.0 ** -12) * A + torch.einsum("hnt,thd->nhd", w * d, v.abs()) + \
                 ref.abs() * (w * d).sum(-1).T[..., None]
             # which kernel takes a row follows from the whole call's sizes: either bar's kernel may have had it
             bar = torch.maximum(bar, full) if many or len(new) > 1 else bar
