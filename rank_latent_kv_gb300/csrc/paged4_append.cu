@@ -10,7 +10,9 @@
 // word's eight codes as a product's operand.  So a block's value codes are put
 // together in shared memory and go out as whole words, or, where the call does
 // not bring all of a word's tokens, as the bytes that it does bring.  Queries
-// take the same path as in the uncompressed cache, in CTAs of their own.
+// take the same path as in the uncompressed cache, in CTAs of their own, which
+// wait for memory while those of keys and values compute: so the two kinds
+// alternate in the grid.
 #include <math.h>
 
 #include "paged4.cuh"
@@ -152,8 +154,8 @@ __device__ __forceinline__ int value_scale(int t, int group) {
 }
 
 struct Append4Params {
-  QkParams q;      // with the operands of keys and values
-  long long q_ctas;
+  QkParams q;             // with the operands of keys and values
+  unsigned long long kv;  // CTAs of keys and values, of all, in 2^-32, rounded up
   int kv_runs;
 };
 
@@ -163,12 +165,14 @@ __global__ void __launch_bounds__(kAppendThreads, 5) paged4_append_kernel(const 
   __shared__ __align__(16) uint8_t stage[kRunHeads * (kBlock4 - kValueCodes4)];
   __shared__ __align__(16) uint16_t turned[kAppendThreads / 16][kHeadDim];
   __shared__ unsigned live_s;
-  if (blockIdx.x < a.q_ctas) {
-    const int tile = blockIdx.x / p.q_runs;
-    transform_tile<BF16, INTERLEAVED, true>(p, tile, blockIdx.x - tile * p.q_runs);
+  // CTAs of keys and values before this one; whether it is one
+  const int y = (int)(blockIdx.x * a.kv >> 32);
+  if ((int)((blockIdx.x + 1) * a.kv >> 32) == y) {
+    const int z = (int)blockIdx.x - y, tile = z / p.q_runs;
+    transform_tile<BF16, INTERLEAVED, true>(p, tile, z - tile * p.q_runs);
     return;
   }
-  const int y = (int)(blockIdx.x - a.q_ctas), x = y / (2 * a.kv_runs), run = y - x * 2 * a.kv_runs;
+  const int x = y / (2 * a.kv_runs), run = y - x * 2 * a.kv_runs;
   const bool values = run >= a.kv_runs;
   const int h0 = (values ? run - a.kv_runs : run) * kRunHeads, nh = min(kRunHeads, p.hk - h0);
   const int t = threadIdx.x >> 4, lane = threadIdx.x & 15;
@@ -443,9 +447,11 @@ extern "C" palu_status palu_paged4_append(const palu_paged4_cache* cache, const 
   p.offsets = offsets;
   p.c = paged4_view(cache);
   a.kv_runs = (cache->kv_heads + kRunHeads - 1) / kRunHeads;
-  a.q_ctas = (tokens + kAppendThreads / 16 - 1) / (kAppendThreads / 16) * p.q_runs;
-  const long long grid = a.q_ctas + (tokens / 16 + 2LL * cache->batch) * 2 * a.kv_runs;
+  const long long q_ctas = (tokens + kAppendThreads / 16 - 1) / (kAppendThreads / 16) * p.q_runs;
+  const long long kv_ctas = (tokens / 16 + 2LL * cache->batch) * 2 * a.kv_runs, grid = q_ctas + kv_ctas;
   if (grid > 0x7fffffff) return fail(PALU_ERR_UNSUPPORTED, "too many rows for one call");
+  // rounded up: of i CTAs floor(i kv / 2^32) are of keys and values, and of all of them kv_ctas, as grid < 2^32
+  a.kv = (((unsigned long long)kv_ctas << 32) + grid - 1) / grid;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = cache->dtype == PALU_TYPE_BF16, inter = p.tr.interleaved != 0;
   auto* const kernel = bf16 ? inter ? paged4_append_kernel<true, true> : paged4_append_kernel<true, false>
