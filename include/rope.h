@@ -35,7 +35,7 @@ typedef struct {
   double original;       /* PARTS: tokens of the training's context, > 0 */
   double low_turns;      /* PARTS: 0 <= low_turns < high_turns */
   double high_turns;
-  double magnitude;      /* the cosines and sines are multiplied by it; finite */
+  double magnitude;      /* the cosines and sines are multiplied by it; finite in fp32 */
 } palu_rope_scaling;
 
 /* Row r of the table, r in 0 .. positions - 1: the cosines, then the sines, of

@@ -12,7 +12,8 @@
 // rows, half as fast for 4,096 with 35,000, and its code costs the smallest calls
 // 2 us; the host takes longer than either.)
 // Pages given back may be taken by the same call, so the cluster meets between
-// the two, and once more before the rows look pages up.
+// the two, and once more before the rows look pages up.  16 sequences take 5 us a
+// plan, 512 with 66,000 rows 20.
 #include <cooperative_groups.h>
 
 #include "pages.h"

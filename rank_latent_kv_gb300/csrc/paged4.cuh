@@ -38,14 +38,15 @@ __device__ __forceinline__ uint8_t* page4(const PagedView& c, int page, int head
 
 // Queries enter fp16 products times 2^e, e such that the row's largest value
 // `big` comes to 2^13 .. 2^14 (rows of zeros or of infinities: as they are), and
-// the factor that takes the products back to log2 (not 0, whatever the scale: a
-// masked score of -infinity stays one).
+// the factor that takes the products back to log2: not 0, whatever the scale, so
+// that a masked score of -infinity stays one, and not infinite (queries above 2^118
+// give one key all the weight, by whatever factor).
 __device__ __forceinline__ int query_shift(float big) {
   const int ex = (int)(__float_as_uint(big) >> 23);
   return ex == 0 || ex == 255 ? 0 : max(min(13 + 127 - ex, 100), -113);
 }
 __device__ __forceinline__ float query_factor(int e, float scale_log2) {
-  return fmaxf(__uint_as_float((uint32_t)(127 - e) << 23) * scale_log2, 0x1p-120f);
+  return fminf(fmaxf(__uint_as_float((uint32_t)(127 - e) << 23) * scale_log2, 0x1p-120f), 3e38f);
 }
 
 // Work on whole blocks without a scan over the sequences: n rows touch at most
@@ -95,7 +96,7 @@ __device__ __forceinline__ bool block_work(const PagedView& c, const int* offset
   long long first, len;
   if (tell && x < c.batch && threadIdx.x == 0) {
     unsigned bad = span(x, &o0, &n, &first, &len);
-    if (n == 0 && starts) bad = 0;  // no tokens: no matter where from
+    if (n == 0 && o0 >= 0 && o0 <= rows) bad = 0;  // no tokens: no matter what its length is
     if (x == 0 && o0 != 0) bad |= PALU_DEVERR_SPAN;
     if (bad) atomicOr(c.error, bad);
   }

@@ -18,13 +18,18 @@
 //   Values: a row's weights p, in fp16, are the n side of the products with the
 //   zeros and, times the tokens' scales of the group, with the codes.  p is
 //   relative to a reference that lies 2^6 under the row's maximum and is raised
-//   when a weight would pass 2^14; where a scale above 1 is met both bounds are
-//   lowered by its power of two, so that no p s passes 2^15.  Weights down to
+//   when a weight would pass 2^14; where a scale of 2 or more is met both bounds
+//   are lowered by its power of two, so that no p s passes 2^15.  Weights down to
 //   2^-20 of the largest keep all their bits.
 // A persistent CTA an SM; a loading warp copies 240 keys at a time, a page of a
 // head by one bulk copy, into a ring of stages; 15 warps take a block of 16
 // tokens of a stage each (for 9 to 16 rows, whose accumulators need the
-// registers, 8 warps two blocks of 256 keys each).
+// registers, 8 warps two blocks of 256 keys each: 87 us where 8 rows take 53).
+//
+// 16 sequences of up to 32,768 tokens, 28 heads of 4: 257 MB in 52.7 us, 9 of them
+// fixed, then 5.8 TB/s; 64 of up to 8,191 with 16 heads of 16: 1,012 MB in 174 us.
+// The copies alone take 48.7 and 161: instructions and memory bound it together
+// (300 warp instructions a block, 47 % of the issue slots).
 #pragma once
 
 #include <math.h>
@@ -49,7 +54,7 @@ template <int NT>
 constexpr int kFew4MergeBytes = kFew4Warps<NT> * 8 * kMerge4Stride * 4;
 constexpr float kLift4 = 6.f;      // log2: the reference's distance from the maximum
 constexpr float kRaise4 = 14.f;    // log2: the largest weight before it is raised
-constexpr float kNothing4 = -1e30f;  // a reference before any key has been seen
+constexpr float kNothing4 = -3e38f;  // a reference before any key has been seen: below any score
 
 // One stage, as the loading warp hands it to the others.
 struct Stage4Meta {

@@ -807,7 +807,7 @@ class PagePool:
     """Pages handed out on the device (include/pages.h) for the caches that read page_table int32 [B, width] and lengths
     int64 [B].  held int32 [B]: how many entries of its row a sequence has (default: none); free_pages int32 [n] and
     n_free int32 [1]: the stack of free pages (default: pages n_pages-1 .. 0, so that page 0 is taken first).  All of
-    them are the program's to read and, between calls, to write."""
+    them are the program's to read and, between calls, to write; what is made here is made on the current stream."""
 
     def __init__(self, page_table, lengths, page_size, held=None, free_pages=None, n_free=None, n_pages=None):
         dev = _here(page_table, "page_table")

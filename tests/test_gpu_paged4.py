@@ -257,6 +257,20 @@ def test_an_append_token_by_token_is_one_of_a_chunk(P):
     assert torch.equal(a.pages, b.pages) and a.cache.sync() == 0 and b.cache.sync() == 0
 
 
+def test_lengths_of_sequences_without_new_tokens_do_not_matter(P):
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(9, 2, D, generator=g).half().to(DEV)
+    case, other = (Case(P, torch.float16, [20, 30, 20], 16, 1, data=False, fill=0) for _ in range(2))
+    for bad in (-5, 1 << 40):
+        case.len[1] = bad
+        case.cache.append(x[:, :1], x[:, 1:], offsets_of([4, 0, 5]))
+        k, v = case.cache.read(offsets_of([4, 0, 5]), 9)
+        assert case.cache.sync() == 0
+    other.cache.append(x[:, :1], x[:, 1:], offsets_of([4, 0, 5]))
+    assert torch.equal(case.pages, other.pages)
+    assert all(torch.equal(a, b) for a, b in zip((k, v), other.cache.read(offsets_of([4, 0, 5]), 9)))
+
+
 def test_read_from_given_places(P):
     case = Case(P, torch.float16, [50, 7, 200], 32, 2)
     starts = torch.tensor([3, 0, 111], dtype=torch.int64, device=DEV)
@@ -378,6 +392,24 @@ def test_scales_that_grow_along_the_sequence(P, dt):
     case.pages.copy_(torch.from_numpy(case.host.reshape(*case.host.shape[:2], -1)))
     q = torch.randn(1, 7, D, device=DEV).to(DT[dt])
     check_attend(case, q, [1], case.cache.attend(q, offsets_of([1]), 1))
+
+
+def test_scores_far_below_zero(P):
+    """Queries of 2^120: every score of a row below -1e30, or every one above 1e30, and one key has all the weight."""
+    case = Case(P, torch.bfloat16, [60], 16, 1, seed=2, data=False, fill=0)
+    g = torch.Generator().manual_seed(8)
+    x, y = torch.rand(60, 1, D, generator=g) + 1, torch.randn(60, 1, D, generator=g)
+    case.cache.append(x.bfloat16().to(DEV), y.bfloat16().to(DEV), offsets_of([60]))
+    case.host = case.pages.cpu().numpy().reshape(case.host.shape)
+    k, v = (torch.from_numpy(a)[:, 0] for a in case.rows(0))
+    q = torch.full((1, 2, D), 2.0 ** 120, dtype=torch.bfloat16)
+    q[0, 1] *= -1
+    out = case.cache.attend(q.to(DEV), offsets_of([1]), 1).cpu().double()
+    sums = k.sum(1)
+    for h, at, other in ((0, sums.argmax(), sums.topk(2).values), (1, sums.argmin(), sums.topk(2, largest=False).values)):
+        assert (other[0] - other[1]).abs() > 2.0 ** -18 * sums.max()              # fp32's sums tell them apart
+        bar = (2.0 ** -8 + 2.0 ** -9) * torch.from_numpy(case.size_rows(0, 60))[at, 0]   # bf16's rounding, and the weight's
+        assert ((out[0, h] - v[at]).abs() <= bar).all()
 
 
 def test_softmax_scale_and_zero_queries(P):

@@ -59,7 +59,7 @@ def test_cache_init(palu):
     assert st == 0 and (c.kv_heads, c.page_size, c.batch, c.table_width, c.n_pages) == (2, 32, 3, 4, 8)
     for bad in (dict(dtype=2), dict(hk=0), dict(page=24), dict(page=256), dict(n_pages=0), dict(n_pages=1 << 31), dict(pages=0),
                 dict(pages=A + 8), dict(strides=(10240, 5128)), dict(strides=(-10240, 5120)), dict(strides=(0, 5120)),
-                dict(strides=(1 << 39, 5120)), dict(table=0), dict(table=A + 2), dict(batch=0), dict(batch=4097), dict(width=0),
+                dict(strides=(1 << 39, 5120)), dict(n_pages=(1 << 31) - 1, strides=(1 << 38, 5120)), dict(table=0), dict(table=A + 2), dict(batch=0), dict(batch=4097), dict(width=0),
                 dict(width=(1 << 25) + 1), dict(lengths=0), dict(lengths=A + 4), dict(error=0), dict(error=A + 1)):
         st, c = init(palu, **bad)
         assert st in (1, 2) and c.magic == 0 and palu.palu_last_error(), bad
@@ -171,7 +171,7 @@ def test_rope_table_refusals(palu):
     for bad in (dict(kind=-1), dict(kind=4), dict(d=0), dict(d=24), dict(d=144), dict(base=1.0), dict(base=math.nan), dict(base=math.inf),
                 dict(kind=1, factor=0.5), dict(kind=2, factor=math.nan), dict(kind=3, factor=math.inf, original=8.0),
                 dict(kind=3), dict(kind=3, original=8.0, low=-1.0), dict(kind=3, original=8.0, low=2.0, high=2.0),
-                dict(kind=3, original=8.0, high=math.inf), dict(magnitude=math.nan), dict(magnitude=math.inf), dict(start=-1),
+                dict(kind=3, original=8.0, high=math.inf), dict(magnitude=math.nan), dict(magnitude=math.inf), dict(magnitude=1e39), dict(start=-1),
                 dict(start=(1 << 40) + 1), dict(positions=-1), dict(positions=1 << 31), dict(out=0), dict(out=A + 8)):
         assert table(**bad) in (1, 2) and palu.palu_last_error(), bad
     assert table(positions=0, out=0) == 0
