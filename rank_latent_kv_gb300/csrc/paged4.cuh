@@ -36,6 +36,22 @@ __device__ __forceinline__ uint8_t* page4(const PagedView& c, int page, int head
   return reinterpret_cast<uint8_t*>(c.k) + (long long)page * c.ks0 + (long long)head * c.ks1;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
 // Queries enter fp16 products times 2^e, e such that the row's largest value
 // `big` comes to 2^13 .. 2^14 (rows of zeros or of infinities: as they are), and
 // the factor that takes the products back to log2: not 0, whatever the scale, so

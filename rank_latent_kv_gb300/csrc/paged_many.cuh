@@ -70,8 +70,10 @@ constexpr int kMany4Threads = 640;
 struct Many4Smem : ManySmem {
   uint64_t first_done[2];   // a half's product with the first 64 values of a tile
   float factor[kManyRows];  // of each row: from the products back to log2
+  alignas(16) uint8_t codes[2][kKeyTile / 16 * (kBlock4 / 2)];  // of the next tile's keys and values, each thread's own 80 bytes
 };
-constexpr int kMany4SmemBytes = 1024 + (2 + kRing) * kTileBytes + (int)sizeof(Many4Smem);
+constexpr int kRing4 = 4;  // a stage of codes takes the fifth's place
+constexpr int kMany4SmemBytes = 1024 + (2 + kRing4) * kTileBytes + (int)sizeof(Many4Smem);
 static_assert(kMany4SmemBytes + sizeof(PlanScratch) <= 232448, "shared memory of a many-rows CTA");
 
 // ---------------------------------------------------------------- tcgen05
@@ -217,7 +219,7 @@ __device__ __forceinline__ uint8_t* many_smem(uint8_t* raw) {
 }
 
 // ---------------------------------------------------------------- tiles from 4-bit codes
-// A thread's part of a 128-key tile, as it lies in the pages: one token's key
+// A thread's part of a 128-key tile, as the pages have it: one token's key
 // codes and scales; of the value codes the words of two m (of 16 channels each)
 // for four tokens, and those tokens' scales of the one group that these are in.
 struct Key4 {
@@ -228,17 +230,9 @@ struct Value4 {
   uint32_t s[2], z[2];
   int left;  // tokens that the block has
 };
-// Loaded registers pass through here where their use begins: nothing that waits for them moves in front.
-__device__ __forceinline__ void use(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
-__device__ __forceinline__ void use(Key4& k) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) use(k.codes[i]);
-  use(k.sz);
-}
-__device__ __forceinline__ void use(Value4& v) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(v.codes[i].x), "+r"(v.codes[i].y));
-  asm volatile("" : "+r"(v.s[0]), "+r"(v.s[1]), "+r"(v.z[0]), "+r"(v.z[1]));
+template <int BYTES>
+__device__ __forceinline__ void copy_own(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ uint32_t same_f16x2(uint32_t v, int high) { return __byte_perm(v, 0, high ? 0x3232 : 0x1010); }
 // z + s c of two codes that are 1024 + c, or 1024 + 16 c, in fp16
@@ -312,6 +306,7 @@ template <bool BF16, bool SPLIT, bool FOUR, class Start>
 __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet& part, const CUtensorMap* kmap, const CUtensorMap* vmap,
                                              const PlanScratch& plan, uint8_t* smem, Start&& start) {
   constexpr bool MB = BF16 && !FOUR;  // the products' type
+  constexpr int kRing = FOUR ? kRing4 : palu::kRing, kFull = 2 * kRing;
   uint8_t* ring = smem + 2 * kTileBytes;
   ManySmem& sh = *reinterpret_cast<ManySmem*>(ring + kRing * kTileBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -432,9 +427,10 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         ++u.i;
         return --u.n ? u : next_unit();
       };
-      // The thread's block of a tile is loaded one tile before it is written, and looked up another tile before that:
-      // the 16 threads of a block each for one of 16 tiles (each tile by itself: 1,000 clocks of waiting a tile).  No
-      // branch around the loads, which would wait for them: behind the last key its page is read, and not used.
+      // The thread's part of a tile is copied one tile before it is converted, into shared memory that is the thread's
+      // own (held in registers it was waited for at the loop's end, 1,000 clocks a tile), and looked up another tile
+      // before that: the 16 threads of a block each for one of 16 tiles (each tile by itself: 1,000 clocks of waiting
+      // a tile).  Behind the last key its page is read, and not used.
       int pages = 0;
       auto lookup = [&](const Tile& u) {
         if (u.i & 15) return;
@@ -450,15 +446,21 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
         }
         return page4(p.c, page, u.kh) + (place & (p.c.page - 1)) / 16 * kBlock4;
       };
-      // load(u, block), then store(tile of the ring): items `kv`, `kv` + 2, ...
-      auto run = [&](int kv, auto&& load, auto&& store) {
+      // copy(block), then take(u) and store(tile of the ring): items `kv`, `kv` + 2, ...
+      auto run = [&](int kv, auto&& copy, auto&& take, auto&& store) {
         Tile u = next_unit();
         lookup(u);
-        load(u, block_of(u));
+        copy(block_of(u));
+        cp_async_commit();
         Tile u1 = u.n ? step(u) : u;
         lookup(u1);
         for (int item = kv; u.n; item += 2) {
           const int slot = item % kRing;
+          cp_async_wait<0>();
+          take(u);
+          __syncwarp();  // taken before it is overwritten
+          copy(block_of(u1));
+          cp_async_commit();
           if (item >= kRing) wait_or_fail(&sh.kv_empty[slot], (item / kRing - 1) & 1, &sh.failed, err);
           __syncwarp();
           if (__any_sync(0xffffffffu, failed())) break;
@@ -467,46 +469,52 @@ __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet&
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.kv_full[item % kFull]);
           u = u1;
-          load(u, block_of(u));
           if (u.n) {
             u1 = step(u);
             lookup(u1);
           }
         }
+        cp_async_wait<0>();
       };
+      const uint32_t own = smem_addr(static_cast<Many4Smem&>(sh).codes[values]);
       if (!values) {
         Key4 k;
         run(
             0,
-            [&](const Tile&, const uint8_t* b) {
+            [&](const uint8_t* b) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) k.codes[i] = __ldg(reinterpret_cast<const uint4*>(b + 64 * row) + i);
-              k.sz = __ldg(reinterpret_cast<const uint4*>(b + kKeyScales4 + 16 * row));
+              for (int i = 0; i < 4; ++i) copy_own<16>(own + 2048 * i + 16 * t, b + 64 * row + 16 * i);
+              copy_own<16>(own + 8192 + 16 * t, b + kKeyScales4 + 16 * row);
             },
-            [&](uint32_t tile) {
-              use(k);
-              store_keys(tile, t, k);
-            });
+            [&](const Tile&) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) k.codes[i] = lds128(own + 2048 * i + 16 * t);
+              k.sz = lds128(own + 8192 + 16 * t);
+            },
+            [&](uint32_t tile) { store_keys(tile, t, k); });
       } else {
         Value4 v;
         run(
             1,
-            [&](const Tile& u, const uint8_t* b) {
+            [&](const uint8_t* b) {
 #pragma unroll
               for (int g = 0; g < 8; ++g)
-                v.codes[g] = __ldg(reinterpret_cast<const uint2*>(b + kValueCodes4 + 512 * half + 64 * g + 16 * c + 8 * pair));
+                copy_own<8>(own + 1024 * g + 8 * t, b + kValueCodes4 + 512 * half + 64 * g + 16 * c + 8 * pair);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)  // s and z, of e = 0 and 1
+                copy_own<4>(own + 8192 + 512 * i + 4 * t, b + kValueScales4 + 32 * c + 16 * (i >> 1) + 128 * (i & 1) + 4 * (2 * half + pair));
+            },
+            [&](const Tile& u) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g) v.codes[g] = lds64(own + 1024 * g + 8 * t);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint8_t* sz = b + kValueScales4 + 32 * c + 16 * e + 4 * (2 * half + pair);
-                v.s[e] = __ldg(reinterpret_cast<const uint32_t*>(sz));
-                v.z[e] = __ldg(reinterpret_cast<const uint32_t*>(sz + 128));
+                v.s[e] = lds32(own + 8192 + 1024 * e + 4 * t);
+                v.z[e] = lds32(own + 8192 + 1024 * e + 512 + 4 * t);
               }
               v.left = u.end - u.key0 - (t & ~15);
             },
-            [&](uint32_t tile) {
-              use(v);
-              store_values(tile, t & ~15, half, c, pair, v);
-            });
+            [&](uint32_t tile) { store_values(tile, t & ~15, half, c, pair, v); });
       }
       if (bad) atomicOr(err, bad);
     }
