@@ -294,13 +294,13 @@ __device__ __forceinline__ void store_values(uint32_t tile, int row0, int half, 
 // The CTA's stretch, by all kManyThreads (FOUR: kMany4Threads) threads;
 // `start` is run by warps 8 and up before the others may need the plan (they
 // would only wait for the same code to arrive).
-// FOUR: the pages hold 4-bit codes.  Warp 8 only plans; eight warps fetch the
-// codes into registers, a tile ahead, and write fp16 tiles into the ring.  All
+// FOUR: the pages hold 4-bit codes.  Warp 8 only plans; eight warps copy the
+// codes, a tile ahead, and write them as fp16 tiles into the ring.  All
 // products are in fp16 then, also in a bf16 cache: the queries are brought into
 // its range by a power of two a row, which comes off again with the scores'
 // factor.  A tile of 256 rows takes 4,300 clocks, the softmax's 2,800 (beside
-// converting warps on the same schedulers) and 1,300 of products; 512-token chunks
-// over 8,192 keys, 24 heads of 8: 136 us, 16 of 512 over 9,216, 28 of 4: 1,034 us,
+// converting warps on the same schedulers) and 1,300 of products; one of up to
+// 128 rows 2,300, the converting warps' time.  512-token chunks over 8,192 keys, 24 heads of 8: 136 us, 16 of 512 over 9,216, 28 of 4: 1,034 us,
 // 990 TFLOP/s.
 template <bool BF16, bool SPLIT, bool FOUR, class Start>
 __device__ __forceinline__ void many_stretch(const AttnParams& p, const PartSet& part, const CUtensorMap* kmap, const CUtensorMap* vmap,
