@@ -10,6 +10,8 @@ namespace palu {
 template <int NT>
 constexpr int kBoth4SmemBytes = kFew4SmemBytes<NT> > kMany4SmemBytes ? kFew4SmemBytes<NT> : kMany4SmemBytes;
 static_assert(kFew4Threads<1> <= kMany4Threads && kFew4Threads<2> <= kMany4Threads, "threads of paged4_both_kernel");
+static_assert(kBoth4SmemBytes<1> + sizeof(PlanScratch) <= 232448 && kBoth4SmemBytes<2> + sizeof(PlanScratch) <= 232448,
+              "shared memory of paged4_both_kernel");
 
 template <bool BF16, int NT>
 __global__ void __launch_bounds__(kMany4Threads, 1) paged4_both_kernel(const AttnParams p) {

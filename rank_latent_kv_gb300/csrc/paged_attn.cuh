@@ -210,10 +210,11 @@ enum { kToOut = -1, kToRow = -2 };
 
 // The CTA's stretch of its line, found by THREADS of its threads, tid 0 ..
 // THREADS - 1, which meet at named barrier 3.
+constexpr int kPlanWarps = 20;  // the most that plan: all of paged4_both_kernel
 struct PlanScratch {
-  long long warp_sum[16];
+  long long warp_sum[kPlanWarps];
   long long w0, w1, W, base;
-  int warp_longest[16];
+  int warp_longest[kPlanWarps];
   int cta;         // where there are two lines: its number among the CTAs of its line,
   int has_prefix;  // and whether that is the prefix units'
   int b;
@@ -242,6 +243,7 @@ __device__ __forceinline__ int split_ctas(float a, float b, int grid) {
 template <int R, int RP, int THREADS, bool FOUR = false>
 __device__ __forceinline__ void plan_start(const AttnParams& p, PlanScratch* sc, int tid) {
   constexpr int nthr = THREADS, nwarp = THREADS / 32;
+  static_assert(nwarp <= kPlanWarps, "PlanScratch has a place for each warp that plans");
   constexpr bool SPLIT = R != RP;
   const int warp = tid >> 5, lane = tid & 31;
   auto meet = [] { asm volatile("bar.sync 3, %0;" ::"n"(THREADS) : "memory"); };
