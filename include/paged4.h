@@ -108,13 +108,20 @@ palu_status palu_paged4_attn_workspace_size(const palu_paged4_cache* cache, int6
  * keys and values z + s c.  Arguments, rows without a token, shared pages,
  * refusals and repeated results as there.  Bytes behind a sequence's length do
  * not matter.
- * Up to 16 rows a KV head the codes enter the products as they are, and the
- * scales in fp32 (keys) or with the weights (values: a weight and its product
- * with the scale are each rounded to fp16, in a range that follows the scales).
+ * What is rounded follows from the rows that attend to the same keys through a
+ * KV head, by the sizes given here: for a sequence's own keys min(max_new, tokens)
+ * times q_heads / kv_heads, for shared keys that are read once those of all tokens.
+ * Up to 16 of them the codes enter the products as they are, and the scales in
+ * fp32 (keys) or with the weights (values): a weight is rounded to fp16 (those
+ * under 2^-20 of a row's largest lose bits, those under 2^-31 are lost), and so is
+ * its product with the scale, in units that follow the largest scale of each 16
+ * tokens and 32 channels (products under 2^-17 of the largest weight's with that
+ * scale lose bits, as do scales under 2^-11 of it; scales under 2^-18 have the units
+ * of 2^-18).
  * With more rows keys, values and weights are each rounded once to fp16 (weights
- * under 2^-20 of a row's largest lose bits), in bf16 caches too.  Sums, maxima
- * and accumulators are fp32; queries lose nothing but what lies 2^-24 under a
- * row's largest. */
+ * under 2^-20 of a row's largest lose bits, those under 2^-31 count only in the sum),
+ * in bf16 caches too.  Sums, maxima and accumulators are fp32; queries lose nothing
+ * but what lies 2^-24 under a row's largest. */
 palu_status palu_paged4_attn(const palu_paged4_cache* cache, int64_t tokens, const int32_t* offsets, int32_t max_new,
                              int32_t q_heads, const void* q, const int64_t q_strides[2], int32_t shared_pages,
                              float softmax_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);

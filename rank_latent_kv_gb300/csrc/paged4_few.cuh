@@ -18,9 +18,14 @@
 //   Values: a row's weights p, in fp16, are the n side of the products with the
 //   zeros and, times the tokens' scales of the group, with the codes.  p is
 //   relative to a reference that lies 2^6 under the row's maximum and is raised
-//   when a weight would pass 2^14; where a scale of 2 or more is met both bounds
-//   are lowered by its power of two, so that no p s passes 2^15.  Weights down to
-//   2^-20 of the largest keep all their bits.
+//   when a weight would pass 2^14: weights down to 2^-20 of the largest keep all
+//   their bits.  The scales enter in units of 2^E, an E for each of the four
+//   groups, which comes off again with the accumulators: the largest of a block
+//   lies in 2^-3 .. 2, so that no p s passes 2^15 and, small scales or large, the
+//   products keep all their bits down to 2^-17 of the largest weight's with the
+//   largest scale of the block.  (E stops at -15: under scales of 2^-18 the units
+//   are 2^-15.  Without units 65,536 tokens of scale 2^-14 behind a strong key were
+//   off by 2^-6; they cost 2 % of the time.)
 // A persistent CTA an SM; a loading warp copies 240 keys at a time, a page of a
 // head by one bulk copy, into a ring of stages; 15 warps take a block of 16
 // tokens of a stage each (for 9 to 16 rows, whose accumulators need the
@@ -249,6 +254,8 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
   float ref[NT][2], acc[NT][8][4], zacc[NT][4], factor[NT][2];
   uint32_t qb[NT][4][4], qz[NT][2];
   int lim[NT][2], all_see = 0;  // tokens that every row of the unit sees
+  uint32_t unit_inv[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};  // of the groups' scales: 2^-E, twice
+  auto unit_log = [&](int j) { return 127 - (int)(__float_as_uint(half2_f(unit_inv[j]).x) >> 23); };  // E
   uint32_t joins = 0;
   // the warps meet (bounded, unlike a named barrier)
   auto join = [&] {
@@ -326,10 +333,11 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
           }
         }
       }
-      // ---- the values' scales, and how far they leave room for the weights
+      // ---- the values' scales
       const uint4 sa = lds128(vs), sb = lds128(vs + 16);  // tokens 2 c, 2 c + 1; 2 c + 8, 2 c + 9
       uint32_t s2[2][4] = {{sa.x, sa.y, sa.z, sa.w}, {sb.x, sb.y, sb.z, sb.w}};
       uint32_t z2[2] = {(lds32(vs + 128 + 4 * (g & 3)) & z_keep) | z_ones, (lds32(vs + 144 + 4 * (g & 3)) & z_keep) | z_ones};
+      uint32_t bits = 0x30003000u;  // that a scale of 2^-3 .. 2 has
       if (__builtin_expect(key0 + r0 + 16 > min(all_see, key0 + valid), 0)) {
         // keys that some row does not see; what lies behind the last key must not reach the products: 0 * NaN is NaN
         const int left = valid - r0;
@@ -339,6 +347,7 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
 #pragma unroll
           for (int j = 0; j < 4; ++j) s2[i][j] &= keep;
           z2[i] &= keep;
+          if (i == 0) bits &= keep;  // asked of a half-word only while its first token is there
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -348,35 +357,58 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
             }
         }
       }
-      const uint32_t any = s2[0][0] | s2[0][1] | s2[0][2] | s2[0][3] | s2[1][0] | s2[1][1] | s2[1][2] | s2[1][3];
-      float high = kRaise4;  // the largest weight, log2
-      // a scale of 2 or more (the exponent's top bit)?
-      if (__builtin_expect(__any_sync(0xffffffffu, any & 0x40004000u), 0)) {
-        uint32_t x = 0;
+      // in units: is a scale 2 or more, or a group's larger one of two tokens under 2^-3?  (By the bits: none is negative.)
+      uint32_t su[2][4], top[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x = __vmaxu2(x, s2[i][j]);
-        x = __reduce_max_sync(0xffffffffu, max(x & 0x7fffu, x >> 16 & 0x7fffu));
-        high = kRaise4 - (float)(min((int)(x >> 10), 30) - 15);  // below 2^(exponent + 1)
+      for (int j = 0; j < 4; ++j) {
+        su[0][j] = mul_f16x2(s2[0][j], unit_inv[j]);
+        su[1][j] = mul_f16x2(s2[1][j], unit_inv[j]);
+        top[j] = __vmaxu2(su[0][j], su[1][j]);
       }
-      // ---- weights
-      uint32_t ph[NT][2];
+      const uint32_t any = top[0] | top[1] | top[2] | top[3], all = top[0] & top[1] & top[2] & top[3];
+      // ---- weights; and is one above its bound?
+      float x[NT][4], over = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = fmaf(sc[nt][e], factor[nt][e & 1], -ref[nt][e & 1]);
-        if (__builtin_expect(__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > high), 0)) {
+        for (int e = 0; e < 4; ++e) {
+          x[nt][e] = fmaf(sc[nt][e], factor[nt][e & 1], -ref[nt][e & 1]);
+          over = fmaxf(over, x[nt][e]);
+        }
+      if (__builtin_expect(__any_sync(0xffffffffu, ((any & 0x40004000u) | (~all & bits)) != 0 || over > kRaise4), 0)) {
+        // other units for a group whose largest scale of the block is not in their range
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = __vmaxu2(s2[0][j], s2[1][j]);
+          const unsigned largest = __reduce_max_sync(0xffffffffu, max(x & 0x7fffu, x >> 16 & 0x7fffu));
+          // the scale is 2^at times 1/2 .. 1
+          const int at = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)largest))) >> 23) - 126;
+          const int to = min(max(at, -15), 16), from = unit_log(j);  // (16: what is not finite leaves no trace in other units)
+          if (largest != 0 && (at > from + 1 || (at < from - 2 && to != from))) {
+            const float f = __uint_as_float((uint32_t)(127 + from - to) << 23), inv = __uint_as_float((uint32_t)(127 - to) << 23);
+            unit_inv[j] = pack_f16x2(inv, inv);
+            su[0][j] = mul_f16x2(s2[0][j], unit_inv[j]);
+            su[1][j] = mul_f16x2(s2[1][j], unit_inv[j]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                acc[nt][2 * j][e] *= f;
+                acc[nt][2 * j + 1][e] *= f;
+              }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             // the scores themselves: next to a reference that says "nothing yet" they were lost
-            x[e] = sc[nt][e] * factor[nt][e];
-            x[e + 2] = sc[nt][e + 2] * factor[nt][e];
-            float bm = fmaxf(x[e], x[e + 2]);
+            x[nt][e] = sc[nt][e] * factor[nt][e];
+            x[nt][e + 2] = sc[nt][e + 2] * factor[nt][e];
+            float bm = fmaxf(x[nt][e], x[nt][e + 2]);
 #pragma unroll
             for (int i = 4; i < 32; i <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, i));
-            const float to = bm > ref[nt][e] + high ? bm - (kLift4 - (kRaise4 - high)) : ref[nt][e], al = ex2f_(ref[nt][e] - to);
+            const float to = bm > ref[nt][e] + kRaise4 ? bm - kLift4 : ref[nt][e], al = ex2f_(ref[nt][e] - to);
             ref[nt][e] = to;
             zacc[nt][e] *= al;
 #pragma unroll
@@ -384,12 +416,15 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
               acc[nt][mt][e] *= al;
               acc[nt][mt][e + 2] *= al;
             }
-            x[e] -= to;
-            x[e + 2] -= to;
+            x[nt][e] -= to;
+            x[nt][e + 2] -= to;
           }
-        }
-        ph[nt][0] = movmatrix_t(pack_f16x2(ex2f_(x[0]), ex2f_(x[1])));
-        ph[nt][1] = movmatrix_t(pack_f16x2(ex2f_(x[2]), ex2f_(x[3])));
+      }
+      uint32_t ph[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        ph[nt][0] = movmatrix_t(pack_f16x2(ex2f_(x[nt][0]), ex2f_(x[nt][1])));
+        ph[nt][1] = movmatrix_t(pack_f16x2(ex2f_(x[nt][2]), ex2f_(x[nt][3])));
         add_f16(zacc[nt], z2[0], 0u, z2[1], 0u, ph[nt][0], ph[nt][1]);
       }
       // ---- values
@@ -400,8 +435,8 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
         uint32_t b[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          b[nt][0] = mul_f16x2(ph[nt][0], s2[0][j]);
-          b[nt][1] = mul_f16x2(ph[nt][1], s2[1][j]);
+          b[nt][0] = mul_f16x2(ph[nt][0], su[0][j]);
+          b[nt][1] = mul_f16x2(ph[nt][1], su[1][j]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -439,8 +474,9 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
           for (int e = 0; e < 2; ++e) {
             const float z = __shfl_sync(0xffffffffu, zacc[nt][e], (mt >> 1) * 4 + c);
             float* to = mw + (2 * c + e) * kMerge4Stride + 16 * mt + g;
-            to[0] = fmaf(acc[nt][mt][e], 0x1p24f, z);
-            to[8] = fmaf(acc[nt][mt][e + 2], 0x1p20f, z);
+            const float up = __uint_as_float((uint32_t)(127 + unit_log(mt >> 1)) << 23);
+            to[0] = fmaf(acc[nt][mt][e], up * 0x1p24f, z);
+            to[8] = fmaf(acc[nt][mt][e + 2], up * 0x1p20f, z);
           }
         join();
         // a warp a row, four channels a lane
