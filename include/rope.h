@@ -40,8 +40,8 @@ typedef struct {
 
 /* Row r of the table, r in 0 .. positions - 1: the cosines, then the sines, of
  * (start + r) f_i, times magnitude.  Angles are reduced in whole numbers (f_i /
- * 2 pi as a 64-bit fraction of a turn): they are off by 2^-50 of the angle and
- * 2^-63 of a turn a position at most, a value by 2^-22 of magnitude more.
+ * 2 pi as a 64-bit fraction of a turn): they are off by 2^-64 of a turn a position
+ * at most (bases up to 10^300), a value by 2^-22 of magnitude more.
  *   out    device fp32 [positions, rope_dim], contiguous, 16-byte aligned.
  *   start  0 .. 2^40.  positions 0 .. 2^31 - 1.
  * One kernel launch. */

@@ -6,7 +6,9 @@
 // fp32 has, and fp64 arithmetic is 1/60 of fp32's rate here.  So a pair's turn a
 // position, f_i / 2 pi, is a 64-bit fraction of a whole turn, and its product
 // with the position wraps around exactly: two integer additions from one row to
-// the next.  Of the fraction the nearest quarter turn is taken off, and the rest,
+// the next.  The host finds those fractions in sums of two doubles: in one double each
+// an exponent's rounding times ln base, and those of the powers, made 2^-48 of the
+// angle, 2^-8 at 2^40 positions.  Of the fraction the nearest quarter turn is taken off, and the rest,
 // at most an eighth of a turn, goes through the Taylor series of sine (to the
 // 9th power, off by 2e-9) and cosine (to the 10th, 1e-10).  131,072 positions of
 // 128: 11.1 us, 6.0 TB/s.
@@ -72,6 +74,40 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_table_kernel(con
   }
 }
 
+// A number as the unevaluated sum of two doubles, hi the nearest: 2^-104 and a
+// few roundings more an operation.
+struct Sum2 {
+  double hi, lo;
+};
+static Sum2 settle(double hi, double lo) {  // |hi| >= |lo|
+  const double s = hi + lo;
+  return {s, lo - (s - hi)};
+}
+static Sum2 add(Sum2 a, Sum2 b) {
+  const double s = a.hi + b.hi, t = s - a.hi;
+  return settle(s, (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo));
+}
+static Sum2 mul(Sum2 a, Sum2 b) {
+  const double p = a.hi * b.hi;
+  return settle(p, fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+static Sum2 div(Sum2 a, Sum2 b) {
+  const double q = a.hi / b.hi;
+  const Sum2 r = add(a, mul({-q, 0.0}, b));
+  return settle(q, r.hi / b.hi);
+}
+// x^(-1/n): pow's root and one step of Newton's method, 1 - (root^n - x) / (n x) times it.
+static Sum2 inverse_root(double x, int n) {
+  const Sum2 root = {pow(x, 1.0 / n), 0.0};
+  Sum2 power = {1.0, 0.0}, square = root;
+  for (int k = n; k; k >>= 1) {
+    if (k & 1) power = mul(power, square);
+    if (k > 1) square = mul(square, square);
+  }
+  const double off = add(power, {-x, 0.0}).hi / x / n;
+  return div({1.0, 0.0}, fabs(off) < 1.0 ? mul(root, settle(1.0, -off)) : root);  // (it may overflow next to the largest x)
+}
+
 }  // namespace palu
 
 using namespace palu;
@@ -95,21 +131,30 @@ extern "C" palu_status palu_rope_table(const palu_rope_scaling* scaling, int64_t
   if (positions == 0) return PALU_OK;
   if (!out || ((uintptr_t)out & 15)) return fail(PALU_ERR_INVALID_ARG, "out must be given, 16-byte aligned");
   RopeParams p = {};
-  const double two_pi = 6.283185307179586476925286766559;
-  const double base = s.kind == PALU_ROPE_NTK ? s.base * pow(s.factor, (double)d / (d - 2)) : s.base;
-  // base^(-2i/d) from the powers 1, 2, 4 .. 32 of its first: 64 calls of pow take longer than the launch
-  double bit[6];
-  for (int b = 0; b < 6; ++b) bit[b] = pow(base, -2.0 * (1 << b) / d);
+  const Sum2 one = {1.0, 0.0}, inv_two_pi = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};
+  // f_1, to whose powers f_i belongs; of NTK base^(-2/d) factor^(-2/(d-2))
+  Sum2 first = inverse_root(s.base, d / 2);
+  if (s.kind == PALU_ROPE_NTK) first = mul(first, inverse_root(s.factor, d / 2 - 1));
+  Sum2 f[kHeadDim / 2] = {one, first};
+  for (int i = 2; i < d / 2; ++i) f[i] = i <= 8 ? mul(f[i - 1], first) : mul(f[i - 8], f[8]);  // (chains side by side)
+  const Sum2 shrink = s.kind == PALU_ROPE_PLAIN ? one : div(one, {s.factor, 0.0});
+  const Sum2 ramp = add({s.high_turns, 0.0}, {-s.low_turns, 0.0});
   for (int i = 0; i < d / 2; ++i) {
-    double f = 1.0;
-    for (int b = 0; b < 6; ++b)
-      if (i >> b & 1) f *= bit[b];
-    if (s.kind == PALU_ROPE_LINEAR) f /= s.factor;
+    Sum2 t = mul(f[i], inv_two_pi);  // turns a position
+    if (s.kind == PALU_ROPE_LINEAR) t = mul(t, shrink);
     if (s.kind == PALU_ROPE_PARTS) {
-      const double r = s.original * f / two_pi, t = fmin(fmax((r - s.low_turns) / (s.high_turns - s.low_turns), 0.0), 1.0);
-      f *= t + (1.0 - t) / s.factor;
+      const Sum2 above = add(mul({s.original, 0.0}, t), {-s.low_turns, 0.0});
+      if (above.hi <= 0.0) {
+        t = mul(t, shrink);
+      } else if (above.hi < ramp.hi) {
+        const Sum2 part = div(above, ramp);
+        t = mul(t, add(part, mul(add(one, {-part.hi, -part.lo}), shrink)));
+      }
     }
-    p.turn[i] = (uint64_t)ldexp(f / two_pi, 64);  // f <= 1: below 2^62
+    // below 2^62, to the nearest
+    const double hi = ldexp(t.hi, 64);
+    p.turn[i] = (uint64_t)hi;
+    p.turn[i] += (int64_t)floor((hi - (double)p.turn[i]) + ldexp(t.lo, 64) + 0.5);
   }
   p.out = out;
   p.start = start;
