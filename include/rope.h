@@ -24,7 +24,11 @@ extern "C" {
  *           turn, the slowest is stretched by factor
  *   PARTS   f_i (t + (1 - t) / factor), with the turns r = original f_i / 2 pi
  *           of the pair in the context of the training and
- *           t = min(max((r - low_turns) / (high_turns - low_turns), 0), 1) */
+ *           t = min(max((r - low_turns) / (high_turns - low_turns), 0), 1).
+ *           The ramp runs over the turns, which is over original / wavelength: a
+ *           model that states it so, without a magnitude, is this kind with magnitude
+ *           1 (low_turns 1 and high_turns 4, say).  A ramp that runs over the pair's
+ *           number i, and frequencies given one by one, are none of these. */
 enum { PALU_ROPE_PLAIN = 0, PALU_ROPE_LINEAR = 1, PALU_ROPE_NTK = 2, PALU_ROPE_PARTS = 3 };
 
 typedef struct {

@@ -25,16 +25,16 @@
 //   products keep all their bits down to 2^-17 of the largest weight's with the
 //   largest scale of the block.  (E stops at -15: under scales of 2^-18 the units
 //   are 2^-15.  Without units 65,536 tokens of scale 2^-14 behind a strong key were
-//   off by 2^-6; they cost 2 % of the time.)
+//   off by 2^-6.  They cost 2 to 3 % of the time, one E for all groups 1 to 2 %.)
 // A persistent CTA an SM; a loading warp copies 240 keys at a time, a page of a
 // head by one bulk copy, into a ring of stages; 15 warps take a block of 16
 // tokens of a stage each (for 9 to 16 rows, whose accumulators need the
-// registers, 8 warps two blocks of 256 keys each: 87 us where 8 rows take 53).
+// registers, 8 warps two blocks of 256 keys each: 88 us where 8 rows take 54).
 //
-// 16 sequences of up to 32,768 tokens, 28 heads of 4: 257 MB in 52.7 us, 9 of them
-// fixed, then 5.8 TB/s; 64 of up to 8,191 with 16 heads of 16: 1,012 MB in 174 us.
+// 16 sequences of up to 32,768 tokens, 28 heads of 4: 257 MB in 53.8 us, 9 of them
+// fixed, then 5.7 TB/s; 64 of up to 8,191 with 16 heads of 16: 1,012 MB in 182 us.
 // The copies alone take 48.7 and 161: instructions and memory bound it together
-// (300 warp instructions a block, 47 % of the issue slots).
+// (310 warp instructions a block, 50 % of the issue slots).
 #pragma once
 
 #include <math.h>

@@ -99,7 +99,9 @@ struct LineCost<kManyRows, false> {
   static constexpr float kClocks = 200.f;
 };
 // Made from codes: of up to 128 rows a tile takes 2,300 clocks and a unit 17,000 more (with 60 and 14 here 77 sequences
-// of 5 tokens behind up to 1,500 keys, 28 heads of 4, took 67 us instead of 63).
+// of 5 tokens behind up to 1,500 keys, 28 heads of 4, took 67 us instead of 63).  Equal units, 1 to 6 a CTA of 1 to 32
+// tiles, fitted: 35 to 128 rows 11,000 to 15,000 clocks a unit and 3,100 a tile, 140 and 256 rows 21,000 to 26,000 and
+// 5,300 (a unit as 4.0 to 4.8 tiles; 100 / 22 is 4.5).
 template <>
 struct LineCost<kManyRows, true> {
   static __device__ int unit(int rows) { return rows > kManyRows / 2 ? 100 : 85; }
@@ -107,7 +109,8 @@ struct LineCost<kManyRows, true> {
   static constexpr int kMaxTile = 22;
   static constexpr float kClocks = 200.f;
 };
-// A tile of codes is 20 KB.
+// A tile of codes is 20 KB.  Equal units as above: up to 8 rows 7,100 clocks a unit and 1,020 a tile, up to 16 rows
+// 11,800 and 1,790 (a unit as 6.9 and 6.6 tiles).
 template <int R>
 struct LineCost<R, true> {
   static __device__ int unit(int rows) { return 6; }

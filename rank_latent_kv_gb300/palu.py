@@ -872,7 +872,7 @@ def rope_table(positions, rope_dim, base=10000.0, scaling="plain", factor=1.0, o
     """The rotation table of positions start .. start + positions - 1 (include/rope.h): fp32 [positions, rope_dim], cosines
     then sines, as qk_norm_rope and the caches' append take it.  scaling: "plain", "linear", "ntk" or "parts" (`original`
     tokens of the training's context, low_turns, high_turns).  magnitude multiplies the table: by default
-    0.1 ln(factor) + 1 for "parts", else 1."""
+    0.1 ln(factor) + 1 for "parts", else 1; for a model that scales by parts without one it has to be given as 1."""
     if scaling not in PALU_ROPE_KINDS:
         raise ValueError(f"scaling is {scaling!r}; expected one of {', '.join(PALU_ROPE_KINDS)}")
     if magnitude is None:
