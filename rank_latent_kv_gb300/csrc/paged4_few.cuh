@@ -29,7 +29,7 @@
 // A persistent CTA an SM; a loading warp copies 240 keys at a time, a page of a
 // head by one bulk copy, into a ring of stages; 15 warps take a block of 16
 // tokens of a stage each (for 9 to 16 rows, whose accumulators need the
-// registers, 8 warps two blocks of 256 keys each: 88 us where 8 rows take 54).
+// registers, 8 warps two blocks of 256 keys each: 87 us where 8 rows take 54).
 //
 // 16 sequences of up to 32,768 tokens, 28 heads of 4: 257 MB in 53.8 us, 9 of them
 // fixed, then 5.7 TB/s; 64 of up to 8,191 with 16 heads of 16: 1,012 MB in 182 us.
@@ -254,7 +254,7 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
   float ref[NT][2], acc[NT][8][4], zacc[NT][4], factor[NT][2];
   uint32_t qb[NT][4][4], qz[NT][2];
   int lim[NT][2], all_see = 0;  // tokens that every row of the unit sees
-  uint32_t unit_inv[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};  // of the groups' scales: 2^-E, twice
+  uint32_t unit_inv[4];  // of the groups' scales: 2^-E, twice
   auto unit_log = [&](int j) { return 127 - (int)(__float_as_uint(half2_f(unit_inv[j]).x) >> 23); };  // E
   uint32_t joins = 0;
   // the warps meet (bounded, unlike a named barrier)
@@ -280,6 +280,8 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
       const UnitMeta m = sh.meta[st].u;
       if (lane == 0) sh.unit[warp] = m;
       all_see = 0x7fffffff;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unit_inv[j] = 0x3c003c00u;  // anew, so that no unit's result depends on another's scales
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int rg = nt * 8 + g;
@@ -383,7 +385,7 @@ __device__ __forceinline__ void few4_work(const AttnParams& p, const PartSet& pa
           const unsigned largest = __reduce_max_sync(0xffffffffu, max(x & 0x7fffu, x >> 16 & 0x7fffu));
           // the scale is 2^at times 1/2 .. 1
           const int at = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)largest))) >> 23) - 126;
-          const int to = min(max(at, -15), 16), from = unit_log(j);  // (16: what is not finite leaves no trace in other units)
+          const int to = min(max(at, -15), 16), from = unit_log(j);  // (at most 16, whatever is not finite)
           if (largest != 0 && (at > from + 1 || (at < from - 2 && to != from))) {
             const float f = __uint_as_float((uint32_t)(127 + from - to) << 23), inv = __uint_as_float((uint32_t)(127 - to) << 23);
             unit_inv[j] = pack_f16x2(inv, inv);

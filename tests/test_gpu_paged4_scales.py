@@ -137,3 +137,27 @@ def test_what_is_not_finite_stays_in_its_sequence(P, Hq, fill):
         one = P.PagedCache4(pages, table[b:b + 1].contiguous(), cache.lengths[:1], page, torch.float16)
         check(one, q[b], out[b], length)
     assert cache.sync() == 0
+
+
+@pytest.mark.parametrize("Hq", [3, 12, 24])
+def test_a_result_does_not_depend_on_what_others_hold(P, Hq):
+    """Bit for bit, whatever scales the sequences have that a CTA takes before: each warp meets a strong key and then
+    weak ones of 1.34 2^-19, whose products would round otherwise in other units, a few of the outputs with them."""
+    B, length, page = 304, 4096, 128
+    g = torch.Generator(device=DEV).manual_seed(11)
+    width = -(-length // page)
+    table = torch.randperm(B * width, generator=g, device=DEV).int().view(B, width)
+    k = torch.zeros(B, length, 1, D, device=DEV)
+    k[:, 0:256:16] = (19 - math.log2(1.34)) * math.log(2) * D ** -0.5
+    v = values_of(codes_like(B * length, 1, g), torch.full((B * length, 1, 4), 2.0 ** -3, device=DEV)).half().view(B, length, 1, D)
+    q = (1 + torch.arange(Hq, device=DEV)[:, None] * 2.0 ** -9).expand(B, Hq, D).half()
+    outs = []
+    for size in (1.0, 2.0 ** -3, 2.0 ** 9):
+        mixed = v.clone()
+        mixed[::2] *= size
+        pages = torch.zeros(B * width, 1, page * 160, dtype=torch.uint8, device=DEV)
+        cache = P.PagedCache4(pages, table, torch.full((B,), length, device=DEV), page, torch.float16)
+        cache.append(k.half().view(-1, 1, D), mixed.view(-1, 1, D), offsets_of([length] * B))
+        outs.append(cache.attend(q, offsets_of([1] * B), 1)[1::2])
+        assert cache.sync() == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
