@@ -35,3 +35,54 @@ def test_hundreds_of_sequences_behind_a_prefix(P, dt, B, Hq, Hk, page, shared, o
         for _ in range(10):
             assert torch.equal(out, cache.attend(q, off, new, shared_pages=shared))
     assert cache.sync() == 0
+
+
+@pytest.mark.parametrize("Hq,Hk,new", [(24, 8, 1), (16, 2, 2)])
+def test_a_captured_call_follows_the_lengths(P, Hq, Hk, new):
+    """One graph, replayed as own tokens come and go: the division of the CTAs between prefix and own keys is the device's."""
+    B, page, shared, own = 96, 64, 48, 700
+    prefix = shared * page
+    cache = filled(P, torch.float16, B, Hk, page, prefix + own, shared=shared, seed=4)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    q = torch.randn(B * new, Hq, D, generator=g, device=DEV).half()
+    off, ws, out = offsets_of([new] * B), cache.attend_workspace(B * new, Hq, new, shared), torch.zeros_like(q)
+
+    def call():
+        cache.attend(q, off, new, shared_pages=shared, workspace=ws, out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lengths in ([prefix + own] * B, [prefix] * B, [prefix // 2 + i for i in range(B)], [prefix + own if i == 7 else 1 + i for i in range(B)],
+                    [0] * (B - 1) + [prefix + 5], [prefix + 1 + 7 * i for i in range(B)]):
+        lengths = [n if n == 0 else max(n, new) for n in lengths]
+        cache.lengths.copy_(torch.tensor(lengths))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(cache, q, [new] * B, out, lengths, only=(0, 7, 40, B - 1))
+        for b in range(B):
+            if lengths[b] == 0:
+                assert bool((out[b * new:(b + 1) * new] == 0).all())
+    assert cache.sync() == 0
+
+
+def test_two_streams_behind_one_prefix(P):
+    B, Hq, Hk, page, shared, own = 64, 24, 8, 32, 128, 300
+    cache = filled(P, torch.bfloat16, B, Hk, page, shared * page + own, shared=shared, seed=8)
+    qs = [torch.randn(B, Hq, D, device=DEV).bfloat16() for _ in range(2)]
+    off = offsets_of([1] * B)
+    want = [cache.attend(q, off, 1, shared_pages=shared) for q in qs]
+    ws = [cache.attend_workspace(B, Hq, 1, shared) for _ in range(2)]
+    outs = [torch.empty_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, w, o, s in zip(qs, ws, outs, streams):
+            cache.attend(q, off, 1, shared_pages=shared, workspace=w, out=o, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert cache.sync() == 0
